@@ -337,6 +337,122 @@ int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* d
                         float* dG_R, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * 4-bit base weight with group scales (POET-X technical summary section 2.6, POET-XQ: a
+ * low-bit base weight, dequantised on the fly where it is needed).  The pages give no scheme;
+ * here one bf16 scale per group of `group` (32, 64 or 128) consecutive columns of a row of W0':
+ *   a = max |w| of the group;  s = a / 7 (fp32, IEEE division) rounded to 5 significant bits,
+ *   nearest even;  q = the integer nearest to w / s (ties to even; decided exactly), clamped to
+ *   [-7, 7].  An all-zero group: scale 0, codes 0.  A group holding an infinity or a NaN: scale
+ *   NaN, codes 0, so it reads back as NaN.
+ * With 5 bits in the scale, s q is exactly a bf16 number: nothing in the library rounds the
+ * dequantised weight, and the few-token and the tensor-core products use the same weight.
+ * Other bf16 scales (written by the caller) are accepted: s q is then rounded to bf16, except
+ * in the forward few-token products, which scale fp32 sums.
+ *
+ * Layout (n % 128 == 0, any m): blocks of 128 columns, each with every row's part side by side:
+ *   q       uint8 [n/128, m, 64]: a row's 64 bytes of a block are four 16-byte chunks t of four
+ *           little-endian 32-bit words w; word (t, w) holds columns 32 w + 8 t + e (e < 8) of
+ *           the block, column e as q + 8 in bits [4 p, 4 p + 4), p = e / 2 + 4 (e % 2).
+ *   scales  bf16 [n/128, m, 128/group].
+ *
+ * poetx_quantize_q4: codes and scales of W.  poetx_merge_perm_q4: of W0' = W0[perm_R][:,
+ * perm_P], straight from W0 (permutation reduction, section 2.2, without forming W0'); NULL for
+ * both maps: identity.  poetx_dequantize_q4: out[i, j] = s q, row-major [m, n].
+ *   W, W0, out device [m, n] (dtype POETX_BF16 or POETX_F32).  perm_R, perm_P device int32 [m],
+ *   [n].  Rows up to 200 KB (n * element size) in the first two.
+ *   Errors: INVALID_ARG, SHAPE, DTYPE, ALIGN, CUDA.
+ */
+int poetx_quantize_q4(const void* W, uint8_t* q, void* scales, int32_t m, int32_t n, int32_t group,
+                      int dtype, void* stream);
+int poetx_merge_perm_q4(const void* W0, uint8_t* W0q, void* scales, int32_t m, int32_t n,
+                        const int32_t* perm_R, const int32_t* perm_P, int32_t group, int dtype,
+                        void* stream);
+int poetx_dequantize_q4(const uint8_t* q, const void* scales, void* out, int32_t m, int32_t n,
+                        int32_t group, int dtype, void* stream);
+
+/*
+ * Products with the 4-bit weight W [m, n] (the W0' products of the input-centric layer,
+ * section 2.1, on the base weight of section 2.6), from one token up:
+ *   transpose = 0:  y[T, m] = x[T, n] W^T      (forward; a matrix-vector product at T = 1)
+ *   transpose = 1:  y[T, n] = x[T, m] W        (the gradient that passes through the weight)
+ *   x, y device bf16 row-major, distinct; fp32 sums, one rounding.  T = 0 is a no-op.
+ * Few tokens: each code is read once and multiplied from registers; the sums of split rows or
+ * columns are added in a fixed order.
+ *   Errors: INVALID_ARG, SHAPE, ALIGN, CUDA.
+ */
+int poetx_matmul_q4(const void* x, const uint8_t* W0q, const void* scales, void* y, int32_t T,
+                    int32_t m, int32_t n, int32_t group, int transpose, void* stream);
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored (POET-X section 2.5 trades
+ * recomputation for memory in the same way; the pages have no dropout).  Value (row t, column
+ * c) of a [rows, cols] matrix is kept when a 16-bit draw is >= thr = round(65536 p), and then
+ * multiplied by 65536 / (65536 - thr) (fp32 product, one rounding); else it becomes 0, whatever
+ * it was.  The draw is lane c % 8 (word lane / 2, low half first) of Philox4x32-10 (Salmon et
+ * al. 2011) with key (seed low, seed high) and counter (c / 8, row0 + t, site, step).  So the
+ * mask depends on nothing but these numbers: the backward, a recomputation and a shard of the
+ * rows (row0 = its first row) see the same one.
+ */
+typedef struct poetx_dropout_desc {
+  double p;             /* probability of dropping, in [0, 65535/65536] (multiples of 2^-16) */
+  uint64_t seed;
+  uint32_t site;        /* which of a program's dropouts this is */
+  uint32_t row0;        /* number of the first row (row0 + rows <= 2^32) */
+  const uint64_t* step; /* device counter of steps, read by the kernels when they run (its low
+                           32 bits; 8-byte aligned), so that a replayed CUDA graph draws new
+                           masks when the caller advances it; NULL: step 0 */
+} poetx_dropout_desc;
+
+/*
+ * poetx_dropout: out = dropout(in); in == out is allowed.  The backward is the same call on the
+ * gradient.
+ * poetx_permute_cols_dropout: fused with an index map of the columns (section 2.2):
+ *   mask_output = 0:  out[t, i] = dropout(in)[t, idx[i]]      (mask by the source column)
+ *   mask_output = 1:  out[t, i] = mask(t, i) in[t, idx[i]]    (mask by the output column): with
+ *   the inverse map, the gradient of the first form.
+ *   in, out device [rows, cols] (dtype), distinct in the second call.  idx device int32 [cols].
+ *   Errors: INVALID_ARG, DTYPE, ALIGN, CUDA.
+ */
+int poetx_dropout(const poetx_dropout_desc* drop, const void* in, void* out, int32_t rows,
+                  int32_t cols, int dtype, void* stream);
+int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, void* out,
+                               const int32_t* idx, int32_t rows, int32_t cols, int mask_output,
+                               int dtype, void* stream);
+
+/*
+ * The layer on any form of the merged weight, with dropout of its input (drop, or NULL for
+ * none): y = layer(dropout(x)); dx is the gradient in x, through the mask.  save_u receives
+ * dropout(x)[:, p_P]; a recomputing backward (NULL save buffers) draws the same mask, so the
+ * step counter must not move between a forward and its backward.
+ *   POETX_WEIGHT_DENSE  w = W0' [m, n] (dtype); scales, group unused
+ *   POETX_WEIGHT_Q8     w = int8 codes, scales fp32 [m] (poetx_merge_perm_q8)
+ *   POETX_WEIGHT_Q4     w = 4-bit codes, scales bf16, group (poetx_merge_perm_q4); bf16 layer.
+ *                       Up to 64 tokens without dropout the forward runs as three launches:
+ *                       gather + block product, weight product, block product + scatter.
+ * Without dropout the first two give the results of poetx_linear_{fwd,bwd}{,_q8} bit for bit.
+ * ws: at least poetx_linear_ex_workspace bytes (enough for either direction).  Other arguments
+ * and errors as poetx_linear_fwd / poetx_linear_bwd.
+ */
+enum { POETX_WEIGHT_DENSE = 0, POETX_WEIGHT_Q8 = 1, POETX_WEIGHT_Q4 = 2 };
+typedef struct poetx_linear_weight {
+  int32_t kind;  /* POETX_WEIGHT_* */
+  int32_t group; /* POETX_WEIGHT_Q4 */
+  const void* w;
+  const void* scales;
+} poetx_linear_weight;
+size_t poetx_linear_ex_workspace(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                                 int has_save_u, int has_save_w);
+int poetx_linear_fwd_ex(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                        const poetx_dropout_desc* drop, const void* x, const void* G_P,
+                        const void* G_R, void* y, void* save_u, void* save_w, void* ws,
+                        size_t ws_bytes, void* stream);
+int poetx_linear_bwd_ex(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                        const poetx_dropout_desc* drop, const void* x, const void* dy,
+                        const void* G_P, const void* G_R, const void* save_u, const void* save_w,
+                        void* dx, float* dG_P, float* dG_R, int accumulate, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
  * Time limit of every bounded wait in the library's kernels (mbarrier waits of the tensor-core
  * GEMM, dependency waits of the CNP task graph), in nanoseconds; 0 restores the default of
  * 2 s.  Kernels read the limit when they are launched (a CUDA graph keeps the value it was

@@ -242,6 +242,91 @@ def dequantize_rows(q, s) -> np.ndarray:
     return np.asarray(s, dtype=np.float64)[:, None] * np.asarray(q, dtype=np.float64)
 
 
+def quantize_groups_q4(W, group: int):
+    """4-bit base weight with group scales: per group of `group` consecutive columns of a row,
+    s = max|w| / 7 (fp32, IEEE division) rounded to 5 significant bits (nearest even),
+    q = the integer nearest to w / s (ties to even) clamped to [-7, 7]; an all-zero group has
+    s = 0 and q = 0, a group with an infinity or a NaN s = NaN and q = 0.  The quotient of a
+    24-bit and a 5-bit number is never closer than 2^-30 to a half without being one, so the
+    float64 division decides it exactly.  Returns (q int8 [m, n], s float32 [m, n/group])."""
+    W32 = np.asarray(W, dtype=np.float32)
+    m, n = W32.shape
+    Wg = W32.reshape(m, n // group, group)
+    amax = np.abs(Wg).max(axis=2).astype(np.float32)
+    finite = np.isfinite(Wg).all(axis=2)
+    a7 = (np.where(finite, amax, 0).astype(np.float32) / np.float32(7.0)).astype(np.float32)
+    bits = a7.view(np.uint32).astype(np.uint64)
+    low = bits & 0x7FFFF                       # 19 bits below the 5 that stay
+    up = (low > 0x40000) | ((low == 0x40000) & ((bits >> 19) & 1 == 1))
+    bits = (bits - low + np.where(up, 0x80000, 0)).astype(np.uint32)
+    s = bits.view(np.float32).copy()
+    safe = np.where(s > 0, s, 1.0).astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        q = np.clip(np.rint(Wg.astype(np.float64) / safe[:, :, None]), -7, 7)
+    q[~((s > 0) & finite)] = 0
+    s[~finite] = np.nan
+    return q.reshape(m, n).astype(np.int8), s
+
+
+def dequantize_groups(q, s) -> np.ndarray:
+    """W = s[i, j // group] q[i, j] (float64)."""
+    q, s = np.asarray(q, dtype=np.float64), np.asarray(s, dtype=np.float64)
+    return q * np.repeat(s, q.shape[1] // s.shape[1], axis=1)
+
+
+def pack_q4(q):
+    """uint8 [n/128, m, 64]: column 128 k + 32 w + 8 t + e of row i as q + 8 in bits
+    [4 p, 4 p + 4), p = e // 2 + 4 (e % 2), of little-endian word 4 t + w of row i of block k."""
+    q = np.asarray(q)
+    m, n = q.shape
+    words = np.zeros((n // 128, m, 16), dtype=np.uint32)
+    for w in range(4):
+        for t in range(4):
+            for e in range(8):
+                col = q[:, 32 * w + 8 * t + e::128].T.astype(np.int64) + 8
+                words[:, :, 4 * t + w] |= (col << (4 * (e // 2 + 4 * (e % 2)))).astype(np.uint32)
+    return words.astype("<u4").view(np.uint8).reshape(n // 128, m, 64)
+
+
+def pack_scales(s, group: int):
+    """[n/128, m, 128/group] from [m, n/group]."""
+    m = s.shape[0]
+    return np.ascontiguousarray(s.reshape(m, -1, 128 // group).transpose(1, 0, 2))
+
+
+def philox4x32_10(ctr, key):
+    """Ten rounds of Philox4x32 (Salmon, Moraes, Dror, Shaw, SC 2011) in Python integers."""
+    c, k, M = list(ctr), list(key), 0xFFFFFFFF
+    for _ in range(10):
+        p0, p1 = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [(p1 >> 32) ^ c[1] ^ k[0], p1 & M, (p0 >> 32) ^ c[3] ^ k[1], p0 & M]
+        k = [(k[0] + 0x9E3779B9) & M, (k[1] + 0xBB67AE85) & M]
+    return c
+
+
+def dropout_factor(rows: int, cols: int, p: float, seed: int, site: int = 0, row0: int = 0,
+                   step: int = 0) -> np.ndarray:
+    """What dropout multiplies a [rows, cols] matrix by (float64, 0 or 65536/(65536 - thr)):
+    value (t, c) is kept when the 16 bits of lane c % 8 of the generator at counter
+    (c // 8, row0 + t, site, step) are >= thr = round(65536 p).  Vectorised philox4x32_10."""
+    thr = int(np.floor(p * 65536 + 0.5))
+    calls = -(-cols // 8)
+    shape = (rows, calls)
+    u = np.uint64
+    c = [np.broadcast_to(np.arange(calls, dtype=u), shape),
+         np.broadcast_to((np.arange(rows, dtype=u) + u(row0))[:, None], shape),
+         np.full(shape, site, u), np.full(shape, step & 0xFFFFFFFF, u)]
+    k = [seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF]
+    m32 = u(0xFFFFFFFF)
+    for _ in range(10):
+        p0, p1 = c[0] * u(0xD2511F53), c[2] * u(0xCD9E8D57)
+        c = [(p1 >> u(32)) ^ c[1] ^ u(k[0]), p1 & m32, (p0 >> u(32)) ^ c[3] ^ u(k[1]), p0 & m32]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    draws = np.stack([h for w in c for h in (w & u(0xFFFF), w >> u(16))], axis=2)
+    keep = draws.reshape(rows, calls * 8)[:, :cols] >= u(thr)
+    return np.where(keep, 65536.0 / (65536 - thr), 0.0)
+
+
 def layer_dense(x, W0, G_P, G_R, perm_P, perm_R) -> np.ndarray:
     """Rows of Y = (R W0 P x_t)^T with the four permutations as matrices and the unmerged
     W0 (the weight-centric reading; small sizes only)."""

@@ -11,8 +11,14 @@
 // elements (the bf16 layer) k_gather_il8 interleaves 8 rows per shared-memory word so
 // that one access serves a column of 8 rows (rows narrower than 2048); the row-staged
 // kernels cover fp32 and wider rows.
+//
+// DROP fuses dropout of the layer's input with the map (philox_dev.cuh; no extra pass and no
+// stored mask): kDropSource masks by the source column while the row is staged (forward, U =
+// dropout(X)[:, p_P]), kDropOutput by the output column as it is written (backward, the same
+// mask on dX).  Both count columns in X's own order, so the two directions share one mask.
 #include <cuda_bf16.h>
 
+#include "philox_dev.cuh"
 #include "poetx_internal.h"
 
 namespace poetx {
@@ -20,6 +26,7 @@ namespace {
 
 constexpr int kGatherThreads = 128;
 constexpr int kMaxSmemRowBytes = 200 * 1024;
+enum { kDropNone = 0, kDropSource = 1, kDropOutput = 2 };
 
 __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
   uint4 v;
@@ -29,11 +36,12 @@ __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
   return v;
 }
 
-template <typename E>
+template <typename E, int DROP>
 __global__ void __launch_bounds__(kGatherThreads)
     k_gather_rows_smem(const E* __restrict__ in, E* __restrict__ out,
                        const int32_t* __restrict__ row_idx, const int32_t* __restrict__ col_idx,
-                       int rows, int cols, int64_t ld_in, int64_t ld_out) {
+                       int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs drop) {
+  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   E* srow = reinterpret_cast<E*>(smem_raw);
   constexpr int V = 16 / sizeof(E);  // elements per 16-byte vector
@@ -43,7 +51,15 @@ __global__ void __launch_bounds__(kGatherThreads)
     sr = min(max(sr, 0), rows - 1);  // keep the read inside the matrix
     const E* src = in + (int64_t)sr * ld_in;
     const bool vin = (cols % V == 0) && ((reinterpret_cast<uintptr_t>(src) & 15) == 0);
-    if (vin) {
+    if (DROP == kDropSource) {  // a thread per mask call, 8 columns
+      for (int c8 = threadIdx.x; c8 < (cols + 7) / 8; c8 += blockDim.x) {
+        const uint32_t keep = drop_bits(drop, drop_words(drop, dstep, (uint32_t)r, c8));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (8 * c8 + e < cols)
+            srow[8 * c8 + e] = drop_one<E>(drop, (keep >> e) & 1u, src[8 * c8 + e]);
+      }
+    } else if (vin) {
       const uint4* s4 = reinterpret_cast<const uint4*>(src);
       uint4* d4 = reinterpret_cast<uint4*>(srow);
       for (int i = threadIdx.x; i < cols / V; i += blockDim.x) d4[i] = ldg_stream(s4 + i);
@@ -53,7 +69,18 @@ __global__ void __launch_bounds__(kGatherThreads)
     __syncthreads();
     E* dst = out + (int64_t)r * ld_out;
     const bool vout = (cols % V == 0) && ((reinterpret_cast<uintptr_t>(dst) & 15) == 0);
-    if (vout) {
+    if (DROP == kDropOutput) {
+      for (int c8 = threadIdx.x; c8 < (cols + 7) / 8; c8 += blockDim.x) {
+        const uint32_t keep = drop_bits(drop, drop_words(drop, dstep, (uint32_t)r, c8));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = 8 * c8 + e;
+          if (c >= cols) break;
+          unsigned ci = (unsigned)__ldg(col_idx + c);
+          dst[c] = drop_one<E>(drop, (keep >> e) & 1u, srow[ci < ucols ? ci : ucols - 1]);
+        }
+      }
+    } else if (vout) {
       for (int c0 = threadIdx.x * V; c0 < cols; c0 += blockDim.x * V) {
         E v[V];
 #pragma unroll
@@ -94,11 +121,13 @@ __device__ __forceinline__ void cp_async_wait() {
 
 constexpr int kPipeThreads = 256;
 
-template <typename E, int MAXV>
+template <typename E, int MAXV, int DROP>
 __global__ void __launch_bounds__(kPipeThreads)
     k_gather_rows_pipe(const E* __restrict__ in, E* __restrict__ out,
                        const int32_t* __restrict__ row_idx, const int32_t* __restrict__ col_idx,
-                       int rows, int cols, int64_t ld_in, int64_t ld_out, int R) {
+                       int rows, int cols, int64_t ld_in, int64_t ld_out, int R,
+                       const DropArgs drop) {
+  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   constexpr int V = 16 / sizeof(E);
   const int nvec = cols / V;                    // 16-byte vectors per row
@@ -157,10 +186,23 @@ __global__ void __launch_bounds__(kPipeThreads)
     if (next < nbatch) issue(next, buf[(it + 1) & 1]);
     cp_async_commit();
     cp_async_wait1();
-    __syncthreads();
-    const E* src = buf[it & 1];
     const int r0 = batch * R;
     const int nr = min(R, rows - r0);
+    if (DROP == kDropSource) {  // in place, each thread on the vectors it copied itself
+      E* b = buf[it & 1];
+      for (int rr = rr_first, vv = vv_first; rr < nr;) {
+        uint4* p = reinterpret_cast<uint4*>(b + (size_t)rr * row_elems + vv * V);
+        *p = drop_vec<sizeof(E)>(drop, dstep, (uint32_t)(r0 + rr), (uint32_t)(vv * V), *p);
+        rr += rr_step;
+        vv += vv_step;
+        if (vv >= nvec) {
+          vv -= nvec;
+          ++rr;
+        }
+      }
+    }
+    __syncthreads();
+    const E* src = buf[it & 1];
     for (int rr = 0; rr < nr; ++rr) {
       const E* srow = src + (size_t)rr * row_elems;
       E* drow = out + (int64_t)(r0 + rr) * ld_out;
@@ -173,8 +215,11 @@ __global__ void __launch_bounds__(kPipeThreads)
             v[e] = srow[idx[j][e / 2] & 0xFFFFu];
             v[e + 1] = srow[idx[j][e / 2] >> 16];
           }
-          *reinterpret_cast<uint4*>(drow + (threadIdx.x + j * kPipeThreads) * V) =
-              *reinterpret_cast<const uint4*>(v);
+          uint4 o = *reinterpret_cast<const uint4*>(v);
+          if (DROP == kDropOutput)
+            o = drop_vec<sizeof(E)>(drop, dstep, (uint32_t)(r0 + rr),
+                                    (uint32_t)((threadIdx.x + j * kPipeThreads) * V), o);
+          *reinterpret_cast<uint4*>(drow + (threadIdx.x + j * kPipeThreads) * V) = o;
         }
       }
     }
@@ -201,11 +246,11 @@ __device__ __forceinline__ uint32_t u4_word(const uint4& v, int w) {
   return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
 }
 
-template <int MAXC, int NS>
+template <int MAXC, int NS, int DROP>
 __global__ void __launch_bounds__(kIlThreads, 1)
     k_gather_il8(const uint16_t* __restrict__ in, uint16_t* __restrict__ out,
                  const int32_t* __restrict__ row_idx, const int32_t* __restrict__ col_idx,
-                 int rows, int cols, int64_t ld_in, int64_t ld_out) {
+                 int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs drop) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   // [NS stages of 8 rows x cols] [interleaved words: cols x 16 bytes]
   uint16_t* const stage0 = reinterpret_cast<uint16_t*>(smem_raw);
@@ -213,6 +258,7 @@ __global__ void __launch_bounds__(kIlThreads, 1)
   const int nchunk = cols / 8;
   pdl_trigger();
   pdl_wait();
+  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
   const unsigned ucols = (unsigned)cols;
   // slots of the source columns of the output chunks this thread owns (2 x 16 bit a word)
   uint32_t src[MAXC][4];
@@ -268,6 +314,11 @@ __global__ void __launch_bounds__(kIlThreads, 1)
       uint4 ld[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) ld[r] = *reinterpret_cast<const uint4*>(sg + (size_t)r * cols + 8 * q);
+      if (DROP == kDropSource) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          ld[r] = drop_bf16x8(drop, ld[r], drop_words(drop, dstep, (uint32_t)(g * 8 + r), q));
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int w = c >> 1;
@@ -299,6 +350,8 @@ __global__ void __launch_bounds__(kIlThreads, 1)
         o.y = __byte_perm(u4_word(col[2], w), u4_word(col[3], w), sel);
         o.z = __byte_perm(u4_word(col[4], w), u4_word(col[5], w), sel);
         o.w = __byte_perm(u4_word(col[6], w), u4_word(col[7], w), sel);
+        if (DROP == kDropOutput)
+          o = drop_bf16x8(drop, o, drop_words(drop, dstep, (uint32_t)row, q));
         *reinterpret_cast<uint4*>(out + (int64_t)row * ld_out + 8 * q) = o;
       }
     }
@@ -306,16 +359,17 @@ __global__ void __launch_bounds__(kIlThreads, 1)
   cp_async_wait<0>();
 }
 
-template <int MAXC, int NS>
+template <int MAXC, int NS, int DROP>
 cudaError_t il8_launch(const void* in, void* out, const int32_t* row_idx, const int32_t* col_idx,
-                       int rows, int cols, int64_t ld_in, int64_t ld_out, cudaStream_t s) {
+                       int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs& drop,
+                       cudaStream_t s) {
   const size_t smem = il_smem(NS, cols);
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(k_gather_il8<MAXC, NS>,
+    cudaError_t e = cudaFuncSetAttribute(k_gather_il8<MAXC, NS, DROP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kIlMaxSmem);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
@@ -326,21 +380,23 @@ cudaError_t il8_launch(const void* in, void* out, const int32_t* row_idx, const 
   int grid = num_sms() * per_sm;
   if (grid > ngroups) grid = ngroups;
   begin_launch("permute", s);
-  const cudaError_t e = launch_pdl(k_gather_il8<MAXC, NS>, dim3(grid), dim3(kIlThreads), smem, s,
-                                   static_cast<const uint16_t*>(in), static_cast<uint16_t*>(out),
-                                   row_idx, col_idx, rows, cols, ld_in, ld_out);
+  const cudaError_t e = launch_pdl(k_gather_il8<MAXC, NS, DROP>, dim3(grid), dim3(kIlThreads),
+                                   smem, s, static_cast<const uint16_t*>(in),
+                                   static_cast<uint16_t*>(out), row_idx, col_idx, rows, cols,
+                                   ld_in, ld_out, drop);
   end_launch("permute", s);
   return e;
 }
 
 // Rows too wide for shared memory: gather straight from global memory (L2 absorbs the
 // sector waste; only used beyond ~100k bf16 columns).
-template <typename E>
+template <typename E, int DROP>
 __global__ void __launch_bounds__(256)
     k_gather_rows_direct(const E* __restrict__ in, E* __restrict__ out,
                          const int32_t* __restrict__ row_idx,
                          const int32_t* __restrict__ col_idx, int rows, int cols, int64_t ld_in,
-                         int64_t ld_out) {
+                         int64_t ld_out, const DropArgs drop) {
+  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
   const unsigned ucols = (unsigned)cols;
   for (int r = blockIdx.x; r < rows; r += gridDim.x) {
     int sr = row_idx ? row_idx[r] : r;
@@ -349,14 +405,19 @@ __global__ void __launch_bounds__(256)
     E* dst = out + (int64_t)r * ld_out;
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
       unsigned ci = (unsigned)__ldg(col_idx + c);
-      dst[c] = src[ci < ucols ? ci : ucols - 1];
+      ci = ci < ucols ? ci : ucols - 1;
+      E v = src[ci];
+      if (DROP)
+        v = drop_one<E>(drop, drop_keep(drop, dstep, (uint32_t)r, DROP == kDropSource ? ci : c), v);
+      dst[c] = v;
     }
   }
 }
 
-template <typename E, int MAXV>
+template <typename E, int MAXV, int DROP>
 cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const int32_t* col_idx,
-                        int rows, int cols, int64_t ld_in, int64_t ld_out, cudaStream_t s) {
+                        int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs& drop,
+                        cudaStream_t s) {
   const size_t row_bytes = (size_t)cols * sizeof(E);
   // R rows per batch: ~32 KB per buffer, two buffers per CTA
   int R = (int)((32 * 1024) / row_bytes);
@@ -367,7 +428,7 @@ cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(k_gather_rows_pipe<E, MAXV>,
+    cudaError_t e = cudaFuncSetAttribute(k_gather_rows_pipe<E, MAXV, DROP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
@@ -378,17 +439,17 @@ cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const
   int grid = num_sms() * per_sm;
   if (grid > nbatch) grid = nbatch;
   begin_launch("permute", s);
-  k_gather_rows_pipe<E, MAXV><<<grid, kPipeThreads, smem, s>>>(
+  k_gather_rows_pipe<E, MAXV, DROP><<<grid, kPipeThreads, smem, s>>>(
       static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
-      ld_out, R);
+      ld_out, R, drop);
   end_launch("permute", s);
   return cudaGetLastError();
 }
 
-template <typename E>
+template <typename E, int DROP>
 cudaError_t gather_impl(const void* in, void* out, const int32_t* row_idx,
                         const int32_t* col_idx, int rows, int cols, int64_t ld_in,
-                        int64_t ld_out, cudaStream_t s) {
+                        int64_t ld_out, const DropArgs& drop, cudaStream_t s) {
   if (rows <= 0 || cols <= 0) return cudaSuccess;
   const size_t row_bytes = ((size_t)cols * sizeof(E) + 15) & ~size_t(15);
   const int sms = num_sms();
@@ -402,38 +463,45 @@ cudaError_t gather_impl(const void* in, void* out, const int32_t* row_idx,
   // the pipeline is as fast or faster (+5% at 2048, +19% at 2560, +10% at 4096 against the
   // interleaved forms that fit there)
   if (sizeof(E) == 2 && vec_ok && cols < 8 * kIlThreads && il_smem(4, cols) <= kIlMaxSmem)
-    return il8_launch<1, 4>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    return il8_launch<1, 4, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
   if (vec_ok && cols <= 65535 && nvec <= 8 * kPipeThreads && 2 * row_bytes <= 96 * 1024) {
     const int need = (nvec + kPipeThreads - 1) / kPipeThreads;
-    if (need <= 1) return pipe_launch<E, 1>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
-    if (need <= 2) return pipe_launch<E, 2>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
-    if (need <= 4) return pipe_launch<E, 4>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
-    return pipe_launch<E, 8>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    if (need <= 1)
+      return pipe_launch<E, 1, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
+    if (need <= 2)
+      return pipe_launch<E, 2, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
+    if (need <= 4)
+      return pipe_launch<E, 4, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
+    return pipe_launch<E, 8, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
   }
   if (row_bytes <= (size_t)kMaxSmemRowBytes) {
-    static bool attr_set = false;  // single-device use; the pipelined path covers the rest
-    if (!attr_set) {
-      cudaError_t e = cudaFuncSetAttribute(k_gather_rows_smem<E>,
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    if (!attr_set[dev]) {
+      cudaError_t e = cudaFuncSetAttribute(k_gather_rows_smem<E, DROP>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMaxSmemRowBytes);
       if (e != cudaSuccess) return e;
-      attr_set = true;
+      attr_set[dev] = true;
     }
     int per_sm = (int)(200 * 1024 / row_bytes);
     per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
     int grid = sms * per_sm;
     if (grid > rows) grid = rows;
     begin_launch("permute", s);
-    k_gather_rows_smem<E><<<grid, kGatherThreads, row_bytes, s>>>(
+    k_gather_rows_smem<E, DROP><<<grid, kGatherThreads, row_bytes, s>>>(
         static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
-        ld_out);
+        ld_out, drop);
     end_launch("permute", s);
   } else {
     int grid = sms * 8;
     if (grid > rows) grid = rows;
     begin_launch("permute", s);
-    k_gather_rows_direct<E><<<grid, 256, 0, s>>>(static_cast<const E*>(in), static_cast<E*>(out),
-                                                 row_idx, col_idx, rows, cols, ld_in, ld_out);
+    k_gather_rows_direct<E, DROP><<<grid, 256, 0, s>>>(
+        static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
+        ld_out, drop);
     end_launch("permute", s);
   }
   return cudaGetLastError();
@@ -462,9 +530,26 @@ cudaError_t launch_compose_perm(const int32_t* outer, const int32_t* inner, int3
 cudaError_t launch_gather(const void* in, void* out, const int32_t* row_idx,
                           const int32_t* col_idx, int rows, int cols, int64_t ld_in,
                           int64_t ld_out, int elem_bytes, cudaStream_t s) {
+  const DropArgs none = {};
   if (elem_bytes == 2)
-    return gather_impl<uint16_t>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
-  return gather_impl<uint32_t>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    return gather_impl<uint16_t, kDropNone>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out,
+                                            none, s);
+  return gather_impl<uint32_t, kDropNone>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out,
+                                          none, s);
+}
+
+cudaError_t launch_gather_drop(const DropArgs& d, bool mask_output, const void* in, void* out,
+                               const int32_t* col_idx, int rows, int cols, int elem_bytes,
+                               cudaStream_t s) {
+  if (elem_bytes == 2)
+    return mask_output ? gather_impl<uint16_t, kDropOutput>(in, out, nullptr, col_idx, rows, cols,
+                                                            cols, cols, d, s)
+                       : gather_impl<uint16_t, kDropSource>(in, out, nullptr, col_idx, rows, cols,
+                                                            cols, cols, d, s);
+  return mask_output ? gather_impl<uint32_t, kDropOutput>(in, out, nullptr, col_idx, rows, cols,
+                                                          cols, cols, d, s)
+                     : gather_impl<uint32_t, kDropSource>(in, out, nullptr, col_idx, rows, cols,
+                                                          cols, cols, d, s);
 }
 
 }  // namespace poetx

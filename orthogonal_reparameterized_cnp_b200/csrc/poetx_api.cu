@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "philox_dev.cuh"
 #include "poetx_internal.h"
 
 namespace poetx {
@@ -1008,12 +1009,15 @@ cudaError_t bf16_w0(const void* in, const void* W0p, void* out, int T, int n, in
 // The merged weight of a layer call: bf16 W0' (q == nullptr), or its int8 codes with per-row
 // scales (the int8 layer) plus one bf16 panel buffer for the shapes that the CTA-pair kernel
 // does not take.
+// A 4-bit weight is given by q4.codes (the other members unused).
 struct W0Ref {
   const void* bf16 = nullptr;
   const int8_t* q = nullptr;
   const float* s = nullptr;
   void* panel = nullptr;
   int panel_f = 0, panel_b = 0;  // panel widths (along N) of the forward / backward GEMMs
+  Q4Weight q4;
+  const void* ptr() const { return q4.codes ? (const void*)q4.codes : q ? (const void*)q : bf16; }
 };
 
 // Panels of the int8 weight along the GEMM's N: a multiple of 256, at most 32 MB of bf16
@@ -1045,6 +1049,7 @@ Q8Layout q8_layout(const poetx_linear_desc* d) {
 // W = V W0'^T (forward) or dV = dW W0' (backward) for either form of the weight.
 cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int m, bool forward,
                     cudaStream_t s) {
+  if (w.q4.codes) return launch_q4_product(w.q4, in, out, T, !forward, s);
   if (!w.q) return bf16_w0(in, w.bf16, out, T, n, m, forward, s);
   // the GEMM as it reads the bf16 merged weight (B's pointer is not used)
   UmmaGemm g;
@@ -1086,15 +1091,35 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
   return cudaSuccess;
 }
 
+// U = X[:, p_P], with dropout of X when `drop` is given.
+cudaError_t gather_x(const poetx_linear_desc* d, const DropArgs* drop, const void* x, void* U,
+                     cudaStream_t s) {
+  const int es = d->dtype == POETX_BF16 ? 2 : 4;
+  if (drop) return launch_gather_drop(*drop, false, x, U, d->perm_P, d->T, d->n, es, s);
+  return launch_gather(x, U, nullptr, d->perm_P, d->T, d->n, d->n, d->n, es, s);
+}
+
+// Tokens up to which the layer on a 4-bit weight takes the few-token kernels (three launches:
+// gather + block product, weight product, block product + scatter).
+constexpr int kFewTokens = 64;
+
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
 // Writes U (if U != x-gather target), V, W; Z and y only when y != nullptr.
 int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, const void* G_R,
-                 const W0Ref& w0, void* y, void* U, void* V, void* W, void* Z, cudaStream_t s) {
+                 const W0Ref& w0, const DropArgs* drop, void* y, void* U, void* V, void* W,
+                 void* Z, cudaStream_t s) {
   const void* W0p = w0.bf16;
   const int T = d->T, n = d->n, m = d->m, b = d->b;
   const bool bf = d->dtype == POETX_BF16;
   const int es = bf ? 2 : 4;
-  POETX_CUDA(launch_gather(x, U, nullptr, d->perm_P, T, n, n, n, es, s), "gather x");
+  if (w0.q4.codes && !drop && T <= kFewTokens) {
+    POETX_CUDA(launch_bd_gather(G_P, x, V, U, d->perm_P, T, n, b, s), "gather + blockdiag G_P");
+    POETX_CUDA(w0_gemm(V, w0, W, T, n, m, true, s), "W0' product");
+    if (y)
+      POETX_CUDA(launch_bd_scatter(G_R, W, y, d->perm_R, T, m, b, s), "blockdiag G_R + scatter");
+    return POETX_OK;
+  }
+  POETX_CUDA(gather_x(d, drop, x, U, s), "gather x");
   if (bf) {
     POETX_CUDA(bf16_blockdiag(U, G_P, V, T, n, b, false, s), "blockdiag G_P");
     POETX_CUDA(w0_gemm(V, w0, W, T, n, m, true, s), "W0' gemm");
@@ -1138,13 +1163,12 @@ size_t poetx_linear_bwd_workspace(const poetx_linear_desc* d, int has_save_u, in
 
 namespace {
 int linear_fwd_impl(const poetx_linear_desc* d, const void* x, const void* G_P, const void* G_R,
-                    const W0Ref& w0, void* y, void* save_u, void* save_w, void* ws,
-                    size_t ws_bytes, void* stream) {
+                    const W0Ref& w0, const DropArgs* drop, void* y, void* save_u, void* save_w,
+                    void* ws, size_t ws_bytes, void* stream) {
   int st = linear_validate(d);
   if (st != POETX_OK) return st;
   if (d->T == 0) return POETX_OK;
-  if ((st = check_ptrs({x, G_P, G_R, w0.q ? (const void*)w0.q : w0.bf16, y})) != POETX_OK)
-    return st;
+  if ((st = check_ptrs({x, G_P, G_R, w0.ptr(), y})) != POETX_OK) return st;
   if ((st = check_opt(save_u)) != POETX_OK || (st = check_opt(save_w)) != POETX_OK) return st;
   const FwdLayout L = fwd_layout(d, save_u != nullptr, save_w != nullptr);
   if (ws_bytes < L.total) return fail(POETX_ERR_WORKSPACE, "forward scratch too small");
@@ -1155,13 +1179,14 @@ int linear_fwd_impl(const poetx_linear_desc* d, const void* x, const void* G_P, 
   void* V = cv.take(L.V);
   void* W = save_w ? save_w : cv.take(L.W);
   void* Z = cv.take(L.Z);
-  return forward_body(d, x, G_P, G_R, w0, y, U, V, W, Z, static_cast<cudaStream_t>(stream));
+  return forward_body(d, x, G_P, G_R, w0, drop, y, U, V, W, Z,
+                      static_cast<cudaStream_t>(stream));
 }
 
 int linear_bwd_impl(const poetx_linear_desc* d, const void* x, const void* dy, const void* G_P,
-                    const void* G_R, const W0Ref& w0, const void* save_u, const void* save_w,
-                    void* dx, float* dG_P, float* dG_R, int accumulate, void* ws,
-                    size_t ws_bytes, void* stream) {
+                    const void* G_R, const W0Ref& w0, const DropArgs* drop, const void* save_u,
+                    const void* save_w, void* dx, float* dG_P, float* dG_R, int accumulate,
+                    void* ws, size_t ws_bytes, void* stream) {
   const void* W0p = w0.bf16;
   int st = linear_validate(d);
   if (st != POETX_OK) return st;
@@ -1178,8 +1203,7 @@ int linear_bwd_impl(const poetx_linear_desc* d, const void* x, const void* dy, c
     }
     return POETX_OK;
   }
-  if ((st = check_ptrs({dy, G_P, G_R, w0.q ? (const void*)w0.q : W0p, dx})) != POETX_OK)
-    return st;
+  if ((st = check_ptrs({dy, G_P, G_R, w0.ptr(), dx})) != POETX_OK) return st;
   if ((st = check_opt(save_u)) != POETX_OK || (st = check_opt(save_w)) != POETX_OK) return st;
   if (!save_u || !save_w)
     if ((st = check_ptrs({x})) != POETX_OK) return st;
@@ -1201,10 +1225,10 @@ int linear_bwd_impl(const poetx_linear_desc* d, const void* x, const void* dy, c
   float* partP = static_cast<float*>(cv.take(L.partP));
   // recompute what the forward did not save (POET-X section 2.5, checkpointing)
   if (!save_w) {
-    st = forward_body(d, x, G_P, G_R, w0, nullptr, U, Vr, W, nullptr, s);
+    st = forward_body(d, x, G_P, G_R, w0, drop, nullptr, U, Vr, W, nullptr, s);
     if (st != POETX_OK) return st;
   } else if (!save_u) {
-    POETX_CUDA(launch_gather(x, U, nullptr, d->perm_P, T, n, n, n, es, s), "gather x");
+    POETX_CUDA(gather_x(d, drop, x, U, s), "gather x");
   }
   // B1: dZ = dY[:, p_R]; dW_j = dZ_j G_R,j; dG_R,j = dZ_j^T W_j
   POETX_CUDA(launch_gather(dy, dZ, nullptr, d->perm_R, T, m, m, m, es, s), "gather dy");
@@ -1232,7 +1256,10 @@ int linear_bwd_impl(const poetx_linear_desc* d, const void* x, const void* dy, c
     POETX_CUDA(f32_block_grad((const float*)dV, (const float*)U, dG_P, T, n, b, accumulate, s),
                "dG_P");
   }
-  POETX_CUDA(launch_gather(dU, dx, nullptr, d->inv_P, T, n, n, n, es, s), "scatter dx");
+  if (drop)
+    POETX_CUDA(launch_gather_drop(*drop, true, dU, dx, d->inv_P, T, n, es, s), "scatter dx");
+  else
+    POETX_CUDA(launch_gather(dU, dx, nullptr, d->inv_P, T, n, n, n, es, s), "scatter dx");
   return POETX_OK;
 }
 }  // namespace
@@ -1244,7 +1271,7 @@ int poetx_linear_fwd(const poetx_linear_desc* d, const void* x, const void* G_P,
                      size_t ws_bytes, void* stream) {
   W0Ref w;
   w.bf16 = W0p;
-  return linear_fwd_impl(d, x, G_P, G_R, w, y, save_u, save_w, ws, ws_bytes, stream);
+  return linear_fwd_impl(d, x, G_P, G_R, w, nullptr, y, save_u, save_w, ws, ws_bytes, stream);
 }
 
 int poetx_linear_bwd(const poetx_linear_desc* d, const void* x, const void* dy, const void* G_P,
@@ -1253,8 +1280,8 @@ int poetx_linear_bwd(const poetx_linear_desc* d, const void* x, const void* dy, 
                      size_t ws_bytes, void* stream) {
   W0Ref w;
   w.bf16 = W0p;
-  return linear_bwd_impl(d, x, dy, G_P, G_R, w, save_u, save_w, dx, dG_P, dG_R, accumulate, ws,
-                         ws_bytes, stream);
+  return linear_bwd_impl(d, x, dy, G_P, G_R, w, nullptr, save_u, save_w, dx, dG_P, dG_R,
+                         accumulate, ws, ws_bytes, stream);
 }
 
 size_t poetx_outer_merge_workspace(int32_t m, int32_t n, int dtype) {
@@ -1395,7 +1422,7 @@ int poetx_linear_fwd_q8(const poetx_linear_desc* d, const void* x, const void* G
   size_t rest_bytes = 0;
   int st = q8_weight(d, W0q, scales, ws, ws_bytes, &w, &rest, &rest_bytes);
   if (st != POETX_OK) return st;
-  return linear_fwd_impl(d, x, G_P, G_R, w, y, save_u, save_w, rest, rest_bytes, stream);
+  return linear_fwd_impl(d, x, G_P, G_R, w, nullptr, y, save_u, save_w, rest, rest_bytes, stream);
 }
 
 int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* dy,
@@ -1407,8 +1434,227 @@ int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* d
   size_t rest_bytes = 0;
   int st = q8_weight(d, W0q, scales, ws, ws_bytes, &w, &rest, &rest_bytes);
   if (st != POETX_OK) return st;
-  return linear_bwd_impl(d, x, dy, G_P, G_R, w, save_u, save_w, dx, dG_P, dG_R, accumulate, rest,
+  return linear_bwd_impl(d, x, dy, G_P, G_R, w, nullptr, save_u, save_w, dx, dG_P, dG_R,
+                         accumulate, rest, rest_bytes, stream);
+}
+
+}  // extern "C"
+
+// ======================================================================= 4-bit weight, dropout
+namespace {
+
+int q4_validate(int32_t m, int32_t n, int32_t group) {
+  if (m < 0 || n < 0) return fail(POETX_ERR_INVALID_ARG, "negative size");
+  if (group != 32 && group != 64 && group != 128)
+    return fail(POETX_ERR_SHAPE, "group must be 32, 64 or 128");
+  if (n % 128) return fail(POETX_ERR_SHAPE, "n must be a multiple of 128 (4-bit weight)");
+  return POETX_OK;
+}
+
+// thr = round(65536 p); *on = false when nothing is dropped (p rounds to 0)
+int drop_args(const poetx_dropout_desc* drop, int64_t rows, DropArgs* a, bool* on) {
+  *on = false;
+  if (!drop) return POETX_OK;
+  if (!(drop->p >= 0.0 && drop->p <= 65535.0 / 65536.0))
+    return fail(POETX_ERR_INVALID_ARG, "dropout p must be in [0, 65535/65536]");
+  if ((int64_t)drop->row0 + rows > (1ll << 32))
+    return fail(POETX_ERR_INVALID_ARG, "dropout row0 + rows must not pass 2^32");
+  if (reinterpret_cast<uintptr_t>(drop->step) & 7)
+    return fail(POETX_ERR_ALIGN, "dropout step counter must be 8-byte aligned");
+  const uint32_t thr = (uint32_t)(drop->p * 65536.0 + 0.5);
+  a->k0 = (uint32_t)drop->seed;
+  a->k1 = (uint32_t)(drop->seed >> 32);
+  a->row0 = drop->row0;
+  a->site = drop->site;
+  a->thr_hi = thr << 16;
+  a->scale = (float)(65536.0 / (65536.0 - (double)thr));
+  a->step = reinterpret_cast<const unsigned long long*>(drop->step);
+  *on = thr != 0;
+  return POETX_OK;
+}
+
+// The weight of a poetx_linear_{fwd,bwd}_ex call as a W0Ref; the int8 form takes its panel
+// buffer from the head of ws.
+int ex_weight(const poetx_linear_desc* d, const poetx_linear_weight* w, void* ws, size_t ws_bytes,
+              W0Ref* r, void** rest, size_t* rest_bytes) {
+  if (!w) return fail(POETX_ERR_INVALID_ARG, "weight is NULL");
+  *rest = ws;
+  *rest_bytes = ws_bytes;
+  int st;
+  if (w->kind == POETX_WEIGHT_DENSE) {
+    r->bf16 = w->w;
+    return POETX_OK;
+  }
+  if (w->kind == POETX_WEIGHT_Q8)
+    return q8_weight(d, static_cast<const int8_t*>(w->w), static_cast<const float*>(w->scales), ws,
+                     ws_bytes, r, rest, rest_bytes);
+  if (w->kind != POETX_WEIGHT_Q4)
+    return fail(POETX_ERR_INVALID_ARG, "unknown weight kind");
+  if ((st = linear_validate(d)) != POETX_OK) return st;
+  if (d->dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "the 4-bit weight needs the bf16 layer");
+  if ((st = q4_validate(d->m, d->n, w->group)) != POETX_OK) return st;
+  if (d->T > 0 && (st = check_ptrs({w->w, w->scales})) != POETX_OK) return st;
+  r->q4.codes = static_cast<const uint8_t*>(w->w);
+  r->q4.scales = w->scales;
+  r->q4.m = d->m;
+  r->q4.n = d->n;
+  r->q4.group = w->group;
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int poetx_quantize_q4(const void* W, uint8_t* q, void* scales, int32_t m, int32_t n, int32_t group,
+                      int dtype, void* stream) {
+  return poetx_merge_perm_q4(W, q, scales, m, n, nullptr, nullptr, group, dtype, stream);
+}
+
+int poetx_merge_perm_q4(const void* W0, uint8_t* W0q, void* scales, int32_t m, int32_t n,
+                        const int32_t* perm_R, const int32_t* perm_P, int32_t group, int dtype,
+                        void* stream) {
+  if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "bad dtype");
+  int st = q4_validate(m, n, group);
+  if (st != POETX_OK) return st;
+  if (m == 0 || n == 0) return POETX_OK;
+  if ((st = check_ptrs({W0, W0q, scales})) != POETX_OK) return st;
+  if ((perm_R == nullptr) != (perm_P == nullptr))
+    return fail(POETX_ERR_INVALID_ARG, "both index maps must be given, or neither");
+  if ((st = check_opt(perm_R)) != POETX_OK || (st = check_opt(perm_P)) != POETX_OK) return st;
+  const int es = dtype == POETX_BF16 ? 2 : 4;
+  if ((size_t)n * es > 200 * 1024)
+    return fail(POETX_ERR_SHAPE, "rows wider than 200 KB are not supported");
+  Q4Weight w;
+  w.codes = W0q;
+  w.scales = scales;
+  w.m = m;
+  w.n = n;
+  w.group = group;
+  POETX_CUDA(launch_merge_q4(W0, perm_R, perm_P, w, es, static_cast<cudaStream_t>(stream)),
+             "merge + quantize (4 bits)");
+  return POETX_OK;
+}
+
+int poetx_dequantize_q4(const uint8_t* q, const void* scales, void* out, int32_t m, int32_t n,
+                        int32_t group, int dtype, void* stream) {
+  if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "bad dtype");
+  int st = q4_validate(m, n, group);
+  if (st != POETX_OK) return st;
+  if (m == 0 || n == 0) return POETX_OK;
+  if ((st = check_ptrs({q, scales, out})) != POETX_OK) return st;
+  Q4Weight w;
+  w.codes = q;
+  w.scales = scales;
+  w.m = m;
+  w.n = n;
+  w.group = group;
+  POETX_CUDA(launch_dequant_q4(w, out, dtype == POETX_BF16 ? 2 : 4,
+                               static_cast<cudaStream_t>(stream)),
+             "dequantize (4 bits)");
+  return POETX_OK;
+}
+
+int poetx_matmul_q4(const void* x, const uint8_t* W0q, const void* scales, void* y, int32_t T,
+                    int32_t m, int32_t n, int32_t group, int transpose, void* stream) {
+  if (transpose != 0 && transpose != 1)
+    return fail(POETX_ERR_INVALID_ARG, "transpose must be 0 or 1");
+  if (T < 0) return fail(POETX_ERR_INVALID_ARG, "negative size");
+  int st = q4_validate(m, n, group);
+  if (st != POETX_OK) return st;
+  if (m < 1 || n < 1) return fail(POETX_ERR_INVALID_ARG, "m and n must be >= 1");
+  if (T == 0) return POETX_OK;
+  if ((st = check_ptrs({x, W0q, scales, y})) != POETX_OK) return st;
+  if (x == y) return fail(POETX_ERR_INVALID_ARG, "x and y must be distinct");
+  W0Ref w;
+  w.q4.codes = W0q;
+  w.q4.scales = scales;
+  w.q4.m = m;
+  w.q4.n = n;
+  w.q4.group = group;
+  POETX_CUDA(w0_gemm(x, w, y, T, n, m, transpose == 0, static_cast<cudaStream_t>(stream)),
+             "4-bit product");
+  return POETX_OK;
+}
+
+int poetx_dropout(const poetx_dropout_desc* drop, const void* in, void* out, int32_t rows,
+                  int32_t cols, int dtype, void* stream) {
+  if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "bad dtype");
+  if (rows < 0 || cols < 0) return fail(POETX_ERR_INVALID_ARG, "negative size");
+  if (!drop) return fail(POETX_ERR_INVALID_ARG, "dropout descriptor is NULL");
+  DropArgs a;
+  bool on;
+  int st = drop_args(drop, rows, &a, &on);
+  if (st != POETX_OK) return st;
+  if (rows == 0 || cols == 0) return POETX_OK;
+  if ((st = check_ptrs({in, out})) != POETX_OK) return st;
+  POETX_CUDA(launch_dropout(a, in, out, rows, cols, dtype == POETX_BF16 ? 2 : 4,
+                            static_cast<cudaStream_t>(stream)),
+             "dropout launch");
+  return POETX_OK;
+}
+
+int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, void* out,
+                               const int32_t* idx, int32_t rows, int32_t cols, int mask_output,
+                               int dtype, void* stream) {
+  if (rows < 0 || cols < 0) return fail(POETX_ERR_INVALID_ARG, "negative size");
+  if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "bad dtype");
+  if (mask_output != 0 && mask_output != 1)
+    return fail(POETX_ERR_INVALID_ARG, "mask_output must be 0 or 1");
+  if (!drop) return fail(POETX_ERR_INVALID_ARG, "dropout descriptor is NULL");
+  DropArgs a;
+  bool on;
+  int st = drop_args(drop, rows, &a, &on);
+  if (st != POETX_OK) return st;
+  if (rows == 0 || cols == 0) return POETX_OK;
+  if ((st = check_ptrs({in, out, idx})) != POETX_OK) return st;
+  if (in == out) return fail(POETX_ERR_INVALID_ARG, "in and out must be distinct");
+  POETX_CUDA(launch_gather_drop(a, mask_output != 0, in, out, idx, rows, cols,
+                                dtype == POETX_BF16 ? 2 : 4, static_cast<cudaStream_t>(stream)),
+             "permute + dropout launch");
+  return POETX_OK;
+}
+
+size_t poetx_linear_ex_workspace(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                                 int has_save_u, int has_save_w) {
+  if (!d || !w || d->T < 0 || d->n < 1 || d->m < 1 || d->b < 1) return 0;
+  const size_t f = fwd_layout(d, has_save_u, has_save_w).total;
+  const size_t g = bwd_layout(d, has_save_u, has_save_w).total;
+  const size_t extra = w->kind == POETX_WEIGHT_Q8 ? poetx_linear_q8_scratch(d) : 0;
+  return extra + (f > g ? f : g);
+}
+
+int poetx_linear_fwd_ex(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                        const poetx_dropout_desc* drop, const void* x, const void* G_P,
+                        const void* G_R, void* y, void* save_u, void* save_w, void* ws,
+                        size_t ws_bytes, void* stream) {
+  W0Ref r;
+  void* rest = nullptr;
+  size_t rest_bytes = 0;
+  DropArgs a;
+  bool on;
+  int st = ex_weight(d, w, ws, ws_bytes, &r, &rest, &rest_bytes);
+  if (st != POETX_OK) return st;
+  if ((st = drop_args(drop, d ? d->T : 0, &a, &on)) != POETX_OK) return st;
+  return linear_fwd_impl(d, x, G_P, G_R, r, on ? &a : nullptr, y, save_u, save_w, rest,
                          rest_bytes, stream);
+}
+
+int poetx_linear_bwd_ex(const poetx_linear_desc* d, const poetx_linear_weight* w,
+                        const poetx_dropout_desc* drop, const void* x, const void* dy,
+                        const void* G_P, const void* G_R, const void* save_u, const void* save_w,
+                        void* dx, float* dG_P, float* dG_R, int accumulate, void* ws,
+                        size_t ws_bytes, void* stream) {
+  W0Ref r;
+  void* rest = nullptr;
+  size_t rest_bytes = 0;
+  DropArgs a;
+  bool on;
+  int st = ex_weight(d, w, ws, ws_bytes, &r, &rest, &rest_bytes);
+  if (st != POETX_OK) return st;
+  if ((st = drop_args(drop, d ? d->T : 0, &a, &on)) != POETX_OK) return st;
+  return linear_bwd_impl(d, x, dy, G_P, G_R, r, on ? &a : nullptr, save_u, save_w, dx, dG_P, dG_R,
+                         accumulate, rest, rest_bytes, stream);
 }
 
 int poetx_device_status(void* stream) {

@@ -92,6 +92,38 @@ cudaError_t launch_dequant_rows(const int8_t* q, const float* s, void* out, int 
 cudaError_t launch_dequant_2d(const int8_t* q, int64_t ldq, const float* s, void* out,
                               int64_t ldo, int rows, int cols, cudaStream_t st);
 
+// ---- 4-bit base weight (kernels_q4.cu; format in q4_dev.cuh) -----------------------
+// codes: uint8 [n/128][m][64], scales: bf16 [n/128][m][128/group]; n % 128 == 0
+struct Q4Weight {
+  const uint8_t* codes = nullptr;
+  const void* scales = nullptr;
+  int m = 0, n = 0, group = 0;  // group in {32, 64, 128}
+};
+// codes and scales of W0[perm_R][:, perm_P] (NULL maps: identity)
+cudaError_t launch_merge_q4(const void* W0, const int32_t* perm_R, const int32_t* perm_P,
+                            const Q4Weight& w, int elem_bytes, cudaStream_t s);
+cudaError_t launch_dequant_q4(const Q4Weight& w, void* out, int elem_bytes, cudaStream_t s);
+// y[T, m] = x[T, n] W^T, or (transpose) y[T, n] = x[T, m] W: the few-token kernels, any T
+cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
+                              cudaStream_t s);
+// few-token block products fused with their index maps (bf16; width % b == 0, b % 128 == 0):
+// out = blockdiag(G) x[:, idx]^T by rows (save_u: the gathered rows too), and y[:, idx] =
+// the block product of `in`
+cudaError_t launch_bd_gather(const void* G, const void* x, void* out, void* save_u,
+                             const int32_t* idx, int T, int width, int b, cudaStream_t s);
+cudaError_t launch_bd_scatter(const void* G, const void* in, void* y, const int32_t* idx, int T,
+                              int width, int b, cudaStream_t s);
+
+// ---- dropout (kernels_dropout.cu, kernels_perm.cu; generator in philox_dev.cuh) ------
+struct DropArgs;
+cudaError_t launch_dropout(const DropArgs& d, const void* in, void* out, int rows, int cols,
+                           int elem_bytes, cudaStream_t s);
+// dropout fused with an index map of the columns: out[r, c] = in[r, idx[c]], masked by the
+// source column idx[c] or (mask_output) by the output column c
+cudaError_t launch_gather_drop(const DropArgs& d, bool mask_output, const void* in, void* out,
+                               const int32_t* col_idx, int rows, int cols, int elem_bytes,
+                               cudaStream_t s);
+
 // ---- fp32 SIMT batched GEMM (kernels_sgemm.cu) -----------------------------------
 enum SgemmMode { SG_FULL = 0, SG_SYM = 1, SG_SYMSKEW = 2 };
 

@@ -40,6 +40,24 @@ class LinearDesc(ctypes.Structure):
                 ("perm_P", _vp), ("inv_P", _vp), ("perm_R", _vp), ("inv_R", _vp)]
 
 
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", _c_u64), ("site", ctypes.c_uint32),
+                ("row0", ctypes.c_uint32), ("step", _vp)]
+
+
+POETX_WEIGHT_DENSE = 0
+POETX_WEIGHT_Q8 = 1
+POETX_WEIGHT_Q4 = 2
+
+
+class LinearWeight(ctypes.Structure):
+    _fields_ = [("kind", _c_i32), ("group", _c_i32), ("w", _vp), ("scales", _vp)]
+
+
+_descp = ctypes.POINTER(LinearDesc)
+_dropp = ctypes.POINTER(DropoutDesc)
+_weightp = ctypes.POINTER(LinearWeight)
+
 # name -> (restype, argtypes); the same list is checked against include/poetx.h by the tests
 SIGNATURES = {
     "poetx_status_string": (ctypes.c_char_p, [_c_int]),
@@ -79,6 +97,20 @@ SIGNATURES = {
                                      _vp, _vp, _vp, _c_size, _vp]),
     "poetx_linear_bwd_q8": (_c_int, [ctypes.POINTER(LinearDesc), _vp, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]),
+    "poetx_quantize_q4": (_c_int, [_vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _c_int, _vp]),
+    "poetx_merge_perm_q4": (_c_int, [_vp, _vp, _vp, _c_i32, _c_i32, _vp, _vp, _c_i32, _c_int,
+                                     _vp]),
+    "poetx_dequantize_q4": (_c_int, [_vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _c_int, _vp]),
+    "poetx_matmul_q4": (_c_int, [_vp, _vp, _vp, _vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_int,
+                                 _vp]),
+    "poetx_dropout": (_c_int, [_dropp, _vp, _vp, _c_i32, _c_i32, _c_int, _vp]),
+    "poetx_permute_cols_dropout": (_c_int, [_dropp, _vp, _vp, _vp, _c_i32, _c_i32, _c_int,
+                                            _c_int, _vp]),
+    "poetx_linear_ex_workspace": (_c_size, [_descp, _weightp, _c_int, _c_int]),
+    "poetx_linear_fwd_ex": (_c_int, [_descp, _weightp, _dropp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _c_size, _vp]),
+    "poetx_linear_bwd_ex": (_c_int, [_descp, _weightp, _dropp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _vp, _c_int, _vp, _c_size, _vp]),
     "poetx_launch_count": (_c_u64, []),
     "poetx_profile_begin": (_c_int, [ctypes.c_char_p]),
     "poetx_profile_end": (_c_int, [_i32p, ctypes.POINTER(ctypes.c_double)]),
@@ -365,6 +397,230 @@ def linear_bwd_q8(desc: LinearDesc, x, dy, G_P, G_R, W0q, scales, save_u, save_w
            "poetx_linear_bwd_q8")
 
 
+# ------------------------------------------------------------------------ 4-bit weight
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_current_device(*tensors):
+    """The calls below launch on the current device's stream: their tensors must live there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"expected tensors on the current CUDA device ({dev}), got {t.device}")
+
+
+def q4_shapes(m: int, n: int, group: int):
+    """Shapes of the codes (uint8) and scales (bf16) of an m x n 4-bit weight."""
+    _require(group in (32, 64, 128), "group must be 32, 64 or 128")
+    _require(n % 128 == 0, "n must be a multiple of 128 (4-bit weight)")
+    return (n // 128, m, 64), (n // 128, m, 128 // group)
+
+
+def _check_q4(q, scales, m, n, group):
+    import torch
+    qs, ss = q4_shapes(m, n, group)
+    _require(tuple(q.shape) == qs and q.dtype == torch.uint8,
+             f"the codes of a {m} x {n} 4-bit weight are uint8 {qs}")
+    _require(tuple(scales.shape) == ss and scales.dtype == torch.bfloat16,
+             f"the scales of a {m} x {n} 4-bit weight with groups of {group} are bfloat16 {ss}")
+
+
+def _check_map(idx, n, what):
+    import torch
+    _require(idx is None or (idx.dtype == torch.int32 and tuple(idx.shape) == (n,)),
+             f"{what} must be int32 with {n} entries")
+
+
+def quantize_q4(W, q, scales, group: int, stream=None):
+    """4-bit codes and group scales of W (format and rounding: see the header)."""
+    _require_cuda()
+    m, n = W.shape
+    _check_q4(q, scales, m, n, group)
+    _on_current_device(W, q, scales)
+    _check(_load().poetx_quantize_q4(_ptr(W), _ptr(q), _ptr(scales), m, n, group, _dtype_code(W),
+                                     _stream(stream)), "poetx_quantize_q4")
+
+
+def merge_perm_q4(W0, q, scales, perm_R, perm_P, group: int, stream=None):
+    """4-bit codes and group scales of W0' = W0[perm_R][:, perm_P], without forming W0' (both
+    maps None: identity)."""
+    _require_cuda()
+    m, n = W0.shape
+    _check_q4(q, scales, m, n, group)
+    _check_map(perm_R, m, "perm_R")
+    _check_map(perm_P, n, "perm_P")
+    _on_current_device(W0, q, scales, perm_R, perm_P)
+    _check(_load().poetx_merge_perm_q4(_ptr(W0), _ptr(q), _ptr(scales), m, n, _ptr(perm_R),
+                                       _ptr(perm_P), group, _dtype_code(W0), _stream(stream)),
+           "poetx_merge_perm_q4")
+
+
+def dequantize_q4(q, scales, out, group: int, stream=None):
+    """out [m, n] (bf16 or fp32) = the weight that 4-bit codes and scales stand for."""
+    _require_cuda()
+    m, n = out.shape
+    _check_q4(q, scales, m, n, group)
+    _on_current_device(q, scales, out)
+    _check(_load().poetx_dequantize_q4(_ptr(q), _ptr(scales), _ptr(out), m, n, group,
+                                       _dtype_code(out), _stream(stream)), "poetx_dequantize_q4")
+
+
+def matmul_q4(x, q, scales, y, group: int, transpose: bool = False, stream=None):
+    """y = x W^T (or, transpose, y = x W) with the 4-bit weight W [m, n]; bf16, T >= 0 rows."""
+    import torch
+    _require_cuda()
+    m, n = (x.shape[1], y.shape[1]) if transpose else (y.shape[1], x.shape[1])
+    T = x.shape[0]
+    _require(y.shape[0] == T, "x and y must have the same number of rows")
+    _require(x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be bfloat16")
+    _check_q4(q, scales, m, n, group)
+    _on_current_device(x, q, scales, y)
+    _check(_load().poetx_matmul_q4(_ptr(x), _ptr(q), _ptr(scales), _ptr(y), T, m, n, group,
+                                   int(bool(transpose)), _stream(stream)), "poetx_matmul_q4")
+
+
+# ------------------------------------------------------------------------ dropout
+def dropout_desc(p: float, seed: int, site: int = 0, row0: int = 0, step=None) -> DropoutDesc:
+    """Dropout settings of a call; step: a one-element int64 CUDA tensor (or None)."""
+    import torch
+    if step is not None:
+        _require(step.dtype == torch.int64 and step.numel() == 1 and step.is_cuda,
+                 "step must be a one-element int64 CUDA tensor")
+    _require(0 <= site < 1 << 32 and 0 <= row0 < 1 << 32, "site and row0 are 32-bit numbers")
+    d = DropoutDesc(float(p), seed & ((1 << 64) - 1), site, row0,
+                    None if step is None else step.data_ptr())
+    d.keep = step  # the tensor lives as long as the descriptor
+    return d
+
+
+def dropout(drop: DropoutDesc, x, out, stream=None):
+    """out = dropout(x) (out may be x); the backward is the same call on the gradient."""
+    _require_cuda()
+    rows, cols = x.shape
+    _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
+    _on_current_device(x, out, drop.keep)
+    _check(_load().poetx_dropout(ctypes.byref(drop), _ptr(x), _ptr(out), rows, cols,
+                                 _dtype_code(x), _stream(stream)), "poetx_dropout")
+
+
+def permute_cols_dropout(drop: DropoutDesc, x, out, idx, mask_output: bool = False, stream=None):
+    """out[:, i] = dropout(x)[:, idx[i]], or (mask_output) x[:, idx[i]] masked by the output
+    column: with the inverse map, the gradient of the first form."""
+    _require_cuda()
+    rows, cols = x.shape
+    _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
+    _check_map(idx, cols, "idx")
+    _on_current_device(x, out, idx, drop.keep)
+    _check(_load().poetx_permute_cols_dropout(ctypes.byref(drop), _ptr(x), _ptr(out), _ptr(idx),
+                                              rows, cols, int(bool(mask_output)), _dtype_code(x),
+                                              _stream(stream)), "poetx_permute_cols_dropout")
+
+
+class Dropout:
+    """Dropout of a layer's input: probability, seed, site and a step counter in device memory
+    (read by the kernels when they run, so a replayed CUDA graph draws a new mask each time the
+    counter moves).  Layers of one program share the counter and differ in ``site``; a
+    data-parallel rank sets ``row0`` to the first token of its shard, so that the masks do not
+    depend on the sharding."""
+
+    def __init__(self, p: float, seed: int, site: int = 0, row0: int = 0, step=None, device=None):
+        import torch
+        _require(0.0 <= p <= 65535 / 65536, "p must be in [0, 65535/65536]")
+        if step is None:
+            step = torch.zeros(1, dtype=torch.int64, device=device or "cuda")
+        self.p, self.seed, self.site, self.row0, self.step = p, seed, site, row0, step
+
+    def at_site(self, site: int) -> "Dropout":
+        """The same dropout at another site (same seed and step counter)."""
+        return Dropout(self.p, self.seed, site, self.row0, self.step)
+
+    def desc(self) -> DropoutDesc:
+        return dropout_desc(self.p, self.seed, self.site, self.row0, self.step)
+
+    def advance(self, stream=None):
+        """Moves the step counter (on `stream`): the next forward draws a new mask."""
+        import torch
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            self.step.add_(1)
+
+
+# ------------------------------------------------------------------------ layer, any weight
+def linear_weight_dense(W0p) -> LinearWeight:
+    w = LinearWeight(POETX_WEIGHT_DENSE, 0, _ptr(W0p), None)
+    w.keep = (W0p,)
+    return w
+
+
+def linear_weight_q8(W0q, scales) -> LinearWeight:
+    w = LinearWeight(POETX_WEIGHT_Q8, 0, _ptr(W0q), _ptr(scales))
+    w.keep = (W0q, scales)
+    return w
+
+
+def linear_weight_q4(W0q, scales, group: int) -> LinearWeight:
+    w = LinearWeight(POETX_WEIGHT_Q4, group, _ptr(W0q), _ptr(scales))
+    w.keep = (W0q, scales)
+    return w
+
+
+def _check_weight(desc: LinearDesc, w: LinearWeight):
+    if w.kind == POETX_WEIGHT_Q4:
+        _check_q4(*w.keep, desc.m, desc.n, w.group)
+    elif w.kind == POETX_WEIGHT_Q8:
+        import torch
+        q, s = w.keep
+        _require(tuple(q.shape) == (desc.m, desc.n) and q.dtype == torch.int8 and
+                 tuple(s.shape) == (desc.m,) and s.dtype == torch.float32,
+                 "the int8 weight is int8 [m, n] with float32 scales [m]")
+    else:
+        _require(tuple(w.keep[0].shape) == (desc.m, desc.n), "the merged weight is [m, n]")
+
+
+def _drop_ref(drop):
+    return None if drop is None else ctypes.byref(drop)
+
+
+def linear_ex_workspace(desc: LinearDesc, weight: LinearWeight, has_save_u=True,
+                        has_save_w=True) -> int:
+    """Scratch bytes of linear_fwd_ex and linear_bwd_ex (the larger of the two)."""
+    return int(_load().poetx_linear_ex_workspace(ctypes.byref(desc), ctypes.byref(weight),
+                                                 int(has_save_u), int(has_save_w)))
+
+
+def linear_fwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, G_P, G_R, y, save_u, save_w,
+                  ws, stream=None):
+    """Layer forward on any form of the merged weight, with dropout of x (drop or None)."""
+    _require_cuda()
+    _check_weight(desc, weight)
+    _on_current_device(x, y, G_P, G_R, save_u, save_w, ws, *weight.keep)
+    _require(tuple(x.shape) == (desc.T, desc.n) and tuple(y.shape) == (desc.T, desc.m),
+             "x must be [T, n] and y [T, m]")
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_load().poetx_linear_fwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
+                                       _ptr(x), _ptr(G_P), _ptr(G_R), _ptr(y), _ptr(save_u),
+                                       _ptr(save_w), _ptr(ws), ws_bytes, _stream(stream)),
+           "poetx_linear_fwd_ex")
+
+
+def linear_bwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, dy, G_P, G_R, save_u, save_w,
+                  dx, dG_P, dG_R, accumulate: int, ws, stream=None):
+    """Layer backward on any form of the merged weight; drop as in the forward."""
+    _require_cuda()
+    _check_weight(desc, weight)
+    _on_current_device(x, dy, dx, G_P, G_R, save_u, save_w, dG_P, dG_R, ws, *weight.keep)
+    _require(tuple(dx.shape) == (desc.T, desc.n) and tuple(dy.shape) == (desc.T, desc.m),
+             "dx must be [T, n] and dy [T, m]")
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_load().poetx_linear_bwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
+                                       _ptr(x), _ptr(dy), _ptr(G_P), _ptr(G_R), _ptr(save_u),
+                                       _ptr(save_w), _ptr(dx), _ptr(dG_P), _ptr(dG_R),
+                                       int(accumulate), _ptr(ws), ws_bytes, _stream(stream)),
+           "poetx_linear_bwd_ex")
+
+
 def selftest_wait_timeout(theta, G, b: int, k: int, ws, stream=None):
     """Runs the CNP forward with a dependency that is never met (see the header)."""
     _require_cuda()
@@ -429,6 +685,7 @@ class CnpBuffers:
 
 
 def _layer_scratch_bytes(desc, save: bool, int8: bool) -> int:
+    """(The 4-bit layer needs no scratch beyond the bf16 layer's.)"""
     q8 = linear_q8_scratch(desc) if int8 else 0
     return max(linear_fwd_workspace(desc, save, save), linear_bwd_workspace(desc, save, save),
                16) + q8
@@ -443,13 +700,19 @@ class PoetxLinear:
     ``theta``, ``G``, ``dG``, ``dtheta`` are this layer's rows of it.  The inverse index
     maps come from the library, which rejects a perm_P or perm_R that is not a bijection.
     The permutations are merged into W0' once, at construction (and again by merge()).
+
+    The merged weight is kept in W0's type, in int8 (int8_weight) or in 4 bits with a scale per
+    int4_group (32, 64 or 128) columns.  dropout (a Dropout) acts on the layer's input while
+    ``training`` is true; step() moves its counter.
     """
 
     def __init__(self, W0, theta_P, theta_R, perm_P, perm_R, b: int, k: int, T: int,
                  save_activations: bool = True, int8_weight: bool = False, cnp=None,
-                 first_block: int = 0, ws=None):
+                 first_block: int = 0, ws=None, int4_group: int = 0, dropout=None):
         import torch
         self.m, self.n = W0.shape
+        if int8_weight and int4_group:
+            raise ValueError("the merged weight is either int8 or 4-bit")
         # the index maps are checked (bijections) and inverted by the library, on the host,
         # before any device work
         pP = np.ascontiguousarray(np.asarray(perm_P), dtype=np.int32)
@@ -467,7 +730,7 @@ class PoetxLinear:
         self.perm_P, self.inv_P = torch.as_tensor(pP, **i32), torch.as_tensor(iP, **i32)
         self.perm_R, self.inv_R = torch.as_tensor(pR, **i32), torch.as_tensor(iR, **i32)
         self.W0 = W0
-        self.W0p = None if int8_weight else torch.empty_like(W0)
+        self.W0p = None if int8_weight or int4_group else torch.empty_like(W0)
         if cnp is None:
             cnp = CnpBuffers(nblk, b, k, dev, W0.dtype if self.bf16 else None)
             first_block = 0
@@ -497,6 +760,16 @@ class PoetxLinear:
                 raise ValueError("the int8 base weight needs the bf16 layer")
             self.W0q = torch.empty((self.m, self.n), dtype=torch.int8, device=dev)
             self.scales = torch.empty((self.m,), dtype=torch.float32, device=dev)
+        # 4-bit merged weight: codes + group scales (bf16)
+        self.int4_group = int4_group
+        if int4_group:
+            if not self.bf16:
+                raise ValueError("the 4-bit base weight needs the bf16 layer")
+            qs, ss = q4_shapes(self.m, self.n, int4_group)
+            self.W0q = torch.empty(qs, dtype=torch.uint8, device=dev)
+            self.scales = torch.empty(ss, dtype=torch.bfloat16, device=dev)
+        self.dropout = dropout
+        self.training = True
         need = _layer_scratch_bytes(self.desc, self.save, int8_weight)
         if ws is None:
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -505,15 +778,28 @@ class PoetxLinear:
         self.ws = ws
         if int8_weight:  # the merged weight exists only as int8 codes (merge_perm_q8)
             self.W0p = None
+        if int4_group:
+            self.weight = linear_weight_q4(self.W0q, self.scales, int4_group)
+        elif int8_weight:
+            self.weight = linear_weight_q8(self.W0q, self.scales)
+        else:
+            self.weight = linear_weight_dense(self.W0p)
         self.merge()
+
+    def _drop(self):
+        """Descriptor of the active dropout, or None."""
+        return self.dropout.desc() if self.dropout is not None and self.training else None
 
     def G_ops(self):
         G = self.G_lp if self.bf16 else self.G
         return G[: self.nP], G[self.nP:]
 
     def merge(self, stream=None):
-        """W0' = Pi_R W0 Pi_P^T (and its int8 codes): once per set of permutations."""
-        if self.int8:
+        """W0' = Pi_R W0 Pi_P^T (or its int8 or 4-bit codes): once per set of permutations."""
+        if self.int4_group:
+            merge_perm_q4(self.W0, self.W0q, self.scales, self.perm_R, self.perm_P,
+                          self.int4_group, stream)
+        elif self.int8:
             merge_perm_q8(self.W0, self.W0q, self.scales, self.perm_R, self.perm_P, stream)
         else:
             merge_perm(self.W0, self.W0p, self.perm_R, self.perm_P, stream)
@@ -523,7 +809,11 @@ class PoetxLinear:
 
     def forward(self, x, y, stream=None):
         GP, GR = self.G_ops()
-        if self.int8:
+        drop = self._drop()
+        if self.int4_group or drop is not None:
+            linear_fwd_ex(self.desc, self.weight, drop, x, GP, GR, y, self.U, self.Wsave, self.ws,
+                          stream)
+        elif self.int8:
             linear_fwd_q8(self.desc, x, GP, GR, self.W0q, self.scales, y, self.U, self.Wsave,
                           self.ws, stream)
         else:
@@ -531,7 +821,11 @@ class PoetxLinear:
 
     def backward(self, x, dy, dx, accumulate=0, stream=None):
         GP, GR = self.G_ops()
-        if self.int8:
+        drop = self._drop()
+        if self.int4_group or drop is not None:
+            linear_bwd_ex(self.desc, self.weight, drop, x, dy, GP, GR, self.U, self.Wsave, dx,
+                          self.dG[: self.nP], self.dG[self.nP:], accumulate, self.ws, stream)
+        elif self.int8:
             linear_bwd_q8(self.desc, x, dy, GP, GR, self.W0q, self.scales, self.U, self.Wsave,
                           dx, self.dG[: self.nP], self.dG[self.nP:], accumulate, self.ws,
                           stream)
@@ -550,6 +844,8 @@ class PoetxLinear:
         self.forward(x, y, stream)
         self.backward(x, dy, dx, 0, stream)
         self.cnp_backward(stream)
+        if self.dropout is not None and self.training:
+            self.dropout.advance(stream)
 
 
 class PoetxLinearGroup:
@@ -557,11 +853,13 @@ class PoetxLinearGroup:
     backward each run as one call over all of their blocks, and whose layer calls share one
     scratch buffer (they run one after another on one stream).
 
-    specs: list of (W0, theta_P, theta_R, perm_P, perm_R) per linear.
+    specs: list of (W0, theta_P, theta_R, perm_P, perm_R) per linear.  int8_weight, int4_group:
+    the form of every linear's merged weight; dropout: of every linear's input, linear i at
+    site dropout.site + i with the shared step counter.
     """
 
     def __init__(self, specs, b: int, k: int, T: int, save_activations: bool = True,
-                 int8_weight: bool = False):
+                 int8_weight: bool = False, int4_group: int = 0, dropout=None):
         import torch
         _require_cuda()
         W0s = [sp[0] for sp in specs]
@@ -581,9 +879,19 @@ class PoetxLinearGroup:
             W0, tP, tR, pP, pR = sp
             self.layers.append(PoetxLinear(W0, tP, tR, pP, pR, b, k, T, save_activations,
                                            int8_weight, cnp=self.cnp, first_block=off,
-                                           ws=self.ws))
+                                           ws=self.ws, int4_group=int4_group,
+                                           dropout=None if dropout is None else
+                                           dropout.at_site(dropout.site + len(self.layers))))
             off += nb
+        self.dropout = dropout
+        self.training = True
         self.b, self.k, self.T = b, k, T
+
+    def train(self, mode: bool = True):
+        """Dropout on (mode) or off, in every linear."""
+        self.training = mode
+        for L in self.layers:
+            L.training = mode
 
     def merge(self, stream=None):
         for L in self.layers:
@@ -610,3 +918,5 @@ class PoetxLinearGroup:
         self.forward(xs, ys, stream)
         self.backward(xs, dys, dxs, 0, stream)
         self.cnp_backward(stream)
+        if self.dropout is not None and self.training:
+            self.dropout.advance(stream)
