@@ -38,6 +38,15 @@
 // reading the codes straight from global memory (less shared-memory traffic) and a 512 x 128
 // pair tile (half the conversions per FLOP, more shared-memory traffic) did not raise it.
 //
+// 4-bit merged weight (Q4 instantiation; format in q4_dev.cuh): the same roles with the tiles
+// loaded as 4-bit codes.  The weight is stored in runs of rows per 128-column block, so a tile
+// and its scales are two contiguous runs, fetched with untiled bulk copies.  Forward: one 8 KB
+// tile (128 rows x 128 columns) holds two K chunks, converted by two groups that share its slot;
+// backward: 4 KB tiles (64 rows x 128 columns), one per chunk.  Converting costs about 1.9
+// instructions a code (a mask, half a shift, half a subtraction and half a multiplication in
+// packed bf16, all exact for the quantiser's scales) against 2.8 for int8, and the smaller slots
+// leave room for a fifth operand stage.
+//
 // Every mbarrier wait is bounded (Params2::wait_ns): on a timeout the waiting role records
 // POETX_ERR_TIMEOUT in the device flag and leaves its loop; the CTAs then drain what they can
 // observe with short bounded waits, meet at a cluster barrier and free TMEM.
@@ -46,6 +55,7 @@
 #include <cudaTypedefs.h>
 
 #include "poetx_internal.h"
+#include "q4_dev.cuh"
 #include "umma_ptx.cuh"
 
 namespace poetx {
@@ -79,26 +89,35 @@ constexpr int kConvChunks = (kTileChunks + kGroupThreads - 1) / kGroupThreads;  
 // TMA fills; with the int8 weight A's stages are filled by TMA and B's by the converters, each
 // with barriers of its own, and four of each leave room for the staging slots), epilogue
 // warps, staging slots, threads and shared memory.
-template <bool Q8>
+// QB: bits of the stored weight's codes (0: bf16 weight, no conversion).
+template <int QB>
 struct PairCfg {
-  static constexpr int RA = Q8 ? 4 : 6;
-  static constexpr int RB = Q8 ? 4 : 6;
-  static constexpr int EPI = Q8 ? PAIR_Q8_EPI : 8;
-  static constexpr bool ld32 = Q8 && kConvWarps > 8;  // epilogue loads of 32 columns
-  static constexpr int SLOTS = Q8 ? 2 * kConvGroups : 0;
-  static constexpr int threads = 64 + 32 * EPI + (Q8 ? 32 + 32 * kConvWarps : 0);
-  // with the int8 weight and RA == RB one set of stage barriers serves both operands
-  static constexpr bool split = Q8 && RA != RB;
+  static constexpr bool conv = QB != 0;
+  static constexpr int RA = QB == 0 ? 6 : QB == 8 ? 4 : 5;
+  static constexpr int RB = RA;
+  static constexpr int EPI = conv ? PAIR_Q8_EPI : 8;
+  static constexpr bool ld32 = conv && kConvWarps > 8;  // epilogue loads of 32 columns
+  static constexpr int SLOTS = conv ? 2 * kConvGroups : 0;
+  // 8-bit: a tile of codes per slot; 4-bit: 4 slots of 8 KB + 1 KB of scales (forward) or 8 of
+  // 4 KB + 512 B (backward)
+  static constexpr int slot_total = QB == 8 ? SLOTS * kQ8Bytes : QB == 4 ? 8 * 4608 : 0;
+  static constexpr int threads = 64 + 32 * EPI + (conv ? 32 + 32 * kConvWarps : 0);
+  // with a converted weight and RA == RB one set of stage barriers serves both operands
+  static constexpr bool split = conv && RA != RB;
   static constexpr int nbar = 2 * RA + (split ? 2 * RB : 0) + 6 + 2 * SLOTS;
-  static constexpr int smem =
-      1024 + RA * kPairA + RB * kPairB + SLOTS * kQ8Bytes + EPI * 4096 + 512;
+  static constexpr int smem = 1024 + RA * kPairA + RB * kPairB + slot_total + EPI * 4096 + 512;
 };
-static_assert(PairCfg<false>::smem <= 227 * 1024 && PairCfg<true>::smem <= 227 * 1024,
+static_assert(PairCfg<0>::smem <= 227 * 1024 && PairCfg<8>::smem <= 227 * 1024 &&
+                  PairCfg<4>::smem <= 227 * 1024,
               "shared memory per CTA");
-static_assert(PairCfg<false>::nbar * 8 <= 512 && PairCfg<true>::nbar * 8 <= 512, "barriers");
+static_assert(PairCfg<0>::nbar * 8 <= 512 && PairCfg<8>::nbar * 8 <= 512 &&
+                  PairCfg<4>::nbar * 8 <= 512,
+              "barriers");
+static_assert(PairCfg<4>::slot_total % 1024 == 0, "epilogue staging alignment");
 // a group's waits on the converted-operand ring see consecutive phases
-static_assert(kConvGroups <= PairCfg<true>::RB, "converter groups");
-static_assert(PairCfg<true>::threads <= 1024, "threads");
+static_assert(kConvGroups <= PairCfg<8>::RB && kConvGroups <= PairCfg<4>::RB, "converter groups");
+static_assert(kConvGroups == 4, "the 4-bit tiles are shared by groups 2 p and 2 p + 1");
+static_assert(PairCfg<8>::threads <= 1024 && PairCfg<4>::threads <= 1024, "threads");
 constexpr uint32_t kPairTmemCols = 2 * kPairBN;
 
 #ifndef PAIR_GROUP_M
@@ -109,6 +128,9 @@ struct Params2 {
   int* err;
   unsigned long long wait_ns;
   const float* scales;  // Q8: scale of each row of the int8 weight
+  const uint8_t* codes4;      // Q4: codes and scales of the 4-bit weight
+  const uint16_t* scales4;
+  int rows4, sg4;             // its rows (m) and scales per row and block (128 / group)
   int group_m;          // tile raster: groups of group_m M-tiles swept over the N-tiles
 };
 
@@ -300,6 +322,35 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
                : "memory");
 }
 
+// untiled bulk copy of contiguous bytes into this CTA's shared memory
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Slot (and its use, whose parity the barriers count) of K chunk `it` of a CTA's flat sequence.
+// 8-bit, and 4-bit backward: group it % 4 has slots 2 g and 2 g + 1 in turn.  4-bit forward: a
+// tile holds chunks 2 j and 2 j + 1; tiles go to slots 2 p and 2 p + 1, p = j % 2, in turn, and
+// groups 2 p and 2 p + 1 read it.
+template <bool PAIRED>
+__device__ __forceinline__ int slot_of(int it, int& use) {
+  const int u = it / kConvGroups;
+  use = u >> 1;
+  return PAIRED ? 2 * ((it >> 1) & 1) + (u & 1) : 2 * (it % kConvGroups) + (u & 1);
+}
+
 template <bool B_MN>
 __device__ __forceinline__ uint32_t make_idesc_pair() {
   return (1u << 4)                              // D format: f32
@@ -311,26 +362,31 @@ __device__ __forceinline__ uint32_t make_idesc_pair() {
          | ((uint32_t)(256 >> 4) << 24);        // M = 256 (the pair)
 }
 
-// tmB: the bf16 B operand, or (Q8) the int8 weight W0q with 8 KB boxes and no swizzle
-template <bool B_MN, bool Q8>
-__global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
+// tmB: the bf16 B operand, or (Q8) the int8 weight W0q with 8 KB boxes and no swizzle (Q4:
+// unused)
+template <bool B_MN, int QB>
+__global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
     k_umma_gemm_pair(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmD, const Params2 p) {
-  using C = PairCfg<Q8>;
+  using C = PairCfg<QB>;
+  constexpr bool CONV = C::conv;
+  constexpr bool PAIRED = QB == 4 && !B_MN;  // two chunks per loaded tile
+  constexpr int kSlotBytes = QB == 8 ? kQ8Bytes : B_MN ? 4608 : 9216;
+  constexpr int kSlotCodes = QB == 8 ? kQ8Bytes : B_MN ? 4096 : 8192;
   constexpr int RA = C::RA, RB = C::RB, EPI = C::EPI;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t sA = base;                                   // RA x 16 KB
   const uint32_t sB = sA + RA * kPairA;                       // RB x 16 KB
-  const uint32_t sQ = sB + RB * kPairB;                       // Q8: slots x 8 KB
-  const uint32_t sEpi = sQ + C::SLOTS * kQ8Bytes;             // 1024-aligned staging tiles
+  const uint32_t sQ = sB + RB * kPairB;                       // slots of codes
+  const uint32_t sEpi = sQ + C::slot_total;                   // 1024-aligned staging tiles
   const uint32_t sBar = sEpi + EPI * 4096;
   // A ring (with the bf16 weight: the common ring of A and B)
   auto fullA = [&](int s) { return sBar + 8u * s; };
   auto emptyA = [&](int s) { return sBar + 8u * (RA + s); };
-  // Q8: ring of converted B operands (the A ring's barriers when the rings are equal)
+  // ring of converted B operands (the A ring's barriers when the rings are equal)
   auto fullB = [&](int s) { return C::split ? sBar + 8u * (2 * RA + s) : fullA(s); };
   auto emptyB = [&](int s) { return C::split ? sBar + 8u * (2 * RA + RB + s) : emptyA(s); };
   constexpr int X = 2 * RA + (C::split ? 2 * RB : 0);
@@ -354,10 +410,10 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
     for (int s = 0; s < RA; ++s) {
       // the leader's expect_tx (and the TMA bytes of both CTAs); with shared stage barriers
       // also one arrival from the owning converter group of each CTA
-      mbar_init(fullA(s), (Q8 && !C::split) ? 3 : 1);
+      mbar_init(fullA(s), (CONV && !C::split) ? 3 : 1);
       mbar_init(emptyA(s), 1);
     }
-    if (Q8) {
+    if (CONV) {
       if (C::split) {
         for (int s = 0; s < RB; ++s) {
           mbar_init(fullB(s), 2);  // the owning converter group of each CTA
@@ -366,7 +422,7 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
       }
       for (int j = 0; j < C::SLOTS; ++j) {
         mbar_init(q8full_bar(j), 1);
-        mbar_init(q8free_bar(j), 1);
+        mbar_init(q8free_bar(j), PAIRED ? 2 : 1);  // the groups that read the slot
       }
     }
     for (int a = 0; a < 2; ++a) {
@@ -376,7 +432,7 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
     mbar_init(drain_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+    if (QB != 4) prefetch_tmap(&tmB);
     prefetch_tmap(&tmD);
   }
   if (warp == 1) {
@@ -407,7 +463,7 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
         }
         const uint32_t fb = map_to_rank(fullA(s), 0);
         const int k = kc * kPairBK;
-        if (!Q8) {
+        if (!CONV) {
           if (leader) mbar_expect_tx(fullA(s), 2u * (kPairA + kPairB));
           tma_load_2d_pair(sA + s * kPairA, &tmA, k, m0, fb);
           const uint32_t b_dst = sB + s * kPairB;
@@ -445,9 +501,9 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairBN);
       for (int kc = 0; kc < p.total_kc; ++kc, ++it) {
         const int s = it % RA, r = it / RA;
-        const int sb = Q8 ? it % RB : s;
+        const int sb = CONV ? it % RB : s;
         // (converter arrivals come from both CTAs: cluster-scope acquire)
-        if (!(Q8 && !C::split ? mbar_wait_cluster(fullA(s), r & 1, p.err, p.wait_ns)
+        if (!(CONV && !C::split ? mbar_wait_cluster(fullA(s), r & 1, p.err, p.wait_ns)
                               : mbar_wait(fullA(s), r & 1, p.err, p.wait_ns)) ||
             (C::split && !mbar_wait_cluster(fullB(sb), (it / RB) & 1, p.err, p.wait_ns))) {
           ok = false;
@@ -472,7 +528,52 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
     // every MMA issued here completes before TMEM is released
     umma_commit_pair(drain_bar);
     mbar_drain_wait(drain_bar, 0);
-  } else if (Q8 && warp == 2 + EPI) {
+  } else if (QB == 4 && warp == 2 + EPI) {
+    // ------------------------------------------------------------ 4-bit tile loads
+    // Codes and scales of one tile: two contiguous runs, one barrier.  (A failed wait leaves
+    // loads in flight as in the int8 form below: they are drained before the CTA ends.)
+    if (lane == 0) {
+      constexpr int STEP = PAIRED ? 2 : 1;  // chunks per tile
+      const int total = ((p.num_items - cid + nclusters - 1) / nclusters) * p.total_kc;
+      int ir = 0, kc = 0, n0 = 0, last_ir = -1, it = 0;
+      bool ok = true;
+      for (; it < total; it += STEP) {
+        if (ir != last_ir) {
+          int tm, tn;
+          pair_tile(p, cid + ir * nclusters, tm, tn);
+          n0 = tn * kPairBN + (int)rank * (kPairBN / 2);
+          last_ir = ir;
+        }
+        int use;
+        const int slot = slot_of<PAIRED>(it, use);
+        if (!mbar_wait(q8free_bar(slot), (use & 1) ^ 1, p.err, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        const int k = kc * kPairBK;
+        // forward: rows n0 .. n0 + 127 of block k / 128; backward: rows k .. of block n0 / 128
+        const int64_t row = PAIRED ? (int64_t)(k >> 7) * p.rows4 + n0
+                                   : (int64_t)(n0 >> 7) * p.rows4 + k;
+        const uint32_t rows = PAIRED ? 128u : (uint32_t)min(64, p.K - k);
+        mbar_expect_tx(q8full_bar(slot), rows * (64u + 2u * (uint32_t)p.sg4));
+        const uint32_t dst = sQ + slot * kSlotBytes;
+        bulk_load(dst, p.codes4 + row * 64, rows * 64u, q8full_bar(slot));
+        bulk_load(dst + kSlotCodes, p.scales4 + row * p.sg4, rows * 2u * (uint32_t)p.sg4,
+                  q8full_bar(slot));
+        kc += STEP;
+        if (kc == p.total_kc) {
+          kc = 0;
+          ++ir;
+        }
+      }
+      if (!ok)
+        for (int j = (it > C::SLOTS ? it - C::SLOTS : 0); j < it; j += STEP) {
+          int use;
+          const int slot = slot_of<PAIRED>(j, use);
+          mbar_drain_wait(q8full_bar(slot), use & 1);
+        }
+    }
+  } else if (QB == 8 && warp == 2 + EPI) {
     // ------------------------------------------------------------ int8 tile loads
     // The CTA's K chunks form one flat sequence it = (item round) * total_kc + kc.  Chunk
     // it (turn u = it / G of group it % G) goes to slot 2 (it % G) + (u & 1) as soon as the
@@ -515,8 +616,8 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
         }
       }
     }
-  } else if (Q8 && warp > 2 + EPI) {
-    // ------------------------------------------------------------ int8 -> bf16 operands
+  } else if (CONV && warp > 2 + EPI) {
+    // ------------------------------------------------------------ codes -> bf16 operands
     // Group g takes chunks it = g + G u (u = 0, 1, ...): it waits for the chunk's int8 tile
     // (slot 2 g + (u & 1)) and for B stage it % RB to be free, converts, completes the stage with one
     // arrival per CTA on the leader's fullB barrier, and frees the slot.
@@ -546,7 +647,8 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
     bool ok = true;
     for (int u = 0; it < total; ++u) {
       const int k = kc * kPairBK;
-      if (!B_MN) {  // the scale follows the operand row n: fixed while the tile is
+      if (QB == 4) {  // (the scales come with the tile)
+      } else if (!B_MN) {  // the scale follows the operand row n: fixed while the tile is
         if (n0 != scale_n0) {
 #pragma unroll
           for (int jj = 0; jj < kConvChunks; ++jj) {
@@ -565,10 +667,11 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
           sc[jj] = (o < p.K && gt + kGroupThreads * jj < kTileChunks) ? __ldg(p.scales + o) : 0.f;
         }
       }
-      const int sb = it % RB, slot = 2 * grp + (u & 1);
+      int use;
+      const int sb = it % RB, slot = slot_of<PAIRED>(it, use);
       int got = 1;
       if (lane == 0) {
-        got = mbar_wait(q8full_bar(slot), (u >> 1) & 1, p.err, p.wait_ns) &&
+        got = mbar_wait(q8full_bar(slot), use & 1, p.err, p.wait_ns) &&
               mbar_wait(emptyB(sb), ((it / RB) & 1) ^ 1, p.err, p.wait_ns);
       }
       // every thread of the group takes the same branch (a failed wait of any warp)
@@ -577,12 +680,44 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
         break;
       }
       // both phases have completed: every lane acquires them (returns at once)
-      while (!mbar_try_wait(q8full_bar(slot), (u >> 1) & 1)) {
+      while (!mbar_try_wait(q8full_bar(slot), use & 1)) {
       }
       while (!mbar_try_wait(emptyB(sb), ((it / RB) & 1) ^ 1)) {
       }
-      const uint32_t src = sQ + slot * kQ8Bytes;
+      const uint32_t src = sQ + slot * kSlotBytes;
       const uint32_t dst = sB + sb * kPairB;
+      if (QB == 4) {
+        // 512 units of two code words (16 codes): row r of the tile, 16-byte chunk t, columns
+        // 64 h + 8 t .. and 64 h + 32 + 8 t ..: chunks t and 4 + t of the row's 64 columns in
+        // the operand (forward: row r of the stage, h the chunk's half of the tile; backward:
+        // row r of box h).  Odd rows store their second word first, so that 8 lanes (two rows)
+        // write 8 different bank groups.
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+          const uint32_t ch = (uint32_t)(gt + 64 * jj);
+          const uint32_t t = ch & 3u, r = (ch >> 2) & (B_MN ? 63u : 127u);
+          const uint32_t h = B_MN ? ch >> 8 : (uint32_t)it & 1u;
+          const uint2 wd = lds64(src + r * 64u + t * 16u + h * 8u);
+          const uint32_t sg = (uint32_t)p.sg4;
+          const uint32_t srow = src + kSlotCodes + r * sg * 2u;
+          const uint32_t s0 = lds_u16(srow + (((2u * h) * sg) >> 2) * 2u);
+          const uint32_t s1 = lds_u16(srow + (((2u * h + 1u) * sg) >> 2) * 2u);
+          const bool odd = (r & 1u) != 0;
+          const bool live = !B_MN || k + (int)r < p.K;  // rows past K: zero operands
+          const uint32_t row = dst + (B_MN ? h * 8192u : 0u) + r * 128u;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const bool second = (i == 1) != odd;
+            const uint32_t word = second ? wd.y : wd.x;
+            const uint32_t s2 = (second ? s1 : s0) * 0x10001u;
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = live ? bf2_mul(q4_pair(word, e), s2) : 0u;
+            const uint32_t c = ((second ? 4u : 0u) + t) ^ (r & 7u);
+            sts128(row + (c << 4), o[0], o[1], o[2], o[3]);
+          }
+        }
+      } else {
 #pragma unroll
       for (int jj = 0; jj < kConvChunks; ++jj) {
         const int ch = gt + kGroupThreads * jj;
@@ -606,6 +741,7 @@ __global__ void __launch_bounds__(PairCfg<Q8>::threads, 1)
         }
         sts128(row + (c0 << 4), o[0], o[1], o[2], o[3]);
         sts128(row + (c1 << 4), o[4], o[5], o[6], o[7]);
+      }
       }
       fence_async_smem();  // the generic-proxy stores, then the tensor core's reads
       named_sync(bar_id, kGroupThreads);  // the whole tile is written and the slot read
@@ -736,12 +872,12 @@ bool map2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool B_MN, bool Q8>
+template <bool B_MN, int QB>
 cudaError_t launch_pair_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
                           const Params2& p, int grid, const char* family, cudaStream_t s) {
-  auto kern = k_umma_gemm_pair<B_MN, Q8>;
-  constexpr int threads = PairCfg<Q8>::threads;
-  constexpr int smem = PairCfg<Q8>::smem;
+  auto kern = k_umma_gemm_pair<B_MN, QB>;
+  constexpr int threads = PairCfg<QB>::threads;
+  constexpr int smem = PairCfg<QB>::smem;
   static bool attr_done[64] = {false};  // once per device, outside any stream capture
   int dev = 0;
   cudaGetDevice(&dev);
@@ -815,8 +951,8 @@ cudaError_t launch_umma_gemm_pair(const UmmaGemm& g, const char* family, cudaStr
   int grid = (num_sms() / 2) * 2;
   if (grid > 2 * p.num_items) grid = 2 * p.num_items;
   if (grid < 2) return cudaErrorInvalidValue;
-  return g.B.mn_major ? launch_pair_t<true, false>(ma, mb, md, p, grid, family, s)
-                      : launch_pair_t<false, false>(ma, mb, md, p, grid, family, s);
+  return g.B.mn_major ? launch_pair_t<true, 0>(ma, mb, md, p, grid, family, s)
+                      : launch_pair_t<false, 0>(ma, mb, md, p, grid, family, s);
 }
 
 cudaError_t launch_umma_gemm_pair_q8(const UmmaGemm& g, const PairQ8& q, const char* family,
@@ -853,8 +989,37 @@ cudaError_t launch_umma_gemm_pair_q8(const UmmaGemm& g, const PairQ8& q, const c
   int grid = (num_sms() / 2) * 2;
   if (grid > 2 * p.num_items) grid = 2 * p.num_items;
   if (grid < 2) return cudaErrorInvalidValue;
-  return b_mn ? launch_pair_t<true, true>(ma, mq, md, p, grid, family, s)
-              : launch_pair_t<false, true>(ma, mq, md, p, grid, family, s);
+  return b_mn ? launch_pair_t<true, 8>(ma, mq, md, p, grid, family, s)
+              : launch_pair_t<false, 8>(ma, mq, md, p, grid, family, s);
+}
+
+bool umma_pair_q4_eligible(const UmmaGemm& g, const Q4Weight& w) {
+  // whole 128-column blocks along K (forward), 16-byte runs of rows along K (backward)
+  return umma_pair_eligible(g) && (g.B.mn_major ? w.m % 8 == 0 : w.n % 128 == 0);
+}
+
+cudaError_t launch_umma_gemm_pair_q4(const UmmaGemm& g, const Q4Weight& w, const char* family,
+                                     cudaStream_t s) {
+  // g.B describes the bf16 weight that the codes stand for (its pointer is not read)
+  if (!umma_pair_q4_eligible(g, w) || !w.codes || !w.scales) return cudaErrorInvalidValue;
+  const bool b_mn = g.B.mn_major != 0;
+  if ((b_mn ? w.m : w.n) != g.K || (b_mn ? w.n : w.m) != g.N) return cudaErrorInvalidValue;
+  CUtensorMap ma, md;
+  if (!map2d(&ma, g.A.ptr, g.A.rows, g.A.cols, g.A.ld, 64u, (uint32_t)kPairBM, false))
+    return cudaErrorInvalidValue;
+  if (!map2d(&md, g.D, g.M, g.N, g.ldd, 64u, 32u, true)) return cudaErrorInvalidValue;
+  Params2 p;
+  cudaError_t e = pair_params(g, &p);
+  if (e != cudaSuccess) return e;
+  p.codes4 = w.codes;
+  p.scales4 = static_cast<const uint16_t*>(w.scales);
+  p.rows4 = w.m;
+  p.sg4 = 128 / w.group;
+  int grid = (num_sms() / 2) * 2;
+  if (grid > 2 * p.num_items) grid = 2 * p.num_items;
+  if (grid < 2) return cudaErrorInvalidValue;
+  return b_mn ? launch_pair_t<true, 4>(ma, ma, md, p, grid, family, s)
+              : launch_pair_t<false, 4>(ma, ma, md, p, grid, family, s);
 }
 
 }  // namespace poetx

@@ -1049,8 +1049,7 @@ Q8Layout q8_layout(const poetx_linear_desc* d) {
 // W = V W0'^T (forward) or dV = dW W0' (backward) for either form of the weight.
 cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int m, bool forward,
                     cudaStream_t s) {
-  if (w.q4.codes) return launch_q4_product(w.q4, in, out, T, !forward, s);
-  if (!w.q) return bf16_w0(in, w.bf16, out, T, n, m, forward, s);
+  if (!w.q && !w.q4.codes) return bf16_w0(in, w.bf16, out, T, n, m, forward, s);
   // the GEMM as it reads the bf16 merged weight (B's pointer is not used)
   UmmaGemm g;
   UmmaOperand B;
@@ -1060,6 +1059,13 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
   g.M = T; g.N = forward ? m : n; g.K = forward ? n : m;
   g.batch = 1; g.out_f32 = 0;
   g.D = out; g.ldd = g.N;
+  if (w.q4.codes) {
+    // from 256 tokens on (and whole 256-column tiles) the tensor-core kernel converts the codes
+    // on chip; other calls take the few-token kernels, in tiles of tokens
+    if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4))
+      return launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
+    return launch_q4_product(w.q4, in, out, T, !forward, s);
+  }
   if (gemm_pairs_enabled() && umma_pair_eligible(g) && n % 16 == 0) {  // converted on chip
     PairQ8 q;
     q.q = w.q; q.ldq = n; q.scales = w.s;

@@ -300,6 +300,10 @@ struct PairQ8 {
 };
 cudaError_t launch_umma_gemm_pair_q8(const UmmaGemm& g, const PairQ8& q, const char* family,
                                      cudaStream_t s);
+// The CTA-pair GEMM with B from the 4-bit weight, each tile converted in shared memory.
+bool umma_pair_q4_eligible(const UmmaGemm& g, const Q4Weight& w);
+cudaError_t launch_umma_gemm_pair_q4(const UmmaGemm& g, const Q4Weight& w, const char* family,
+                                     cudaStream_t s);
 // ksplit the launcher would choose for the given problem (used to size scratch).
 int umma_choose_ksplit(int M, int N, int K, int batch);
 

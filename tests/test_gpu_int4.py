@@ -335,7 +335,7 @@ def test_layer_equals_the_bf16_layer_on_the_dequantised_weight(P, T):
     P.linear_fwd(L.desc, x, GP, GR, W, y0, U, Ws, ws)
     P.linear_bwd(L.desc, x, dy, GP, GR, W, U, Ws, dx0, dGP, dGR, 0, ws)
     assert torch.equal(L.U, U)  # gathered bit for bit in either form
-    if False and T >= 256:  # the same tensor-core kernel on the same operands
+    if T >= 256:  # the same tensor-core kernel on the same operands
         assert torch.equal(y, y0) and torch.equal(dx, dx0)
         assert torch.equal(L.dG[: L.nP], dGP) and torch.equal(L.dG[L.nP:], dGR)
     else:
