@@ -124,265 +124,414 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------------------
-// y[t, i] = sum_j W[i, j] x[t, j], few tokens.  One CTA: 16 rows of W, 8 NT tokens; the K blocks
-// are dealt to the 8 warps.  Lane (g, t) loads chunk t of rows g and g + 8 (1 KB a warp and
-// block, contiguous), which is its A fragment of 8 MMAs once the nibbles are bf16 integers;
-// the integers are multiplied exactly, and the group's sum is scaled in fp32.
+// y[t, i] = sum_j W[i, j] x[t, j], up to 8 tokens.  One CTA: 16 rows of W; the K blocks are
+// dealt to the 8 warps.  Lane (g, t) loads chunk t of rows g and g + 8 (1 KB a warp and block,
+// contiguous), which is its A fragment of 8 MMAs once the nibbles are bf16 integers; the
+// integers are multiplied exactly, and the group's sum is scaled in fp32.  U blocks' loads are
+// in flight at a time.
 constexpr int kRowWarps = 8;
 
-template <int NT, int GS>
+template <int GS, int U>
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_q4_rows(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
               const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y, int T, int m,
               int n) {
-  __shared__ float red[kRowWarps][NT * 8][17];
+  __shared__ float red[kRowWarps][8][17];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int row0 = blockIdx.x * 16, tok0 = blockIdx.y * (8 * NT);
+  const int row0 = blockIdx.x * 16;
   const int ra = min(row0 + g, m - 1), rb = min(row0 + g + 8, m - 1);
   const int nb = n / 128;
   constexpr int SG = 128 / GS;  // scales per row and block
-  float acc[NT][4];
-#pragma unroll
-  for (int a = 0; a < NT; ++a)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[a][c] = 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool tok_on = g < T;
+  const uint16_t* sc16 = reinterpret_cast<const uint16_t*>(scales);
 
-  for (int kb = warp; kb < nb; kb += kRowWarps) {
-    const int64_t base = (int64_t)kb * m;
-    const uint4 ca = __ldg(reinterpret_cast<const uint4*>(codes + (base + ra) * 64) + t);
-    const uint4 cb = __ldg(reinterpret_cast<const uint4*>(codes + (base + rb) * 64) + t);
-    float sa[SG], sb[SG];
+  for (int kb0 = warp; kb0 < nb; kb0 += kRowWarps * U) {
+    uint4 ca[U], cb[U], xv[U][4];
+    uint16_t sa[U][SG], sb[U][SG];
 #pragma unroll
-    for (int h = 0; h < SG; ++h) {
-      sa[h] = __bfloat162float(scales[(base + ra) * SG + h]);
-      sb[h] = __bfloat162float(scales[(base + rb) * SG + h]);
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + u * kRowWarps;
+      const bool on = kb < nb;
+      const int64_t base = (int64_t)(on ? kb : kb0) * m;
+      // blocks past the end: codes 8 (q = 0) and scale 0
+      ca[u] = cb[u] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      if (on) {
+        ca[u] = __ldg(reinterpret_cast<const uint4*>(codes + (base + ra) * 64) + t);
+        cb[u] = __ldg(reinterpret_cast<const uint4*>(codes + (base + rb) * 64) + t);
+      }
+#pragma unroll
+      for (int h = 0; h < SG; ++h) {
+        sa[u][h] = on ? __ldg(sc16 + (base + ra) * SG + h) : (uint16_t)0;
+        sb[u][h] = on ? __ldg(sc16 + (base + rb) * SG + h) : (uint16_t)0;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        xv[u][w] = make_uint4(0, 0, 0, 0);
+        if (tok_on && on)
+          xv[u][w] =
+              __ldg(reinterpret_cast<const uint4*>(x + (int64_t)g * n + kb * 128 + w * 32) + t);
+      }
     }
-    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
-    float part[NT][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w % (GS / 32) == 0) {
+    for (int u = 0; u < U; ++u) {
+      const uint32_t wa[4] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w};
+      const uint32_t wb[4] = {cb[u].x, cb[u].y, cb[u].z, cb[u].w};
+      float part[4];
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) part[a][c] = 0.f;
-      }
-      uint32_t pa[4], pb[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        pa[p] = q4_pair(wa[w], p);
-        pb[p] = q4_pair(wb[w], p);
-      }
-#pragma unroll
-      for (int a = 0; a < NT; ++a) {
-        const int tok = tok0 + a * 8 + g;
-        uint4 xv = make_uint4(0, 0, 0, 0);
-        if (tok < T)
-          xv = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)tok * n + kb * 128 + w * 32) + t);
-        mma16816(part[a], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
-        mma16816(part[a], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
-      }
-      if ((w + 1) % (GS / 32) == 0) {
-        const float fa = sa[w / (GS / 32)], fb = sb[w / (GS / 32)];
-#pragma unroll
-        for (int a = 0; a < NT; ++a) {
-          acc[a][0] = fmaf(fa, part[a][0], acc[a][0]);
-          acc[a][1] = fmaf(fa, part[a][1], acc[a][1]);
-          acc[a][2] = fmaf(fb, part[a][2], acc[a][2]);
-          acc[a][3] = fmaf(fb, part[a][3], acc[a][3]);
+      for (int w = 0; w < 4; ++w) {
+        if (w % (GS / 32) == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
+        mma16816(part, q4_pair(wa[w], 0), q4_pair(wb[w], 0), q4_pair(wa[w], 1),
+                 q4_pair(wb[w], 1), xv[u][w].x, xv[u][w].y);
+        mma16816(part, q4_pair(wa[w], 2), q4_pair(wb[w], 2), q4_pair(wa[w], 3),
+                 q4_pair(wb[w], 3), xv[u][w].z, xv[u][w].w);
+        if ((w + 1) % (GS / 32) == 0) {
+          const float fa = __uint_as_float((uint32_t)sa[u][w / (GS / 32)] << 16);
+          const float fb = __uint_as_float((uint32_t)sb[u][w / (GS / 32)] << 16);
+          acc[0] = fmaf(fa, part[0], acc[0]);
+          acc[1] = fmaf(fa, part[1], acc[1]);
+          acc[2] = fmaf(fb, part[2], acc[2]);
+          acc[3] = fmaf(fb, part[3], acc[3]);
         }
       }
     }
   }
-#pragma unroll
-  for (int a = 0; a < NT; ++a) {
-    red[warp][a * 8 + 2 * t][g] = acc[a][0];
-    red[warp][a * 8 + 2 * t + 1][g] = acc[a][1];
-    red[warp][a * 8 + 2 * t][g + 8] = acc[a][2];
-    red[warp][a * 8 + 2 * t + 1][g + 8] = acc[a][3];
-  }
+  red[warp][2 * t][g] = acc[0];
+  red[warp][2 * t + 1][g] = acc[1];
+  red[warp][2 * t][g + 8] = acc[2];
+  red[warp][2 * t + 1][g + 8] = acc[3];
   __syncthreads();
-  for (int o = threadIdx.x; o < NT * 8 * 16; o += 32 * kRowWarps) {
-    const int tok = o >> 4, r = o & 15;
+  if (threadIdx.x < 128) {
+    const int tok = threadIdx.x >> 4, r = threadIdx.x & 15;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) v += red[w][tok][r];  // fixed order
-    if (tok0 + tok < T && row0 + r < m)
-      y[(int64_t)(tok0 + tok) * m + row0 + r] = __float2bfloat16_rn(v);
+    if (tok < T && row0 + r < m) y[(int64_t)tok * m + row0 + r] = __float2bfloat16_rn(v);
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// dx[t, j] = sum_i W[i, j] dy[t, i], few tokens.  One CTA: 64 JW columns (JW code words a lane),
-// 8 NT tokens; the 16-row steps of its share of the rows are dealt to the 8 warps.  Lane (g, t)
-// loads words g of rows 4 t .. 4 t + 3; halves of two rows' words side by side give bf16
-// pairs along the rows, which the MMA sums over.  The scale changes along the summed index, so
-// it multiplies the bf16 integers (exact for scales of 5 significant bits, else rounded to
-// bf16 as in the tensor-core path).
-template <int NT, int JW, int GS>
-__global__ void __launch_bounds__(32 * kRowWarps)
-    k_q4_cols(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
-              const __nv_bfloat16* __restrict__ dy, __nv_bfloat16* __restrict__ dx, int T, int m,
-              int n, int steps_per_cta) {
-  extern __shared__ __align__(16) float redc[];  // [4][8 NT][64 JW]
-  constexpr int COLS = 64 * JW, TOK = 8 * NT;
-  constexpr int SG = 128 / GS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tok0 = blockIdx.z * TOK;
-  const int splits = gridDim.y;
-  const int L0 = blockIdx.x * (8 * JW) + g * JW;  // first code word of the lane in a row
-  const int blk = min(L0 >> 4, n / 128 - 1), wi0 = L0 & 15;
-  const int64_t base = (int64_t)blk * m;
-  const int nsteps = (m + 15) / 16;
-  const int s_first = blockIdx.y * steps_per_cta;
-  const int s_last = min(nsteps, s_first + steps_per_cta);
-  float acc[NT][JW][4][4];
-#pragma unroll
-  for (int a = 0; a < NT; ++a)
-#pragma unroll
-    for (int j = 0; j < JW; ++j)
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[a][j][p][c] = 0.f;
+// Products with 8 NT tokens a CTA, both directions.  Each CTA: an output tile of 128 rows of W
+// (forward) or 256 columns (transposed), 8 NT tokens, and its share of the summed axis in steps
+// of 128; the shares of a tile are a cluster, whose partial sums are added in rank order through
+// distributed shared memory.  Warps: 4 along the tile x 2 along the summed axis.  The
+// activations of a step pass through shared memory (cp.async, two stages); the codes go straight
+// to registers, one step ahead.  The scale multiplies the bf16 integers (exact for scales of 5
+// significant bits).
+constexpr int kTileThreads = 256;
 
-  for (int ks = s_first + warp; ks < s_last; ks += kRowWarps) {
-    const int i0 = ks * 16 + 4 * t;
-    uint32_t wd[4][JW];
-    uint16_t sc[4][JW];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = base + min(i0 + r, m - 1);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(codes + row * 64) + wi0;
-      if constexpr (JW == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-        wd[r][0] = v.x; wd[r][1] = v.y; wd[r][2] = v.z; wd[r][3] = v.w;
-      } else if constexpr (JW == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-        wd[r][0] = v.x; wd[r][1] = v.y;
-      } else {
-        wd[r][0] = __ldg(src);
-      }
-#pragma unroll
-      for (int j = 0; j < JW; ++j)
-        sc[r][j] = __ldg(reinterpret_cast<const uint16_t*>(scales) + row * SG +
-                         ((wi0 + j) & 3) / (GS / 32));
-    }
-    uint32_t b0[NT], b1[NT];
-#pragma unroll
-    for (int a = 0; a < NT; ++a) {
-      const int tok = tok0 + a * 8 + g;
-      uint16_t d[4] = {0, 0, 0, 0};
-      if (tok < T) {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(dy) + (int64_t)tok * m + i0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (i0 + r < m) d[r] = __ldg(src + r);
-      }
-      b0[a] = d[0] | ((uint32_t)d[1] << 16);
-      b1[a] = d[2] | ((uint32_t)d[3] << 16);
-    }
-#pragma unroll
-    for (int j = 0; j < JW; ++j) {
-      // rows past the end have zero dy; their clamped scale must not bring in a NaN of its own
-      const uint32_t s01 = sc[0][j] | ((uint32_t)sc[1][j] << 16);
-      const uint32_t s23 = sc[2][j] | ((uint32_t)sc[3][j] << 16);
-      const uint32_t lo01 = __byte_perm(wd[0][j], wd[1][j], 0x5410);
-      const uint32_t hi01 = __byte_perm(wd[0][j], wd[1][j], 0x7632);
-      const uint32_t lo23 = __byte_perm(wd[2][j], wd[3][j], 0x5410);
-      const uint32_t hi23 = __byte_perm(wd[2][j], wd[3][j], 0x7632);
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t a0 = bf2_mul(q4_pair(lo01, p), s01);
-        const uint32_t a1 = bf2_mul(q4_pair(hi01, p), s01);
-        const uint32_t a2 = bf2_mul(q4_pair(lo23, p), s23);
-        const uint32_t a3 = bf2_mul(q4_pair(hi23, p), s23);
-#pragma unroll
-        for (int a = 0; a < NT; ++a) mma16816(acc[a][j][p], a0, a1, a2, a3, b0[a], b1[a]);
-      }
-    }
-  }
-  // the 8 warps' sums, halves added in a fixed order; then the splits, through the cluster
-  auto at = [&](int slot, int tok, int col) -> float& {
-    return redc[((size_t)slot * TOK + tok) * COLS + col];
-  };
-  // lane's value (a, j, p, c): token a * 8 + 2 t + (c & 1), column 8 (g JW + j) + 2 p + (c >> 1)
-#pragma unroll
-  for (int half = 4; half >= 1; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int a = 0; a < NT; ++a)
-#pragma unroll
-        for (int j = 0; j < JW; ++j)
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              at(warp - half, a * 8 + 2 * t + (c & 1), 8 * (g * JW + j) + 2 * p + (c >> 1)) =
-                  acc[a][j][p][c];
-    }
-    __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int a = 0; a < NT; ++a)
-#pragma unroll
-        for (int j = 0; j < JW; ++j)
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              acc[a][j][p][c] +=
-                  at(warp, a * 8 + 2 * t + (c & 1), 8 * (g * JW + j) + 2 * p + (c >> 1));
-    }
-    __syncthreads();
-  }
-  if (warp == 0) {
-#pragma unroll
-    for (int a = 0; a < NT; ++a)
-#pragma unroll
-      for (int j = 0; j < JW; ++j)
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            at(0, a * 8 + 2 * t + (c & 1), 8 * (g * JW + j) + 2 * p + (c >> 1)) = acc[a][j][p][c];
-  }
-  // word L of the row holds columns 128 (L / 16) + 32 (L % 4) + 8 ((L / 4) % 4) ..
-  auto store = [&](int o, float v) {
-    const int tok = o / COLS, col = o - tok * COLS;
-    const int L = blockIdx.x * (8 * JW) + col / 8;
-    const int j = (L >> 4) * 128 + 32 * (L & 3) + 8 * ((L >> 2) & 3) + (col & 7);
-    if (tok0 + tok < T && (L >> 4) < n / 128)
-      dx[(int64_t)(tok0 + tok) * n + j] = __float2bfloat16_rn(v);
-  };
+// adds the two half-sums and the cluster's shares, and hands every (token, column) of the
+// COLS-wide tile to `store`.  buf: [TOK][COLS + 4] floats.
+template <int TOK, int COLS, typename Put, typename Store>
+__device__ __forceinline__ void tile_reduce(float* buf, bool upper, Put put, Store store) {
+  constexpr int LD = COLS + 4;
+  __syncthreads();  // the stages that share this memory are done
+  if (upper) put(buf, LD, false);
+  __syncthreads();
+  if (!upper) put(buf, LD, true);
+  const int splits = gridDim.z;
   if (splits == 1) {
     __syncthreads();
-    for (int o = threadIdx.x; o < TOK * COLS; o += 32 * kRowWarps) store(o, redc[o]);
+    for (int o = threadIdx.x; o < TOK * COLS; o += kTileThreads) {
+      const int tok = o / COLS, c = o - tok * COLS;
+      store(tok, c, buf[tok * LD + c]);
+    }
     return;
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
-  uint32_t rank;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const int per = TOK * COLS / splits;  // (splits divides 64)
-  const uint32_t local = (uint32_t)__cvta_generic_to_shared(redc);
-  for (int o = (int)rank * per + threadIdx.x; o < ((int)rank + 1) * per; o += 32 * kRowWarps) {
+  const uint32_t local = (uint32_t)__cvta_generic_to_shared(buf);
+  for (int o = (int)blockIdx.z * kTileThreads + threadIdx.x; o < TOK * COLS;
+       o += splits * kTileThreads) {
+    const int tok = o / COLS, c = o - tok * COLS;
     float v = 0.f;
     for (int q = 0; q < splits; ++q) {
       uint32_t addr;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(addr) : "r"(local + 4u * (uint32_t)o), "r"(q));
+                   : "=r"(addr) : "r"(local + 4u * (uint32_t)(tok * LD + c)), "r"(q));
       float f;
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
       v += f;
     }
-    store(o, v);
+    store(tok, c, v);
   }
   // no CTA leaves while another still reads its shared memory
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
+}
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+
+// a step of 128 values of 8 NT tokens into shared memory rows of LDB bytes; values past `len`
+// (and tokens past T) are zero
+template <int TOK, int LDB>
+__device__ __forceinline__ void stage_tokens(unsigned char* dst, const __nv_bfloat16* x, int tok0,
+                                             int T, int k0, int len, bool vec) {
+  if (vec) {  // rows of whole 16-byte vectors
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+#pragma unroll
+    for (int e0 = 0; e0 < TOK * 16; e0 += kTileThreads) {
+      const int e = e0 + threadIdx.x;
+      if (TOK * 16 % kTileThreads != 0 && e >= TOK * 16) break;
+      const int tok = e >> 4, c = (e & 15) * 8;
+      const bool on = tok0 + tok < T && k0 + c < len;
+      const __nv_bfloat16* src = on ? x + (int64_t)(tok0 + tok) * len + k0 + c : x;
+      cp_async16_zfill(d + tok * LDB + c * 2, src, on);
+    }
+  } else {
+    for (int e = threadIdx.x; e < TOK * 128; e += kTileThreads) {
+      const int tok = e >> 7, c = e & 127;
+      __nv_bfloat16 v = __ushort_as_bfloat16(0);
+      if (tok0 + tok < T && k0 + c < len) v = x[(int64_t)(tok0 + tok) * len + k0 + c];
+      *reinterpret_cast<__nv_bfloat16*>(dst + tok * LDB + c * 2) = v;
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+constexpr int tile_row_smem(int nt) {
+  const int stages = 2 * 2 * nt * 8 * 320, sums = nt * 8 * (128 + 4) * 4;
+  return stages > sums ? stages : sums;
+}
+constexpr int tile_col_smem(int nt) {
+  const int stages = 2 * nt * 8 * 288, sums = nt * 8 * (256 + 4) * 4;
+  return stages > sums ? stages : sums;
+}
+
+// forward: warp (rw, kw) takes rows 32 rw .. 32 rw + 31 of the tile and every second block
+template <int NT, int GS>
+__global__ void __launch_bounds__(kTileThreads, 2)
+    k_q4_tile_rows(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
+                   const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y, int T,
+                   int m, int n, int blocks_per_cta) {
+  extern __shared__ __align__(16) unsigned char tile_raw[];
+  constexpr int TOK = 8 * NT, LDB = 320, STAGE = TOK * LDB;
+  constexpr int SG = 128 / GS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rw = warp & 3, kw = warp >> 2;
+  const int row0 = blockIdx.x * 128 + rw * 32, tok0 = blockIdx.y * TOK;
+  const int nb = n / 128;
+  const int kb_first = blockIdx.z * blocks_per_cta;
+  const int kb_last = min(nb, kb_first + blocks_per_cta);
+  const int iters = (kb_last - kb_first + 1) / 2;
+  int row[4];  // rows g, g + 8, g + 16, g + 24 of the warp's 32
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row[i] = min(row0 + 8 * i + g, m - 1);
+  const uint16_t* sc16 = reinterpret_cast<const uint16_t*>(scales);
+  float acc[2][NT][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][a][c] = 0.f;
+  uint4 cd[4];
+  uint16_t sc[4][SG];
+  auto load_codes = [&](int kb) {
+    const bool on = kb < kb_last;
+    const int64_t base = (int64_t)(on ? kb : kb_first) * m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cd[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      if (on) cd[i] = __ldg(reinterpret_cast<const uint4*>(codes + (base + row[i]) * 64) + t);
+#pragma unroll
+      for (int h = 0; h < SG; ++h)
+        sc[i][h] = on ? __ldg(sc16 + (base + row[i]) * SG + h) : (uint16_t)0;
+    }
+  };
+  auto stage = [&](int it) {  // both blocks of iteration `it`
+    unsigned char* d = tile_raw + (it & 1) * 2 * STAGE;
+    const int k0 = (kb_first + 2 * it) * 128;
+    stage_tokens<TOK, LDB>(d, x, tok0, T, k0, n, true);
+    stage_tokens<TOK, LDB>(d + STAGE, x, tok0, T, k0 + 128, n, true);
+  };
+  if (iters > 0) {
+    stage(0);
+    load_codes(kb_first + kw);
+  }
+  for (int it = 0; it < iters; ++it) {
+    if (it + 1 < iters) stage(it + 1);
+    if (it + 1 < iters)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    uint4 cur[4];
+    uint32_t s2[4][SG];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cur[i] = cd[i];
+#pragma unroll
+      for (int h = 0; h < SG; ++h) s2[i][h] = (uint32_t)sc[i][h] * 0x10001u;
+    }
+    if (it + 1 < iters) load_codes(kb_first + 2 * (it + 1) + kw);
+    const unsigned char* xs = tile_raw + (it & 1) * 2 * STAGE + kw * STAGE;
+    // (a block past the share is left out whole: 0 times an infinity there would be a NaN)
+    const int words = kb_first + 2 * it + kw < kb_last ? 4 : 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w >= words) break;
+      uint32_t p[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t wd = w == 0 ? cur[i].x : w == 1 ? cur[i].y : w == 2 ? cur[i].z : cur[i].w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[i][e] = bf2_mul(q4_pair(wd, e), s2[i][w / (GS / 32)]);
+      }
+#pragma unroll
+      for (int a = 0; a < NT; ++a) {
+        const uint4 xv =
+            *reinterpret_cast<const uint4*>(xs + (a * 8 + g) * LDB + w * 64 + t * 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma16816(acc[i][a], p[2 * i][0], p[2 * i + 1][0], p[2 * i][1], p[2 * i + 1][1], xv.x,
+                   xv.y);
+          mma16816(acc[i][a], p[2 * i][2], p[2 * i + 1][2], p[2 * i][3], p[2 * i + 1][3], xv.z,
+                   xv.w);
+        }
+      }
+    }
+    __syncthreads();  // the stage may be refilled
+  }
+  auto put = [&](float* buf, int ld, bool add) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float* q = buf + (a * 8 + 2 * t + (c & 1)) * ld + rw * 32 + 16 * i + 8 * (c >> 1) + g;
+          *q = add ? acc[i][a][c] + *q : acc[i][a][c];
+        }
+  };
+  tile_reduce<TOK, 128>(reinterpret_cast<float*>(tile_raw), kw == 1, put,
+                        [&](int tok, int c, float v) {
+                          const int r = blockIdx.x * 128 + c;
+                          if (tok0 + tok < T && r < m)
+                            y[(int64_t)(tok0 + tok) * m + r] = __float2bfloat16_rn(v);
+                        });
+}
+
+// transposed: dx[t, j] = sum_i W[i, j] dy[t, i].  Warp (cw, kw) takes code words 8 cw .. 8 cw + 7
+// of the tile's 32 (64 columns) and half of the 128 rows of a step, 16 rows an MMA: lane (g, t)
+// loads word g of rows 4 t .. 4 t + 3; halves of two rows' words side by side give bf16 pairs
+// along the rows, which the MMA sums over.
+template <int NT, int GS>
+__global__ void __launch_bounds__(kTileThreads, NT <= 4 ? 2 : 1)
+    k_q4_tile_cols(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
+                   const __nv_bfloat16* __restrict__ dy, __nv_bfloat16* __restrict__ dx, int T,
+                   int m, int n, int steps_per_cta) {
+  extern __shared__ __align__(16) unsigned char tile_raw[];
+  constexpr int TOK = 8 * NT, LDB = 288, STAGE = TOK * LDB;
+  constexpr int SG = 128 / GS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int cw = warp & 3, kw = warp >> 2;
+  const int tok0 = blockIdx.y * TOK;
+  const int L = min((int)blockIdx.x * 32 + cw * 8 + g, n / 8 - 1);  // code word of the lane
+  const int blk = L >> 4, wi = L & 15;
+  const int64_t base = (int64_t)blk * m;
+  const uint32_t* c32 = reinterpret_cast<const uint32_t*>(codes) + base * 16 + wi;
+  const uint16_t* sc16 =
+      reinterpret_cast<const uint16_t*>(scales) + base * SG + (wi & 3) / (GS / 32);
+  const int nsteps = (m + 127) / 128;
+  const int s_first = blockIdx.z * steps_per_cta;
+  const int iters = max(0, min(nsteps, s_first + steps_per_cta) - s_first);
+  const bool vec = m % 8 == 0;
+  float acc[NT][4][4];
+#pragma unroll
+  for (int a = 0; a < NT; ++a)
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[a][p][c] = 0.f;
+  uint32_t cd[4][4];
+  uint16_t sc[4][4];
+  auto load_codes = [&](int it) {
+    const int i0 = (s_first + it) * 128 + kw * 64 + 4 * t;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // rows past the end: zero dy; the last row's word and scale again (its own group, so
+        // nothing enters that is not there already)
+        const int64_t row = min(i0 + 16 * q + r, m - 1);
+        cd[q][r] = __ldg(c32 + row * 16);
+        sc[q][r] = __ldg(sc16 + row * SG);
+      }
+  };
+  auto stage = [&](int it) {
+    stage_tokens<TOK, LDB>(tile_raw + (it & 1) * STAGE, dy, tok0, T, (s_first + it) * 128, m, vec);
+  };
+  if (iters > 0) {
+    stage(0);
+    load_codes(0);
+  }
+  for (int it = 0; it < iters; ++it) {
+    if (it + 1 < iters) {
+      stage(it + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    uint32_t cur[4][4], s01[4], s23[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) cur[q][r] = cd[q][r];
+      s01[q] = sc[q][0] | ((uint32_t)sc[q][1] << 16);
+      s23[q] = sc[q][2] | ((uint32_t)sc[q][3] << 16);
+    }
+    if (it + 1 < iters) load_codes(it + 1);
+    const unsigned char* xs = tile_raw + (it & 1) * STAGE + kw * 128 + t * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t lo01 = __byte_perm(cur[q][0], cur[q][1], 0x5410);
+      const uint32_t hi01 = __byte_perm(cur[q][0], cur[q][1], 0x7632);
+      const uint32_t lo23 = __byte_perm(cur[q][2], cur[q][3], 0x5410);
+      const uint32_t hi23 = __byte_perm(cur[q][2], cur[q][3], 0x7632);
+      uint2 b[NT];
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+        b[a] = *reinterpret_cast<const uint2*>(xs + (a * 8 + g) * LDB + q * 32);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t a0 = bf2_mul(q4_pair(lo01, p), s01[q]);
+        const uint32_t a1 = bf2_mul(q4_pair(hi01, p), s01[q]);
+        const uint32_t a2 = bf2_mul(q4_pair(lo23, p), s23[q]);
+        const uint32_t a3 = bf2_mul(q4_pair(hi23, p), s23[q]);
+#pragma unroll
+        for (int a = 0; a < NT; ++a) mma16816(acc[a][p], a0, a1, a2, a3, b[a].x, b[a].y);
+      }
+    }
+    __syncthreads();
+  }
+  // lane's value (a, p, c): token 8 a + 2 t + (c & 1), column 2 p + (c >> 1) of word 8 cw + g
+  auto put = [&](float* buf, int ld, bool add) {
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float* q = buf + (a * 8 + 2 * t + (c & 1)) * ld + 8 * (8 * cw + g) + 2 * p + (c >> 1);
+          *q = add ? acc[a][p][c] + *q : acc[a][p][c];
+        }
+  };
+  tile_reduce<TOK, 256>(reinterpret_cast<float*>(tile_raw), kw == 1, put,
+                        [&](int tok, int c, float v) {
+                          // word l of the row: columns 128 (l / 16) + 32 (l % 4) + 8 (l / 4 % 4)
+                          const int l = blockIdx.x * 32 + c / 8;
+                          const int j = (l >> 4) * 128 + 32 * (l & 3) + 8 * ((l >> 2) & 3) + (c & 7);
+                          if (tok0 + tok < T && l < n / 8)
+                            dx[(int64_t)(tok0 + tok) * n + j] = __float2bfloat16_rn(v);
+                        });
 }
 
 // ---------------------------------------------------------------------------------------
@@ -501,31 +650,24 @@ cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m
   return cudaGetLastError();
 }
 
-template <int NT, int GS>
-cudaError_t rows_t(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+template <int GS>
+cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  constexpr int U = 3;
   begin_launch("gemm_w0", s);
-  const cudaError_t e =
-      launch_pdl(k_q4_rows<NT, GS>, dim3((w.m + 15) / 16, (T + 8 * NT - 1) / (8 * NT)),
-                 dim3(32 * kRowWarps), 0, s, w.codes, static_cast<const __nv_bfloat16*>(w.scales),
-                 static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), T, w.m,
-                 w.n);
+  const cudaError_t e = launch_pdl(
+      k_q4_rows<GS, U>, dim3((w.m + 15) / 16), dim3(32 * kRowWarps), 0, s, w.codes,
+      static_cast<const __nv_bfloat16*>(w.scales), static_cast<const __nv_bfloat16*>(x),
+      static_cast<__nv_bfloat16*>(y), T, w.m, w.n);
   end_launch("gemm_w0", s);
   return e;
 }
-template <int GS>
-cudaError_t rows_gs(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  if (T <= 8) return rows_t<1, GS>(w, x, y, T, s);
-  if (T <= 16) return rows_t<2, GS>(w, x, y, T, s);
-  if (T <= 32) return rows_t<4, GS>(w, x, y, T, s);
-  return rows_t<8, GS>(w, x, y, T, s);
-}
 
-template <int NT, int JW, int GS>
-cudaError_t cols_t(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
-  auto kern = k_q4_cols<NT, JW, GS>;
-  constexpr int COLS = 64 * JW, TOK = 8 * NT;
-  constexpr int smem = 4 * TOK * COLS * 4;
-  static bool attr_done[64] = {false};
+// A tile kernel with its summed axis split over a cluster: as many shares (at most 8) as keep
+// the grid within one wave of `per_sm` CTAs an SM, and at least `min_steps` steps a share.
+template <typename Kern>
+cudaError_t launch_tiles(Kern kern, const Q4Weight& w, const void* x, void* y, int T, int tiles,
+                         int tok, int steps, int min_steps, int per_sm, int smem, bool* attr_done,
+                         cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
@@ -535,40 +677,57 @@ cudaError_t cols_t(const Q4Weight& w, const void* dy, void* dx, int T, cudaStrea
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  const int tiles = (w.n + COLS - 1) / COLS, ztiles = (T + TOK - 1) / TOK;
-  const int nsteps = (w.m + 15) / 16;
-  // split the rows over a cluster while the grid is below two CTAs per SM and every warp
-  // keeps a step
-  int splits = 1;
-  while (splits < 8 && tiles * ztiles * splits < 2 * num_sms() &&
-         nsteps >= 2 * splits * kRowWarps)
-    splits *= 2;
+  const int ttiles = (T + tok - 1) / tok;
+  int64_t splits = (int64_t)per_sm * num_sms() / ((int64_t)tiles * ttiles);
+  if (splits > steps / min_steps) splits = steps / min_steps;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  const int per = (int)((steps + splits - 1) / splits);
+  splits = (steps + per - 1) / per;  // every share has a step
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, splits, ztiles);
-  cfg.blockDim = dim3(32 * kRowWarps);
+  cfg.gridDim = dim3(tiles, ttiles, (unsigned)splits);
+  cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = splits;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = (unsigned)splits;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   begin_launch("gemm_w0", s);
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, kern, w.codes, static_cast<const __nv_bfloat16*>(w.scales),
-      static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx), T, w.m, w.n,
-      (nsteps + splits - 1) / splits);
+      static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), T, w.m, w.n, per);
   end_launch("gemm_w0", s);
   return e;
 }
+
+template <int NT, int GS>
+cudaError_t tile_rows_t(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  static bool attr_done[64] = {false};
+  return launch_tiles(k_q4_tile_rows<NT, GS>, w, x, y, T, (w.m + 127) / 128, 8 * NT, w.n / 128, 2,
+                      2, tile_row_smem(NT), attr_done, s);
+}
+template <int NT, int GS>
+cudaError_t tile_cols_t(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
+  static bool attr_done[64] = {false};
+  return launch_tiles(k_q4_tile_cols<NT, GS>, w, dy, dx, T, (w.n + 255) / 256, 8 * NT,
+                      (w.m + 127) / 128, 1, NT <= 4 ? 2 : 1, tile_col_smem(NT), attr_done, s);
+}
+template <int GS>
+cudaError_t rows_gs(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  if (T <= 8) return rows8<GS>(w, x, y, T, s);
+  if (T <= 16) return tile_rows_t<2, GS>(w, x, y, T, s);
+  if (T <= 32) return tile_rows_t<4, GS>(w, x, y, T, s);
+  return tile_rows_t<8, GS>(w, x, y, T, s);
+}
 template <int GS>
 cudaError_t cols_gs(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
-  if (T <= 8) return cols_t<1, 4, GS>(w, dy, dx, T, s);
-  if (T <= 16) return cols_t<2, 2, GS>(w, dy, dx, T, s);
-  if (T <= 32) return cols_t<4, 1, GS>(w, dy, dx, T, s);
-  return cols_t<8, 1, GS>(w, dy, dx, T, s);
+  if (T <= 8) return tile_cols_t<1, GS>(w, dy, dx, T, s);
+  if (T <= 16) return tile_cols_t<2, GS>(w, dy, dx, T, s);
+  if (T <= 32) return tile_cols_t<4, GS>(w, dy, dx, T, s);
+  return tile_cols_t<8, GS>(w, dy, dx, T, s);
 }
 
 template <int NT, bool GATHER>

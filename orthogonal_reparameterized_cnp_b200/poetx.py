@@ -165,8 +165,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # (the raw handle: building a Stream object costs 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -408,7 +408,7 @@ def _on_current_device(*tensors):
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:  # (-1 for a CPU tensor)
             raise ValueError(f"expected tensors on the current CUDA device ({dev}), got {t.device}")
 
 
@@ -422,10 +422,11 @@ def q4_shapes(m: int, n: int, group: int):
 def _check_q4(q, scales, m, n, group):
     import torch
     qs, ss = q4_shapes(m, n, group)
-    _require(tuple(q.shape) == qs and q.dtype == torch.uint8,
-             f"the codes of a {m} x {n} 4-bit weight are uint8 {qs}")
-    _require(tuple(scales.shape) == ss and scales.dtype == torch.bfloat16,
-             f"the scales of a {m} x {n} 4-bit weight with groups of {group} are bfloat16 {ss}")
+    if q.shape != qs or q.dtype is not torch.uint8:
+        raise ValueError(f"the codes of a {m} x {n} 4-bit weight are uint8 {qs}")
+    if scales.shape != ss or scales.dtype is not torch.bfloat16:
+        raise ValueError(f"the scales of a {m} x {n} 4-bit weight with groups of {group} are "
+                         f"bfloat16 {ss}")
 
 
 def _check_map(idx, n, what):
