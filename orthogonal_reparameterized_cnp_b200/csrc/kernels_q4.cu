@@ -101,11 +101,12 @@ __global__ void __launch_bounds__(kThreads)
                                 4 * (l & 3) + (l >> 2));
     const float s = __bfloat162float(scales[r * (128 / GS) + l / (GS / 8)]);
     float f[8];
+    uint32_t q[4];
+    q4_unpack(word, q);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const uint32_t q2 = q4_pair(word, p);
-      f[2 * p] = s * bf_lo(q2);
-      f[2 * p + 1] = s * bf_hi(q2);
+      f[2 * p] = s * (4.f * bf_lo(q[p]));
+      f[2 * p + 1] = s * (4.f * bf_hi(q[p]));
     }
     E* o = out + (int64_t)i * n + blk * 128 + 8 * l;
     if constexpr (sizeof(E) == 2) {
@@ -125,91 +126,319 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------------------------------
 // y[t, i] = sum_j W[i, j] x[t, j], up to 8 tokens.  One CTA: 16 rows of W; the K blocks are
-// dealt to the 8 warps.  Lane (g, t) loads chunk t of rows g and g + 8 (1 KB a warp and block,
+// dealt to its warps.  Lane (g, t) loads chunk t of rows g and g + 8 (1 KB a warp and block,
 // contiguous), which is its A fragment of 8 MMAs once the nibbles are bf16 integers; the
-// integers are multiplied exactly, and the group's sum is scaled in fp32.  U blocks' loads are
-// in flight at a time.
-constexpr int kRowWarps = 8;
+// integers are multiplied exactly, and the group's sum is scaled in fp32.  Lanes of tokens past
+// T read the last token's row: a column of the MMA is one token's alone, and theirs is not
+// stored.
+// Small CTAs (four warps) spread evenly over the SMs.  Each lane's codes of the next kRowD
+// blocks are on their way into its own slots of shared memory (cp.async; nothing is shared, so
+// nothing is synchronised).  Offsets count 16-byte chunks in 32 bits: one wide multiply-add an
+// address.
+//
+// Bound: codes and scales at HBM rate (5.6 us at 13824 x 5120); the conversion's masks on the
+// half-rate integer pipe come next (about 3 us there, overlapped in part).  Measured, T = 1, group
+// 128: 6.6 us at 5120 x 5120, 11.3 at 13824 x 5120, 13.6 at 5120 x 13824 (loads alone: 7.0 at
+// 13824 x 5120).  One load a block without the ring: 8.5, 16.4, 20.4; a persistent grid with
+// the ring in registers: 9.4, 15.4, 22.5 (320 row tiles do not divide evenly).
+constexpr int kRowD = 4;
 
-template <int GS, int U>
-__global__ void __launch_bounds__(32 * kRowWarps)
-    k_q4_rows(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
+// a row's scales in a block as one load
+template <int SG>
+struct RowScales;
+template <>
+struct RowScales<1> {
+  uint32_t v = 0;
+  __device__ __forceinline__ void load(const uint16_t* p, bool on) { ld_u16_if(v, p, on); }
+  __device__ __forceinline__ float at(int) const { return __uint_as_float(v << 16); }
+};
+template <>
+struct RowScales<2> {
+  uint32_t v = 0;
+  __device__ __forceinline__ void load(const uint16_t* p, bool on) { ld_u32_if(v, p, on); }
+  __device__ __forceinline__ float at(int h) const {
+    return __uint_as_float(h ? v & 0xffff0000u : v << 16);
+  }
+};
+template <>
+struct RowScales<4> {
+  uint2 v = {0, 0};
+  __device__ __forceinline__ void load(const uint16_t* p, bool on) { ld_u2_if(v, p, on); }
+  __device__ __forceinline__ float at(int h) const {
+    const uint32_t w = h & 2 ? v.y : v.x;
+    return __uint_as_float(h & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+
+template <int GS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
+    k_q4_rows(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
               const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y, int T, int m,
               int n) {
-  __shared__ float red[kRowWarps][8][17];
-  pdl_trigger();
-  pdl_wait();
+  constexpr int SG = 128 / GS, D = kRowD;  // SG: scales per row and block
+  extern __shared__ __align__(16) unsigned char row_ring[];
+  uint4 (*ring)[WARPS][64] = reinterpret_cast<uint4 (*)[WARPS][64]>(row_ring);  // [D]
+  __shared__ float red[WARPS][8][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int row0 = blockIdx.x * 16;
   const int ra = min(row0 + g, m - 1), rb = min(row0 + g + 8, m - 1);
-  const int nb = n / 128;
-  constexpr int SG = 128 / GS;  // scales per row and block
+  const int cnt = (n / 128 - warp + WARPS - 1) / WARPS;  // blocks warp, warp + 4, ...
+  const uint4* c16 = reinterpret_cast<const uint4*>(codes);
+  uint32_t oc = ((uint32_t)warp * (uint32_t)m + (uint32_t)ra) * 4u + (uint32_t)t;
+  uint32_t os = ((uint32_t)warp * (uint32_t)m + (uint32_t)ra) * SG;
+  const uint32_t dc = (uint32_t)(rb - ra) * 4u, ds = (uint32_t)(rb - ra) * SG;
+  const uint32_t step = (uint32_t)WARPS * (uint32_t)m;
+  const uint4* xp =
+      reinterpret_cast<const uint4*>(x + (int64_t)min(g, T - 1) * n) + warp * 16 + t;
+  RowScales<SG> sa[2], sb[2];
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(&ring[0][warp][lane]);
+  int left = cnt;  // blocks whose loads are to be issued
+  auto load = [&](uint32_t slot) {
+    if (left > 0) {  // (uniform; an empty group otherwise)
+      cp_async16_cg(slot, c16 + oc);
+      cp_async16_cg(slot + 512u, c16 + (oc + dc));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    --left;
+    oc += step * 4u;
+  };
+  auto load_scales = [&](int b, bool on) {
+    sa[b].load(scales + os, on);
+    sb[b].load(scales + (os + ds), on);
+    os += step * SG;
+  };
+  pdl_trigger();
+  pdl_wait();
+  constexpr uint32_t kSlot = WARPS * 1024u;  // bytes of a ring stage
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(slot0 + d * kSlot);
+  load_scales(0, cnt > 0);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const bool tok_on = g < T;
-  const uint16_t* sc16 = reinterpret_cast<const uint16_t*>(scales);
-
-  for (int kb0 = warp; kb0 < nb; kb0 += kRowWarps * U) {
-    uint4 ca[U], cb[U], xv[U][4];
-    uint16_t sa[U][SG], sb[U][SG];
+  uint32_t slot = slot0;
+  auto compute = [&](int b) {
+    uint4 xv[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * kRowWarps;
-      const bool on = kb < nb;
-      const int64_t base = (int64_t)(on ? kb : kb0) * m;
-      // blocks past the end: codes 8 (q = 0) and scale 0
-      ca[u] = cb[u] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-      if (on) {
-        ca[u] = __ldg(reinterpret_cast<const uint4*>(codes + (base + ra) * 64) + t);
-        cb[u] = __ldg(reinterpret_cast<const uint4*>(codes + (base + rb) * 64) + t);
+    for (int w = 0; w < 4; ++w) xv[w] = ld_u4(xp + w * 4);
+    xp += WARPS * 16;
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    const uint4 ca = lds_u4(slot), cb = lds_u4(slot + 512u);
+    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+    float part[4], odd[4];  // two chains of MMAs
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t qa[4], qb[4];
+      q4_unpack(wa[w], qa);
+      q4_unpack(wb[w], qb);
+      if (w % (GS / 32) == 0) {
+        mma16816_zero(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
+        mma16816_zero(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
+      } else {
+        mma16816(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
+        mma16816(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
       }
-#pragma unroll
-      for (int h = 0; h < SG; ++h) {
-        sa[u][h] = on ? __ldg(sc16 + (base + ra) * SG + h) : (uint16_t)0;
-        sb[u][h] = on ? __ldg(sc16 + (base + rb) * SG + h) : (uint16_t)0;
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        xv[u][w] = make_uint4(0, 0, 0, 0);
-        if (tok_on && on)
-          xv[u][w] =
-              __ldg(reinterpret_cast<const uint4*>(x + (int64_t)g * n + kb * 128 + w * 32) + t);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t wa[4] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w};
-      const uint32_t wb[4] = {cb[u].x, cb[u].y, cb[u].z, cb[u].w};
-      float part[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (w % (GS / 32) == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
-        mma16816(part, q4_pair(wa[w], 0), q4_pair(wb[w], 0), q4_pair(wa[w], 1),
-                 q4_pair(wb[w], 1), xv[u][w].x, xv[u][w].y);
-        mma16816(part, q4_pair(wa[w], 2), q4_pair(wb[w], 2), q4_pair(wa[w], 3),
-                 q4_pair(wb[w], 3), xv[u][w].z, xv[u][w].w);
-        if ((w + 1) % (GS / 32) == 0) {
-          const float fa = __uint_as_float((uint32_t)sa[u][w / (GS / 32)] << 16);
-          const float fb = __uint_as_float((uint32_t)sb[u][w / (GS / 32)] << 16);
-          acc[0] = fmaf(fa, part[0], acc[0]);
-          acc[1] = fmaf(fa, part[1], acc[1]);
-          acc[2] = fmaf(fb, part[2], acc[2]);
-          acc[3] = fmaf(fb, part[3], acc[3]);
-        }
+      if ((w + 1) % (GS / 32) == 0) {
+        const float a = sa[b].at(w / (GS / 32)), c = sb[b].at(w / (GS / 32));
+        acc[0] = fmaf(a, part[0] + odd[0], acc[0]);
+        acc[1] = fmaf(a, part[1] + odd[1], acc[1]);
+        acc[2] = fmaf(c, part[2] + odd[2], acc[2]);
+        acc[3] = fmaf(c, part[3] + odd[3], acc[3]);
       }
     }
+    load(slot);  // (the slot's codes are in registers)
+    slot = slot == slot0 + (D - 1) * kSlot ? slot0 : slot + kSlot;
+  };
+  int j = 0;
+  for (; j + 2 <= cnt; j += 2) {
+    load_scales(1, true);
+    compute(0);
+    load_scales(0, j + 2 < cnt);
+    compute(1);
   }
+  if (j < cnt) compute(0);
   red[warp][2 * t][g] = acc[0];
   red[warp][2 * t + 1][g] = acc[1];
   red[warp][2 * t][g + 8] = acc[2];
   red[warp][2 * t + 1][g + 8] = acc[3];
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int tok = threadIdx.x >> 4, r = threadIdx.x & 15;
+  const int tok = threadIdx.x >> 4, r = threadIdx.x & 15;
+  if (tok < min(T, 8) && row0 + r < m) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) v += red[w][tok][r];  // fixed order
-    if (tok < T && row0 + r < m) y[(int64_t)tok * m + row0 + r] = __float2bfloat16_rn(v);
+    for (int w = 0; w < WARPS; ++w) v += red[w][tok][r];  // fixed order
+    y[(int64_t)tok * m + row0 + r] = __float2bfloat16_rn(4.f * v);
   }
+}
+
+// ---------------------------------------------------------------------------------------
+// dx[t, j] = sum_i W[i, j] dy[t, i], up to 8 tokens.  One CTA: one block of 128 columns; its
+// share of the 16-row steps is dealt to 8 warps, and the shares of a block form a cluster.  Lane
+// (g, t) loads two words (chunk g / 2, half g % 2) of rows 4 t .. 4 t + 3; halves of two rows'
+// words side by side give bf16 pairs along the rows, which the MMA sums over.  The scale changes
+// along the summed index, so it multiplies the bf16 integers (exact for scales of 5 significant
+// bits).  Measured, T = 1, group 128: 8.1 us at 5120 x 5120, 15.1 at 13824 x 5120, 16.4 at 5120 x
+// 13824; with loads inside branches (waited for where the paths meet) 10.7, 20.9, 21.5; adding the
+// warps' sums in three halving rounds instead of one costs 1 us.
+constexpr int kColWarps = 8;
+constexpr int kColU = 3;  // steps in flight per warp
+
+// WHOLE: m % 16 == 0
+template <int GS, bool WHOLE>
+__global__ void __launch_bounds__(32 * kColWarps, 2)
+    k_q4_cols(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+              const __nv_bfloat16* __restrict__ dy, __nv_bfloat16* __restrict__ dx, int T, int m,
+              int n, int steps_per_cta) {
+  __shared__ __align__(16) float sums[kColWarps][8][132];
+  constexpr int SG = 128 / GS, U = kColU;
+  constexpr int NS = GS == 32 ? 2 : 1;  // scales per row for the lane's two words
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int blk = blockIdx.x;
+  const int nsteps = (m + 15) / 16;
+  const int s_first = blockIdx.y * steps_per_cta;
+  const int s_last = min(nsteps, s_first + steps_per_cta);
+  const int64_t base = (int64_t)blk * m;
+  // the warp's steps s_first + warp, s_first + warp + 8, ...: 16 rows, 4 of them the lane's
+  const int cnt = max(0, (s_last - s_first - warp + kColWarps - 1) / kColWarps);
+  const int i_first = (s_first + warp) * 16 + 4 * t;
+  const uint2* c8 = reinterpret_cast<const uint2*>(codes);
+  uint32_t oc = ((uint32_t)base + (uint32_t)i_first) * 8u + (uint32_t)g;  // 8 bytes x 8 a row
+  uint32_t os = ((uint32_t)base + (uint32_t)i_first) * SG +
+                (GS == 128 ? 0u : GS == 64 ? (uint32_t)(g & 1) : 2u * (uint32_t)(g & 1));
+  const uint16_t* dp = reinterpret_cast<const uint16_t*>(dy) + (int64_t)min(g, T - 1) * m + i_first;
+  int i0 = i_first;  // of the next load
+  float acc[2][4][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[j][p][c] = 0.f;
+  uint2 wd[U][4], dv[U];
+  uint32_t sc[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    dv[u] = make_uint2(0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      wd[u][r] = make_uint2(0, 0);
+      sc[u][r] = 0;
+    }
+  }
+  auto load = [&](int u, bool on) {
+    if (WHOLE) {
+      ld_u2_if(dv[u], dp, on);
+      const uint2* c = c8 + oc;
+      const uint16_t* q = scales + os;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        ld_u2_if(wd[u][r], c + 8 * r, on);
+        if (NS == 2)
+          ld_u32_if(sc[u][r], q + SG * r, on);
+        else
+          ld_u16_if(sc[u][r], q + SG * r, on);
+      }
+    } else if (on) {
+      // rows past the end have zero dy, and the last row's word and scale again (its own group,
+      // so nothing enters that is not there already)
+      uint32_t d[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        d[r] = i0 + r < m ? ld_u16(dp + r) : 0u;
+        const uint32_t back = (uint32_t)max(0, i0 + r - (m - 1));
+        ld_u2_if(wd[u][r], c8 + (oc + 8u * (uint32_t)r - 8u * back), true);
+        const uint16_t* q = scales + (os + SG * (uint32_t)r - SG * back);
+        sc[u][r] = NS == 2 ? ld_u32(q) : ld_u16(q);
+      }
+      dv[u] = make_uint2(d[0] | (d[1] << 16), d[2] | (d[3] << 16));
+    }
+    oc += kColWarps * 16 * 8;
+    os += kColWarps * 16 * SG;
+    dp += kColWarps * 16;
+    i0 += kColWarps * 16;
+  };
+  auto compute = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t sel = NS == 2 && j ? 0x7632u : 0x5410u;
+      const uint32_t s01 = __byte_perm(sc[u][0], sc[u][1], sel);
+      const uint32_t s23 = __byte_perm(sc[u][2], sc[u][3], sel);
+      const uint32_t w0 = j ? wd[u][0].y : wd[u][0].x, w1 = j ? wd[u][1].y : wd[u][1].x;
+      const uint32_t w2 = j ? wd[u][2].y : wd[u][2].x, w3 = j ? wd[u][3].y : wd[u][3].x;
+      const uint32_t lo01 = __byte_perm(w0, w1, 0x5410), hi01 = __byte_perm(w0, w1, 0x7632);
+      const uint32_t lo23 = __byte_perm(w2, w3, 0x5410), hi23 = __byte_perm(w2, w3, 0x7632);
+      uint32_t a0[4], a1[4], a2[4], a3[4];
+      q4_unpack(lo01, a0);
+      q4_unpack(hi01, a1);
+      q4_unpack(lo23, a2);
+      q4_unpack(hi23, a3);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        mma16816(acc[j][p], bf2_mul(a0[p], s01), bf2_mul(a1[p], s01), bf2_mul(a2[p], s23),
+                 bf2_mul(a3[p], s23), dv[u].x, dv[u].y);
+    }
+  };
+  pdl_trigger();
+  pdl_wait();
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, u < cnt);
+  int k = 0;
+  for (; k + U <= cnt; k += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      compute(u);
+      load(u, k + u + U < cnt);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (k + u < cnt) compute(u);
+  // lane's value (j, p, c): token 2 t + (c & 1), column 2 p + (c >> 1) of word (t' = g / 2,
+  // w = 2 (g % 2) + j), i.e. column 32 w + 8 t' + ...  The warps' sums are added in warp order.
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (2 * t + (c & 1) < T)
+          sums[warp][2 * t + (c & 1)]
+              [32 * (2 * (g & 1) + j) + 8 * (g >> 1) + 2 * p + (c >> 1)] = acc[j][p][c];
+  __syncthreads();
+  for (int o = threadIdx.x; o < T * 128; o += 32 * kColWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kColWarps; ++w) v += sums[w][o >> 7][o & 127];
+    sums[0][o >> 7][o & 127] = v;  // (this thread alone reads and writes the place)
+  }
+  const int splits = gridDim.y;
+  auto store = [&](int tok, int c, float v) {
+    dx[(int64_t)tok * n + blk * 128 + c] = __float2bfloat16_rn(4.f * v);
+  };
+  if (splits == 1) {
+    __syncthreads();
+    for (int o = threadIdx.x; o < T * 128; o += 32 * kColWarps)
+      store(o >> 7, o & 127, sums[0][o >> 7][o & 127]);
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+  const uint32_t local = (uint32_t)__cvta_generic_to_shared(&sums[0][0][0]);
+  for (int o = (int)blockIdx.y * 32 * kColWarps + threadIdx.x; o < T * 128;
+       o += splits * 32 * kColWarps) {
+    float v = 0.f;
+    for (int q = 0; q < splits; ++q) {
+      uint32_t addr;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(addr)
+                   : "r"(local + 4u * (uint32_t)((o >> 7) * 132 + (o & 127))), "r"(q));
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
+      v += f;
+    }
+    store(o >> 7, o & 127, v);
+  }
+  // no CTA leaves while another still reads its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------
@@ -381,8 +610,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t wd = w == 0 ? cur[i].x : w == 1 ? cur[i].y : w == 2 ? cur[i].z : cur[i].w;
+        q4_unpack(wd, p[i]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[i][e] = bf2_mul(q4_pair(wd, e), s2[i][w / (GS / 32)]);
+        for (int e = 0; e < 4; ++e) p[i][e] = bf2_mul(p[i][e], s2[i][w / (GS / 32)]);
       }
 #pragma unroll
       for (int a = 0; a < NT; ++a) {
@@ -414,7 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                         [&](int tok, int c, float v) {
                           const int r = blockIdx.x * 128 + c;
                           if (tok0 + tok < T && r < m)
-                            y[(int64_t)(tok0 + tok) * m + r] = __float2bfloat16_rn(v);
+                            y[(int64_t)(tok0 + tok) * m + r] = __float2bfloat16_rn(4.f * v);
                         });
 }
 
@@ -500,12 +730,15 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 4 ? 2 : 1)
 #pragma unroll
       for (int a = 0; a < NT; ++a)
         b[a] = *reinterpret_cast<const uint2*>(xs + (a * 8 + g) * LDB + q * 32);
+      uint32_t e0[4], e1[4], e2[4], e3[4];
+      q4_unpack(lo01, e0);
+      q4_unpack(hi01, e1);
+      q4_unpack(lo23, e2);
+      q4_unpack(hi23, e3);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t a0 = bf2_mul(q4_pair(lo01, p), s01[q]);
-        const uint32_t a1 = bf2_mul(q4_pair(hi01, p), s01[q]);
-        const uint32_t a2 = bf2_mul(q4_pair(lo23, p), s23[q]);
-        const uint32_t a3 = bf2_mul(q4_pair(hi23, p), s23[q]);
+        const uint32_t a0 = bf2_mul(e0[p], s01[q]), a1 = bf2_mul(e1[p], s01[q]);
+        const uint32_t a2 = bf2_mul(e2[p], s23[q]), a3 = bf2_mul(e3[p], s23[q]);
 #pragma unroll
         for (int a = 0; a < NT; ++a) mma16816(acc[a][p], a0, a1, a2, a3, b[a].x, b[a].y);
       }
@@ -530,7 +763,7 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 4 ? 2 : 1)
                           const int l = blockIdx.x * 32 + c / 8;
                           const int j = (l >> 4) * 128 + 32 * (l & 3) + 8 * ((l >> 2) & 3) + (c & 7);
                           if (tok0 + tok < T && l < n / 8)
-                            dx[(int64_t)(tok0 + tok) * n + j] = __float2bfloat16_rn(v);
+                            dx[(int64_t)(tok0 + tok) * n + j] = __float2bfloat16_rn(4.f * v);
                         });
 }
 
@@ -563,10 +796,10 @@ __global__ void __launch_bounds__(32 * kBdWarps)
     if (tok0 + tok < T) {
       unsigned c = (unsigned)(j * b + k);
       if (GATHER) {
-        c = (unsigned)__ldg(idx + c);
+        c = ld_u32(idx + c);
         c = c < (unsigned)width ? c : (unsigned)width - 1;
       }
-      v = in[(int64_t)(tok0 + tok) * width + c];
+      v = __ushort_as_bfloat16((uint16_t)ld_u16(in + (int64_t)(tok0 + tok) * width + c));
       if (GATHER && save && i0 == 0) save[(int64_t)(tok0 + tok) * width + j * b + k] = v;
     }
     xs[tok * ld + k] = v;
@@ -581,8 +814,8 @@ __global__ void __launch_bounds__(32 * kBdWarps)
   const __nv_bfloat16* gb = ga + 8 * (int64_t)b;
   const int kw = b / kBdWarps;  // 32, 64 or 128
   for (int k = warp * kw; k < (warp + 1) * kw; k += 32) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(ga + k) + t);
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(gb + k) + t);
+    const uint4 a = ld_u4(ga + k + 8 * t);
+    const uint4 c = ld_u4(gb + k + 8 * t);
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       const uint4 xv = *reinterpret_cast<const uint4*>(xs + (q * 8 + g) * ld + k + 8 * t);
@@ -606,7 +839,7 @@ __global__ void __launch_bounds__(32 * kBdWarps)
     for (int w = 0; w < kBdWarps; ++w) v += red[w][tok][r];
     unsigned c = (unsigned)(j * b + i0 + r);
     if (!GATHER) {
-      c = (unsigned)__ldg(idx + c);
+      c = ld_u32(idx + c);
       c = c < (unsigned)width ? c : (unsigned)width - 1;
     }
     out[(int64_t)(tok0 + tok) * width + c] = __float2bfloat16_rn(v);
@@ -650,14 +883,54 @@ cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m
   return cudaGetLastError();
 }
 
-template <int GS>
-cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  constexpr int U = 3;
+template <int GS, int WARPS>
+cudaError_t rows8_t(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  constexpr int smem = kRowD * WARPS * 1024;
   begin_launch("gemm_w0", s);
   const cudaError_t e = launch_pdl(
-      k_q4_rows<GS, U>, dim3((w.m + 15) / 16), dim3(32 * kRowWarps), 0, s, w.codes,
-      static_cast<const __nv_bfloat16*>(w.scales), static_cast<const __nv_bfloat16*>(x),
+      k_q4_rows<GS, WARPS>, dim3((w.m + 15) / 16), dim3(32 * WARPS), smem, s, w.codes,
+      static_cast<const uint16_t*>(w.scales), static_cast<const __nv_bfloat16*>(x),
       static_cast<__nv_bfloat16*>(y), T, w.m, w.n);
+  end_launch("gemm_w0", s);
+  return e;
+}
+template <int GS>
+cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  // eight warps share a row tile where four would leave fewer than 16 warps on an SM
+  const int tiles = (w.m + 15) / 16;
+  if (tiles < 4 * num_sms()) return rows8_t<GS, 8>(w, x, y, T, s);
+  return rows8_t<GS, 4>(w, x, y, T, s);
+}
+
+template <int GS>
+cudaError_t cols8(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
+  const int tiles = w.n / 128, nsteps = (w.m + 15) / 16;
+  // shares: a grid within one wave of two CTAs an SM with a seventh of the places to spare (a
+  // cluster needs all its places in one group of SMs; clusters of 7 pack worst).  5120 x 5120, T =
+  // 1: 21.8 us with 1 share, 10.7 with 3, 9.2 with 6, 13.0 with 8 (two waves).
+  int64_t splits = num_sms() * 17ll / (10ll * tiles);
+  if (splits == 7) splits = 6;
+  if (splits > nsteps / kColWarps) splits = nsteps / kColWarps;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  const int per = (int)((nsteps + splits - 1) / splits);
+  splits = (nsteps + per - 1) / per;  // every share has a step
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, (unsigned)splits);
+  cfg.blockDim = dim3(32 * kColWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)splits;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  begin_launch("gemm_w0", s);
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, w.m % 16 == 0 ? k_q4_cols<GS, true> : k_q4_cols<GS, false>, w.codes, static_cast<const uint16_t*>(w.scales),
+      static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx), T, w.m, w.n, per);
   end_launch("gemm_w0", s);
   return e;
 }
@@ -724,7 +997,7 @@ cudaError_t rows_gs(const Q4Weight& w, const void* x, void* y, int T, cudaStream
 }
 template <int GS>
 cudaError_t cols_gs(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
-  if (T <= 8) return tile_cols_t<1, GS>(w, dy, dx, T, s);
+  if (T <= 8) return cols8<GS>(w, dy, dx, T, s);
   if (T <= 16) return tile_cols_t<2, GS>(w, dy, dx, T, s);
   if (T <= 32) return tile_cols_t<4, GS>(w, dy, dx, T, s);
   return tile_cols_t<8, GS>(w, dy, dx, T, s);

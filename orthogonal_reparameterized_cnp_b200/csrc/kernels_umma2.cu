@@ -42,9 +42,9 @@
 // loaded as 4-bit codes.  The weight is stored in runs of rows per 128-column block, so a tile
 // and its scales are two contiguous runs, fetched with untiled bulk copies.  Forward: one 8 KB
 // tile (128 rows x 128 columns) holds two K chunks, converted by two groups that share its slot;
-// backward: 4 KB tiles (64 rows x 128 columns), one per chunk.  Converting costs about 1.9
-// instructions a code (a mask, half a shift, half a subtraction and half a multiplication in
-// packed bf16, all exact for the quantiser's scales) against 2.8 for int8, and the smaller slots
+// backward: 4 KB tiles (64 rows x 128 columns), one per chunk.  Converting costs about 1.7
+// instructions a code (q4_unpack and half a multiplication in packed bf16, all exact for the
+// quantiser's scales) against 2.8 for int8, and the smaller slots
 // leave room for a fifth operand stage.
 //
 // Every mbarrier wait is bounded (Params2::wait_ns): on a timeout the waiting role records
@@ -709,10 +709,12 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
           for (int i = 0; i < 2; ++i) {
             const bool second = (i == 1) != odd;
             const uint32_t word = second ? wd.y : wd.x;
-            const uint32_t s2 = (second ? s1 : s0) * 0x10001u;
-            uint32_t o[4];
+            // 4 s: the unpacked codes are (code - 8) / 4
+            const uint32_t s2 = bf2_mul((second ? s1 : s0) * 0x10001u, 0x40804080u);
+            uint32_t q[4], o[4];
+            q4_unpack(word, q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = live ? bf2_mul(q4_pair(word, e), s2) : 0u;
+            for (int e = 0; e < 4; ++e) o[e] = live ? bf2_mul(q[e], s2) : 0u;
             const uint32_t c = ((second ? 4u : 0u) + t) ^ (r & 7u);
             sts128(row + (c << 4), o[0], o[1], o[2], o[3]);
           }

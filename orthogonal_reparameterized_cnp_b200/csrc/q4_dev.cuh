@@ -7,7 +7,7 @@
 // are four 16-byte chunks t of four words w; word (t, w) holds columns 32 w + 8 t + e, e < 8,
 // as q + 8: column e sits at nibble e/2 + 4 (e % 2).  Chunk t is then what lane t of a
 // four-lane MMA fragment group needs of the block (8 columns of each 32-column group), and a
-// pair of columns (2p, 2p + 1) is the two 16-bit halves of (word >> 4p) & 0x000f000f.
+// pair of columns (2p, 2p + 1) is nibble p of the word's two 16-bit halves.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -16,14 +16,92 @@
 namespace poetx {
 namespace {
 
-// columns (2p, 2p + 1) of a code word as two bf16 integers q: 0x4300 | u is the bf16 128 + u
-// (one unit in the last place is 1), and subtracting 136 leaves q = u - 8 exactly
-__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int p) {
-  const uint32_t v = ((word >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-  const uint32_t off = 0x43084308u;  // 136, 136
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                             *reinterpret_cast<const __nv_bfloat162*>(&off));
-  return *reinterpret_cast<uint32_t*>(&r);
+// Loads that stay where they are written: after the wait of a kernel that was launched early
+// (__ldg may be moved ahead of it, and the read-only path may hold lines from before it).  The
+// predicate is the instruction's own, with no branch around it: a load inside a branch is waited
+// for where the paths meet, which undoes a prefetch.  Registers keep their values when `on` is
+// false.
+__device__ __forceinline__ void ld_u4_if(uint4& v, const void* p, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((int)on));
+}
+// (codes: each line is read once)
+__device__ __forceinline__ void ld_u4_stream_if(uint4& v, const void* p, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((int)on));
+}
+__device__ __forceinline__ void ld_u2_if(uint2& v, const void* p, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+      "@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
+      : "+r"(v.x), "+r"(v.y)
+      : "l"(p), "r"((int)on));
+}
+__device__ __forceinline__ void ld_u32_if(uint32_t& v, const void* p, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q ld.global.u32 %0, [%1];\n\t}"
+      : "+r"(v)
+      : "l"(p), "r"((int)on));
+}
+__device__ __forceinline__ void ld_u16_if(uint32_t& v, const void* p, bool on) {  // zero-extended
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q ld.global.u16 %0, [%1];\n\t}"
+      : "+r"(v)
+      : "l"(p), "r"((int)on));
+}
+__device__ __forceinline__ void cp_async16_cg(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_u4(const void* p) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  ld_u4_if(v, p, true);
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void* p) {
+  uint32_t v = 0;
+  ld_u32_if(v, p, true);
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u16(const void* p) {
+  uint32_t v = 0;
+  ld_u16_if(v, p, true);
+  return v;
+}
+
+// The 8 columns of a code word as four bf16 pairs (columns 2p, 2p + 1) of (code - 8) / 4,
+// exactly.  Even pairs sit in bits 0-3 of the halves: 0x4300 | u is the bf16 128 + u, and one
+// fused multiply-add gives (128 + u) / 4 - 34.  Odd pairs sit in bits 4-7: alone there, they are
+// the bf16 number u 2^-129 (exponent fields 0 and 1 share one spacing), and u 2^-129 2^127 - 2 is
+// the same (u - 8) / 4.  So a word costs one byte permutation, four masks and four
+// multiply-adds; the shifts of the direct way (3 more instructions on the half-rate integer
+// pipe) made the few-token products 1.2 times slower.  The factor 4 goes to a scale or a sum.
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void q4_unpack(uint32_t word, uint32_t (&q)[4]) {
+  const uint32_t hi = __byte_perm(word, 0, 0x4341);  // the halves' upper bytes
+  q[0] = bf2_fma((word & 0x000f000fu) | 0x43004300u, 0x3e803e80u, 0xc208c208u);
+  q[1] = bf2_fma(word & 0x00f000f0u, 0x7f007f00u, 0xc000c000u);
+  q[2] = bf2_fma((hi & 0x000f000fu) | 0x43004300u, 0x3e803e80u, 0xc208c208u);
+  q[3] = bf2_fma(hi & 0x00f000f0u, 0x7f007f00u, 0xc000c000u);
 }
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
   __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
@@ -36,11 +114,19 @@ __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 accumulation
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A B
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Scale of a group whose largest magnitude has the fp32 bits `amax_bits`: amax / 7 (IEEE
