@@ -22,9 +22,200 @@ __device__ __forceinline__ float q4_f32<uint16_t>(uint16_t v) {
   return __uint_as_float((uint32_t)v << 16);
 }
 
-// Codes and scales of W0[perm_R][:, perm_P] (NULL maps: identity).  One CTA per row: the source
-// row is staged in shared memory, thread c owns the 8 columns of code word c (16 words a
-// block), the group maximum is taken over the 4, 8 or 16 threads of a group by shuffles.
+// Codes and scales of W0[perm_R][:, perm_P] (NULL maps: identity).  Two rows at a time: they come
+// in with cp.async while the pair before them is quantised, and are then interleaved in shared
+// memory, so that one access gathers a column of both (bf16: 4 bytes, fp32: 8).  Thread t owns the
+// code words t, t + threads, .. (8 columns each) of every row, with their index map in registers
+// (16 bits a column); the group maximum is taken over the 4, 8 or 16 threads of a group by
+// shuffles, for bf16 both rows in one register.
+//
+// The code.  A bf16 w (8 bits) over a scale of 5 bits is a half or at least 2^-10 away from one,
+// so w inv rounded to multiples of 2^-11 (one fused multiply-add) is the half exactly or on the
+// right side of it, and adding 1.5 2^23 rounds to the nearest integer, ties to even: checked for
+// every mantissa of w and s.  An fp32 w can lie closer: t = w inv + 1.5 2^23 rounds at once, and
+// the residual w - q s sends the elements next to a half through the exact decision of q4_code.
+// Codes are put together as fp32 sums (16 u1 + u0 ...), which keeps the work on the multiply-add
+// pipe.
+template <typename E>
+struct Pair;  // a column of two rows
+template <>
+struct Pair<uint16_t> {
+  using T = uint32_t;
+  // the largest magnitudes of both rows, 16 bits each
+  uint32_t m = 0;
+  __device__ __forceinline__ void see(T v) { m = __vmaxu2(m, v & 0x7fff7fffu); }
+  __device__ __forceinline__ void meet(int o) { m = __vmaxu2(m, __shfl_xor_sync(~0u, m, o)); }
+  __device__ __forceinline__ uint32_t a() const { return m << 16; }
+  __device__ __forceinline__ uint32_t b() const { return m & 0xffff0000u; }
+  static __device__ __forceinline__ void split(T v, float& a, float& b) {
+    a = __uint_as_float(v << 16);
+    b = __uint_as_float(v & 0xffff0000u);
+  }
+};
+template <>
+struct Pair<uint32_t> {
+  using T = uint2;
+  uint32_t ma = 0, mb = 0;
+  __device__ __forceinline__ void see(T v) {
+    ma = max(ma, v.x & 0x7fffffffu);
+    mb = max(mb, v.y & 0x7fffffffu);
+  }
+  __device__ __forceinline__ void meet(int o) {
+    ma = max(ma, __shfl_xor_sync(~0u, ma, o));
+    mb = max(mb, __shfl_xor_sync(~0u, mb, o));
+  }
+  __device__ __forceinline__ uint32_t a() const { return ma; }
+  __device__ __forceinline__ uint32_t b() const { return mb; }
+  static __device__ __forceinline__ void split(T v, float& a, float& b) {
+    a = __uint_as_float(v.x);
+    b = __uint_as_float(v.y);
+  }
+};
+// row a's and row b's 16-byte vectors, columns interleaved
+__device__ __forceinline__ void put_pair(uint32_t* dst, const uint4& a, const uint4& b) {  // bf16
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  d[0] = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632),
+                    __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
+  d[1] = make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(a.z, b.z, 0x7632),
+                    __byte_perm(a.w, b.w, 0x5410), __byte_perm(a.w, b.w, 0x7632));
+}
+__device__ __forceinline__ void put_pair(uint2* dst, const uint4& a, const uint4& b) {  // fp32
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  d[0] = make_uint4(a.x, b.x, a.y, b.y);
+  d[1] = make_uint4(a.z, b.z, a.w, b.w);
+}
+
+// the code word of 8 columns with scale s (bits sb)
+template <bool BF16>
+__device__ __forceinline__ uint32_t q4_word(const float (&w)[8], uint32_t sb) {
+  float s = __uint_as_float(sb);
+  if (!(s > 0.f)) return 0x88888888u;  // zero or NaN scale
+  // tiny scales go through the exact decision with both sides times 2^100 (exact), so that 1 / s
+  // stays finite
+  const bool tiny = s < 0x1p-100f;
+  const float up = tiny ? 0x1p100f : 1.f;
+  s *= up;
+  float inv;  // (both uses below bear an error of some units in the last place)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float half = 0.5f * s, near = half * 0.9999f;
+  const float magic = 12582920.f;  // 1.5 2^23 + 8: t - 1.5 2^23 is q + 8
+  float u[8];
+  bool exact = tiny;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (BF16) {
+      u[e] = (fmaf(w[e], inv, 6144.f) + (magic - 6144.f)) - 12582912.f;
+    } else {
+      u[e] = fmaf(w[e], inv, magic) - 12582912.f;
+      const float r = fmaf(8.f - u[e], s, w[e]);
+      exact |= !(fabsf(r) < near);
+    }
+  }
+  if (exact) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = (float)(q4_code(w[e] * up, s, inv, half) + 8);
+  }
+  // nibble p of the lower half: columns 0, 2, 4, 6; of the upper half: 1, 3, 5, 7
+  const float lo = fmaf(u[6], 4096.f, fmaf(u[4], 256.f, fmaf(u[2], 16.f, u[0])));
+  const float hi = fmaf(u[7], 4096.f, fmaf(u[5], 256.f, fmaf(u[3], 16.f, u[1])));
+  return __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
+}
+
+template <typename E, int GS, int MAXW>
+__global__ void __launch_bounds__(512)
+    k_merge_q4_pairs(const E* __restrict__ W0, const int32_t* __restrict__ perm_R,
+                     const int32_t* __restrict__ perm_P, uint8_t* __restrict__ codes,
+                     __nv_bfloat16* __restrict__ scales, int m, int n) {
+  extern __shared__ __align__(16) unsigned char row_raw[];
+  using P = Pair<E>;
+  using T = typename P::T;
+  constexpr int V = 16 / sizeof(E);
+  T* pair = reinterpret_cast<T*>(row_raw);                        // [n]
+  const unsigned char* stage = row_raw + (size_t)n * sizeof(T);   // [2][n] elements
+  const uint32_t stage_s = (uint32_t)__cvta_generic_to_shared(stage);
+  const int threads = blockDim.x, tid = threadIdx.x;
+  const int words = n / 8, vecs = n / V;
+  uint32_t idx[MAXW][4];  // byte offset of a column in 4-byte columns, 16 bits (n <= 16384)
+#pragma unroll
+  for (int j = 0; j < MAXW; ++j) {
+    const int c = min(tid + j * threads, words - 1);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      unsigned c0 = 8u * c + e, c1 = c0 + 1;
+      if (perm_P) {
+        c0 = (unsigned)__ldg(perm_P + c0);
+        c1 = (unsigned)__ldg(perm_P + c1);
+      }
+      c0 = c0 < (unsigned)n ? c0 : (unsigned)n - 1;
+      c1 = c1 < (unsigned)n ? c1 : (unsigned)n - 1;
+      idx[j][e / 2] = (4u * c0) | (c1 << 18);
+    }
+  }
+  const int npair = (m + 1) / 2;
+  auto fetch = [&](int pr) {
+    if (pr < npair) {
+      const int i0 = 2 * pr, i1 = min(2 * pr + 1, m - 1);
+      unsigned s0 = perm_R ? (unsigned)__ldg(perm_R + i0) : (unsigned)i0;
+      unsigned s1 = perm_R ? (unsigned)__ldg(perm_R + i1) : (unsigned)i1;
+      s0 = s0 < (unsigned)m ? s0 : (unsigned)m - 1;  // keep the reads inside the matrix
+      s1 = s1 < (unsigned)m ? s1 : (unsigned)m - 1;
+      const uint4* a = reinterpret_cast<const uint4*>(W0 + (int64_t)s0 * n);
+      const uint4* b = reinterpret_cast<const uint4*>(W0 + (int64_t)s1 * n);
+      for (int v = tid; v < vecs; v += threads) {
+        cp_async16_cg(stage_s + 16u * v, a + v);
+        cp_async16_cg(stage_s + 16u * (vecs + v), b + v);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int pr = blockIdx.x;
+  fetch(pr);
+  const unsigned char* cols = row_raw;
+  for (; pr < npair; pr += gridDim.x) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // each thread interleaves the vectors it fetched itself (the gathers of the pair before
+    // ended at the barrier below)
+    for (int v = tid; v < vecs; v += threads)
+      put_pair(pair + v * V, lds_u4(stage_s + 16u * v), lds_u4(stage_s + 16u * (vecs + v)));
+    __syncthreads();
+    fetch(pr + gridDim.x);
+#pragma unroll
+    for (int j = 0; j < MAXW; ++j) {
+      const int c = tid + j * threads;
+      if (c - (tid & 31) >= words) break;  // (whole warps)
+      float a[8], b[8];
+      P most;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t off = (e & 1) ? idx[j][e / 2] >> 16 : idx[j][e / 2] & 0xffffu;
+        const T v = *reinterpret_cast<const T*>(cols + off * (sizeof(T) / 4));
+        most.see(v);
+        P::split(v, a[e], b[e]);
+      }
+#pragma unroll
+      for (int o = 1; o < GS / 8; o <<= 1) most.meet(o);
+      const uint32_t sa = q4_scale_bits(most.a()), sb = q4_scale_bits(most.b());
+      const uint32_t wa = q4_word<sizeof(E) == 2>(a, sa), wb = q4_word<sizeof(E) == 2>(b, sb);
+      if (c < words) {
+        const int blk = c >> 4, l = c & 15;  // columns 8 l: word w = l / 4 of chunk t = l % 4
+        const int64_t r = (int64_t)blk * m + 2 * pr;
+        const bool both = 2 * pr + 1 < m;
+        uint32_t* cw = reinterpret_cast<uint32_t*>(codes + r * 64) + 4 * (l & 3) + (l >> 2);
+        cw[0] = wa;
+        if (both) cw[16] = wb;
+        if ((l & (GS / 8 - 1)) == 0) {
+          uint16_t* sw = reinterpret_cast<uint16_t*>(scales) + r * (128 / GS) + l / (GS / 8);
+          sw[0] = (uint16_t)(sa >> 16);
+          if (both) sw[128 / GS] = (uint16_t)(sb >> 16);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Rows too wide for the pairs (index map or shared memory): one CTA per row; the source row is
+// staged in shared memory, thread c owns the 8 columns of code word c.
 template <typename E, int GS>
 __global__ void __launch_bounds__(kThreads)
     k_merge_q4(const E* __restrict__ W0, const int32_t* __restrict__ perm_R,
@@ -83,32 +274,31 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // out[i, j] = s q (fp32 product, rounded once to the output type; exact for the quantiser's
-// scales).  Thread per code word.
+// scales).  Thread per 16-byte chunk: four consecutive threads hold a row's block, and write it as
+// four runs of 32 columns.
 template <typename E, int GS>
 __global__ void __launch_bounds__(kThreads)
     k_dequant_q4(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
                  E* __restrict__ out, int m, int n) {
-  const int nb = n / 128;
-  const int64_t total = (int64_t)m * nb * 16;
-  for (int64_t v = blockIdx.x * (int64_t)kThreads + threadIdx.x; v < total;
-       v += (int64_t)gridDim.x * kThreads) {
-    // 16 consecutive threads take one row's block in column order
-    const int l = (int)(v & 15);
-    const int64_t rb = v >> 4;
-    const int i = (int)(rb / nb), blk = (int)(rb - (int64_t)i * nb);
-    const int64_t r = (int64_t)blk * m + i;
-    const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(codes + r * 64) +
-                                4 * (l & 3) + (l >> 2));
-    const float s = __bfloat162float(scales[r * (128 / GS) + l / (GS / 8)]);
-    float f[8];
+  const int64_t v = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+  const int blk = blockIdx.y, t = (int)(v & 3);
+  const int64_t i = v >> 2;
+  if (i >= m) return;
+  const int64_t r = (int64_t)blk * m + i;
+  const uint4 cd = __ldg(reinterpret_cast<const uint4*>(codes + r * 64) + t);
+  const uint32_t words[4] = {cd.x, cd.y, cd.z, cd.w};
+  E* o = out + i * n + blk * 128 + 8 * t;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float s = __bfloat162float(scales[r * (128 / GS) + w / (GS / 32)]);
     uint32_t q[4];
-    q4_unpack(word, q);
+    q4_unpack(words[w], q);
+    float f[8];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       f[2 * p] = s * (4.f * bf_lo(q[p]));
       f[2 * p + 1] = s * (4.f * bf_hi(q[p]));
     }
-    E* o = out + (int64_t)i * n + blk * 128 + 8 * l;
     if constexpr (sizeof(E) == 2) {
       uint32_t h[4];
 #pragma unroll
@@ -116,10 +306,10 @@ __global__ void __launch_bounds__(kThreads)
         const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * p], f[2 * p + 1]);
         h[p] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(o + 32 * w) = make_uint4(h[0], h[1], h[2], h[3]);
     } else {
-      reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      reinterpret_cast<float4*>(o + 32 * w)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(o + 32 * w)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
 }
@@ -846,9 +1036,44 @@ __global__ void __launch_bounds__(32 * kBdWarps)
   }
 }
 
+template <typename E, int GS, int MAXW>
+cudaError_t merge_pairs_t(const void* W0, const int32_t* pR, const int32_t* pP, uint8_t* codes,
+                          void* scales, int m, int n, cudaStream_t s) {
+  auto kern = k_merge_q4_pairs<E, GS, MAXW>;
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  const size_t smem = 4 * (size_t)n * sizeof(E);  // two rows as they come, and interleaved
+  const int threads = (n / 8 + MAXW * 32 - 1) / (MAXW * 32) * 32;
+  int per_sm = (int)((224 * 1024) / (smem + 1024));
+  const int by_threads = 1536 / threads;
+  per_sm = per_sm < 1 ? 1 : per_sm > by_threads ? by_threads : per_sm;
+  per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+  int grid = num_sms() * per_sm;
+  if (grid > (m + 1) / 2) grid = (m + 1) / 2;
+  begin_launch("quant", s);
+  kern<<<grid, threads, smem, s>>>(static_cast<const E*>(W0), pR, pP, codes,
+                                   static_cast<__nv_bfloat16*>(scales), m, n);
+  end_launch("quant", s);
+  return cudaGetLastError();
+}
+
 template <typename E, int GS>
 cudaError_t merge_t(const void* W0, const int32_t* pR, const int32_t* pP, uint8_t* codes,
                     void* scales, int m, int n, cudaStream_t s) {
+  // pairs of rows: at most 4 code words a thread (n <= 16384), two rows twice in shared memory
+  const int words = n / 8;
+  if (words <= 4 * 512 && 4 * (size_t)n * sizeof(E) <= 224 * 1024)
+    return words <= 512    ? merge_pairs_t<E, GS, 1>(W0, pR, pP, codes, scales, m, n, s)
+           : words <= 1024 ? merge_pairs_t<E, GS, 2>(W0, pR, pP, codes, scales, m, n, s)
+                           : merge_pairs_t<E, GS, 4>(W0, pR, pP, codes, scales, m, n, s);
   const size_t smem = (size_t)n * sizeof(E);
   if (smem > (size_t)kMaxRowBytes) return cudaErrorInvalidValue;
   static bool attr_done[64] = {false};
@@ -873,9 +1098,7 @@ cudaError_t merge_t(const void* W0, const int32_t* pR, const int32_t* pP, uint8_
 template <typename E, int GS>
 cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m, int n,
                       cudaStream_t s) {
-  const int64_t blocks = ((int64_t)m * (n / 8) + kThreads - 1) / kThreads;
-  int grid = num_sms() * 8;
-  if (grid > blocks) grid = (int)blocks;
+  const dim3 grid((unsigned)((4ll * m + kThreads - 1) / kThreads), (unsigned)(n / 128));
   begin_launch("quant", s);
   k_dequant_q4<E, GS><<<grid, kThreads, 0, s>>>(
       codes, static_cast<const __nv_bfloat16*>(scales), static_cast<E*>(out), m, n);

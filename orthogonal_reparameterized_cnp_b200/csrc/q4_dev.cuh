@@ -134,14 +134,21 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32
 // 3 in the code, s q is a bf16 number: no path of the library rounds the dequantised weight.
 // (amax / s <= 7 / (1 - 2^-5) < 7.5, so the largest value still rounds to code 7.)  A group
 // holding an infinity or a NaN gets the scale NaN.
+// The quotient: q0 = a c with c = 1/7 rounded, then q0 + (a - 7 q0) c in fused multiply-adds,
+// which is a / 7 correctly rounded (Markstein 1990; checked for every mantissa), except where the
+// residual could be subnormal.
 __device__ __forceinline__ uint32_t q4_scale_bits(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return 0x7fc00000u;
-  const uint32_t b = __float_as_uint(__fdiv_rn(__uint_as_float(amax_bits), 7.0f));
+  const float a = __uint_as_float(amax_bits), c = 0x1.24924ap-3f;
+  const float q0 = a * c;
+  float q = fmaf(fmaf(-7.f, q0, a), c, q0);
+  if (a < 0x1p-90f) q = __fdiv_rn(a, 7.f);
+  const uint32_t b = __float_as_uint(q);
   return (b + 0x3ffffu + ((b >> 19) & 1u)) & 0xfff80000u;
 }
 
-// q = the integer nearest to w / s (ties to even), in [-7, 7]; inv = 1 / s rounded.  w * inv is
-// within 2^-22 of w / s, so its rounding can only be off where w / s lies next to a half; the
+// q = the integer nearest to w / s (ties to even), in [-7, 7]; inv = 1 / s within two units in
+// the last place.  w * inv is within 2^-19 of w / s, so its rounding can only be off where w / s lies next to a half; the
 // residual w - q s is exact in fp32 (both are multiples of the finer unit and it is below s),
 // and it decides those cases.
 __device__ __forceinline__ int q4_code(float w, float s, float inv, float half_s) {
