@@ -36,12 +36,11 @@ __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
   return v;
 }
 
-template <typename E, int DROP>
+template <typename E>
 __global__ void __launch_bounds__(kGatherThreads)
     k_gather_rows_smem(const E* __restrict__ in, E* __restrict__ out,
                        const int32_t* __restrict__ row_idx, const int32_t* __restrict__ col_idx,
-                       int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs drop) {
-  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
+                       int rows, int cols, int64_t ld_in, int64_t ld_out) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   E* srow = reinterpret_cast<E*>(smem_raw);
   constexpr int V = 16 / sizeof(E);  // elements per 16-byte vector
@@ -51,15 +50,7 @@ __global__ void __launch_bounds__(kGatherThreads)
     sr = min(max(sr, 0), rows - 1);  // keep the read inside the matrix
     const E* src = in + (int64_t)sr * ld_in;
     const bool vin = (cols % V == 0) && ((reinterpret_cast<uintptr_t>(src) & 15) == 0);
-    if (DROP == kDropSource) {  // a thread per mask call, 8 columns
-      for (int c8 = threadIdx.x; c8 < (cols + 7) / 8; c8 += blockDim.x) {
-        const uint32_t keep = drop_bits(drop, drop_words(drop, dstep, (uint32_t)r, c8));
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (8 * c8 + e < cols)
-            srow[8 * c8 + e] = drop_one<E>(drop, (keep >> e) & 1u, src[8 * c8 + e]);
-      }
-    } else if (vin) {
+    if (vin) {
       const uint4* s4 = reinterpret_cast<const uint4*>(src);
       uint4* d4 = reinterpret_cast<uint4*>(srow);
       for (int i = threadIdx.x; i < cols / V; i += blockDim.x) d4[i] = ldg_stream(s4 + i);
@@ -69,18 +60,7 @@ __global__ void __launch_bounds__(kGatherThreads)
     __syncthreads();
     E* dst = out + (int64_t)r * ld_out;
     const bool vout = (cols % V == 0) && ((reinterpret_cast<uintptr_t>(dst) & 15) == 0);
-    if (DROP == kDropOutput) {
-      for (int c8 = threadIdx.x; c8 < (cols + 7) / 8; c8 += blockDim.x) {
-        const uint32_t keep = drop_bits(drop, drop_words(drop, dstep, (uint32_t)r, c8));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = 8 * c8 + e;
-          if (c >= cols) break;
-          unsigned ci = (unsigned)__ldg(col_idx + c);
-          dst[c] = drop_one<E>(drop, (keep >> e) & 1u, srow[ci < ucols ? ci : ucols - 1]);
-        }
-      }
-    } else if (vout) {
+    if (vout) {
       for (int c0 = threadIdx.x * V; c0 < cols; c0 += blockDim.x * V) {
         E v[V];
 #pragma unroll
@@ -121,13 +101,11 @@ __device__ __forceinline__ void cp_async_wait() {
 
 constexpr int kPipeThreads = 256;
 
-template <typename E, int MAXV, int DROP>
+template <typename E, int MAXV>
 __global__ void __launch_bounds__(kPipeThreads)
     k_gather_rows_pipe(const E* __restrict__ in, E* __restrict__ out,
                        const int32_t* __restrict__ row_idx, const int32_t* __restrict__ col_idx,
-                       int rows, int cols, int64_t ld_in, int64_t ld_out, int R,
-                       const DropArgs drop) {
-  const uint32_t dstep = DROP ? drop_step(drop) : 0u;
+                       int rows, int cols, int64_t ld_in, int64_t ld_out, int R) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   constexpr int V = 16 / sizeof(E);
   const int nvec = cols / V;                    // 16-byte vectors per row
@@ -186,23 +164,10 @@ __global__ void __launch_bounds__(kPipeThreads)
     if (next < nbatch) issue(next, buf[(it + 1) & 1]);
     cp_async_commit();
     cp_async_wait1();
-    const int r0 = batch * R;
-    const int nr = min(R, rows - r0);
-    if (DROP == kDropSource) {  // in place, each thread on the vectors it copied itself
-      E* b = buf[it & 1];
-      for (int rr = rr_first, vv = vv_first; rr < nr;) {
-        uint4* p = reinterpret_cast<uint4*>(b + (size_t)rr * row_elems + vv * V);
-        *p = drop_vec<sizeof(E)>(drop, dstep, (uint32_t)(r0 + rr), (uint32_t)(vv * V), *p);
-        rr += rr_step;
-        vv += vv_step;
-        if (vv >= nvec) {
-          vv -= nvec;
-          ++rr;
-        }
-      }
-    }
     __syncthreads();
     const E* src = buf[it & 1];
+    const int r0 = batch * R;
+    const int nr = min(R, rows - r0);
     for (int rr = 0; rr < nr; ++rr) {
       const E* srow = src + (size_t)rr * row_elems;
       E* drow = out + (int64_t)(r0 + rr) * ld_out;
@@ -215,11 +180,8 @@ __global__ void __launch_bounds__(kPipeThreads)
             v[e] = srow[idx[j][e / 2] & 0xFFFFu];
             v[e + 1] = srow[idx[j][e / 2] >> 16];
           }
-          uint4 o = *reinterpret_cast<const uint4*>(v);
-          if (DROP == kDropOutput)
-            o = drop_vec<sizeof(E)>(drop, dstep, (uint32_t)(r0 + rr),
-                                    (uint32_t)((threadIdx.x + j * kPipeThreads) * V), o);
-          *reinterpret_cast<uint4*>(drow + (threadIdx.x + j * kPipeThreads) * V) = o;
+          *reinterpret_cast<uint4*>(drow + (threadIdx.x + j * kPipeThreads) * V) =
+              *reinterpret_cast<const uint4*>(v);
         }
       }
     }
@@ -388,6 +350,230 @@ cudaError_t il8_launch(const void* in, void* out, const int32_t* row_idx, const 
   return e;
 }
 
+// Dropout fused with the map for rows of whole vectors: two rows at a time.  They come in with
+// cp.async while the pair before them is gathered, and are interleaved in shared memory (masked
+// on the way, kDropSource), so that one access gathers a column of both rows and half as many
+// accesses leave room for the generator's instructions.  Each thread's two generator calls (one a
+// row) run side by side.  Measured (source / output mask): 40 / 39 us at 8192 x
+// 5120 bf16 (floor 25.6 at the HBM copy rate; the map alone 34.6, dropout and map one after the
+// other 67), 54 / 53 us at 4096 x 13824.  With the masks in the row-batched pipeline: 54 / 47 and
+// 76 / 67.  Bound: the generator and selection (about 11 instructions a value) on top of the
+// gather's shared-memory accesses.
+constexpr int kPairThreads = 512;
+constexpr size_t kPairSmem = 224 * 1024;
+
+template <typename E, int MAXV, int DROP>
+__global__ void __launch_bounds__(kPairThreads, 2)
+    k_gather_pairs(const E* __restrict__ in, E* __restrict__ out,
+                   const int32_t* __restrict__ col_idx, int rows, int cols, const DropArgs drop) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  constexpr int V = 16 / sizeof(E);
+  constexpr int PB = 2 * sizeof(E);  // bytes of a column of the pair
+  const uint32_t dstep = drop_step(drop);
+  unsigned char* stage = smem_raw + (size_t)cols * PB;  // [2][cols]
+  const int threads = blockDim.x, tid = threadIdx.x;
+  const int nvec = cols / V;
+  const unsigned ucols = (unsigned)cols;
+  uint32_t idx[MAXV][V / 2];  // 4 x source column, 16 bits (cols <= 16384)
+#pragma unroll
+  for (int j = 0; j < MAXV; ++j) {
+    const int v = min(tid + j * threads, nvec - 1);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      unsigned c0 = (unsigned)__ldg(col_idx + v * V + e);
+      unsigned c1 = (unsigned)__ldg(col_idx + v * V + e + 1);
+      c0 = c0 < ucols ? c0 : ucols - 1;
+      c1 = c1 < ucols ? c1 : ucols - 1;
+      idx[j][e / 2] = (4u * c0) | (c1 << 18);
+    }
+  }
+  const int npair = (rows + 1) / 2;
+  auto fetch = [&](int pr) {
+    if (pr < npair) {
+      const E* a = in + (int64_t)(2 * pr) * cols;
+      const E* b = in + (int64_t)min(2 * pr + 1, rows - 1) * cols;
+      for (int v = tid; v < nvec; v += threads) {
+        cp_async16(stage + 16 * v, a + v * V);
+        cp_async16(stage + 16 * (nvec + v), b + v * V);
+      }
+    }
+    cp_async_commit();
+  };
+  int pr = blockIdx.x;
+  fetch(pr);
+  for (; pr < npair; pr += gridDim.x) {
+    const uint32_t r0 = 2 * (uint32_t)pr;
+    cp_async_wait<0>();
+    // each thread masks and interleaves the vectors it fetched itself
+    for (int v = tid; v < nvec; v += threads) {
+      uint4 a = *reinterpret_cast<const uint4*>(stage + 16 * v);
+      uint4 b = *reinterpret_cast<const uint4*>(stage + 16 * (nvec + v));
+      if (DROP == kDropSource) {
+        a = drop_vec<sizeof(E)>(drop, dstep, r0, (uint32_t)(v * V), a);
+        b = drop_vec<sizeof(E)>(drop, dstep, r0 + 1, (uint32_t)(v * V), b);
+      }
+      uint4* d = reinterpret_cast<uint4*>(smem_raw + (size_t)v * V * PB);
+      if constexpr (sizeof(E) == 2) {
+        d[0] = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632),
+                          __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
+        d[1] = make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(a.z, b.z, 0x7632),
+                          __byte_perm(a.w, b.w, 0x5410), __byte_perm(a.w, b.w, 0x7632));
+      } else {
+        d[0] = make_uint4(a.x, b.x, a.y, b.y);
+        d[1] = make_uint4(a.z, b.z, a.w, b.w);
+      }
+    }
+    __syncthreads();
+    fetch(pr + gridDim.x);
+#pragma unroll
+    for (int j = 0; j < MAXV; ++j) {
+      const int v = tid + j * threads;
+      if (v < nvec) {
+        uint32_t ra[4], rb[4];
+        if constexpr (sizeof(E) == 2) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(smem_raw + (idx[j][e] & 0xffffu));
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(smem_raw + (idx[j][e] >> 16));
+            ra[e] = __byte_perm(x, y, 0x5410);
+            rb[e] = __byte_perm(x, y, 0x7632);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t off = (e & 1) ? idx[j][e / 2] >> 16 : idx[j][e / 2] & 0xffffu;
+            const uint2 x = *reinterpret_cast<const uint2*>(smem_raw + 2u * off);
+            ra[e] = x.x;
+            rb[e] = x.y;
+          }
+        }
+        uint4 a = make_uint4(ra[0], ra[1], ra[2], ra[3]), b = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+        if (DROP == kDropOutput) {
+          a = drop_vec<sizeof(E)>(drop, dstep, r0, (uint32_t)(v * V), a);
+          b = drop_vec<sizeof(E)>(drop, dstep, r0 + 1, (uint32_t)(v * V), b);
+        }
+        E* o = out + (int64_t)r0 * cols + v * V;
+        *reinterpret_cast<uint4*>(o) = a;
+        if ((int)r0 + 1 < rows) *reinterpret_cast<uint4*>(o + cols) = b;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E, int MAXV, int DROP>
+cudaError_t pairs_launch(const void* in, void* out, const int32_t* col_idx, int rows, int cols,
+                         const DropArgs& drop, cudaStream_t s) {
+  auto kern = k_gather_pairs<E, MAXV, DROP>;
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  const size_t smem = 4 * (size_t)cols * sizeof(E);  // two rows as they come, and interleaved
+  const int nvec = cols / (16 / (int)sizeof(E));
+  const int threads = (nvec + MAXV * 32 - 1) / (MAXV * 32) * 32;
+  int per_sm = (int)(kPairSmem / (smem + 1024));
+  if (per_sm > 1536 / threads) per_sm = 1536 / threads;
+  per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+  int grid = num_sms() * per_sm;
+  if (grid > (rows + 1) / 2) grid = (rows + 1) / 2;
+  begin_launch("permute", s);
+  kern<<<grid, threads, smem, s>>>(static_cast<const E*>(in), static_cast<E*>(out), col_idx, rows,
+                                   cols, drop);
+  end_launch("permute", s);
+  return cudaGetLastError();
+}
+
+// The same for rows of any length and alignment: values come and go one at a time, and the mask
+// of the pair of rows is one byte a generator call in shared memory.
+constexpr int kPairAnyThreads = 256;
+template <typename E>
+size_t pairs_any_smem(int cols) {
+  return 2 * (size_t)cols * sizeof(E) + 2 * (((size_t)cols + 7) / 8);
+}
+
+template <typename E, int DROP>
+__global__ void __launch_bounds__(kPairAnyThreads)
+    k_gather_pairs_any(const E* __restrict__ in, E* __restrict__ out,
+                       const int32_t* __restrict__ col_idx, int rows, int cols,
+                       const DropArgs drop) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  const uint32_t dstep = drop_step(drop);
+  const int calls = (cols + 7) / 8;
+  E* pair = reinterpret_cast<E*>(smem_raw);  // [cols][2]
+  unsigned char* keep = smem_raw + 2 * (size_t)cols * sizeof(E);  // [2][calls]
+  const unsigned ucols = (unsigned)cols;
+  const int npair = (rows + 1) / 2;
+  for (int pr = blockIdx.x; pr < npair; pr += gridDim.x) {
+    const uint32_t r0 = 2 * (uint32_t)pr, r1 = min(r0 + 1, (uint32_t)rows - 1);
+    for (int c8 = threadIdx.x; c8 < calls; c8 += kPairAnyThreads) {
+      keep[c8] = (unsigned char)drop_bits(drop, drop_words(drop, dstep, r0, c8));
+      keep[calls + c8] = (unsigned char)drop_bits(drop, drop_words(drop, dstep, r1, c8));
+    }
+    const E* a = in + (int64_t)r0 * cols;
+    const E* b = in + (int64_t)r1 * cols;
+    if (DROP == kDropSource) __syncthreads();
+#pragma unroll 4
+    for (int c = threadIdx.x; c < cols; c += kPairAnyThreads) {
+      E va = a[c], vb = b[c];
+      if (DROP == kDropSource) {
+        va = drop_one<E>(drop, (keep[c >> 3] >> (c & 7)) & 1, va);
+        vb = drop_one<E>(drop, (keep[calls + (c >> 3)] >> (c & 7)) & 1, vb);
+      }
+      pair[2 * c] = va;
+      pair[2 * c + 1] = vb;
+    }
+    __syncthreads();
+    E* oa = out + (int64_t)r0 * cols;
+    E* ob = out + (int64_t)r1 * cols;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < cols; c += kPairAnyThreads) {
+      unsigned ci = (unsigned)__ldg(col_idx + c);
+      ci = ci < ucols ? ci : ucols - 1;
+      E va = pair[2 * ci], vb = pair[2 * ci + 1];
+      if (DROP == kDropOutput) {
+        va = drop_one<E>(drop, (keep[c >> 3] >> (c & 7)) & 1, va);
+        vb = drop_one<E>(drop, (keep[calls + (c >> 3)] >> (c & 7)) & 1, vb);
+      }
+      oa[c] = va;
+      if (r1 != r0) ob[c] = vb;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E, int DROP>
+cudaError_t pairs_any_launch(const void* in, void* out, const int32_t* col_idx, int rows, int cols,
+                             const DropArgs& drop, cudaStream_t s) {
+  auto kern = k_gather_pairs_any<E, DROP>;
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  const size_t smem = pairs_any_smem<E>(cols);
+  int per_sm = (int)(kPairSmem / (smem + 1024));
+  per_sm = per_sm < 1 ? 1 : per_sm > 6 ? 6 : per_sm;
+  int grid = num_sms() * per_sm;
+  if (grid > (rows + 1) / 2) grid = (rows + 1) / 2;
+  begin_launch("permute", s);
+  kern<<<grid, kPairAnyThreads, smem, s>>>(static_cast<const E*>(in), static_cast<E*>(out),
+                                           col_idx, rows, cols, drop);
+  end_launch("permute", s);
+  return cudaGetLastError();
+}
+
 // Rows too wide for shared memory: gather straight from global memory (L2 absorbs the
 // sector waste; only used beyond ~100k bf16 columns).
 template <typename E, int DROP>
@@ -414,10 +600,9 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <typename E, int MAXV, int DROP>
+template <typename E, int MAXV>
 cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const int32_t* col_idx,
-                        int rows, int cols, int64_t ld_in, int64_t ld_out, const DropArgs& drop,
-                        cudaStream_t s) {
+                        int rows, int cols, int64_t ld_in, int64_t ld_out, cudaStream_t s) {
   const size_t row_bytes = (size_t)cols * sizeof(E);
   // R rows per batch: ~32 KB per buffer, two buffers per CTA
   int R = (int)((32 * 1024) / row_bytes);
@@ -428,7 +613,7 @@ cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(k_gather_rows_pipe<E, MAXV, DROP>,
+    cudaError_t e = cudaFuncSetAttribute(k_gather_rows_pipe<E, MAXV>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
@@ -439,9 +624,9 @@ cudaError_t pipe_launch(const void* in, void* out, const int32_t* row_idx, const
   int grid = num_sms() * per_sm;
   if (grid > nbatch) grid = nbatch;
   begin_launch("permute", s);
-  k_gather_rows_pipe<E, MAXV, DROP><<<grid, kPipeThreads, smem, s>>>(
+  k_gather_rows_pipe<E, MAXV><<<grid, kPipeThreads, smem, s>>>(
       static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
-      ld_out, R, drop);
+      ld_out, R);
   end_launch("permute", s);
   return cudaGetLastError();
 }
@@ -464,23 +649,33 @@ cudaError_t gather_impl(const void* in, void* out, const int32_t* row_idx,
   // interleaved forms that fit there)
   if (sizeof(E) == 2 && vec_ok && cols < 8 * kIlThreads && il_smem(4, cols) <= kIlMaxSmem)
     return il8_launch<1, 4, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
-  if (vec_ok && cols <= 65535 && nvec <= 8 * kPipeThreads && 2 * row_bytes <= 96 * 1024) {
+  if constexpr (DROP != kDropNone) {
+    if (vec_ok && cols <= 16384 && 8 * (size_t)cols * sizeof(E) / 2 <= kPairSmem) {
+      const int need = (nvec + kPairThreads - 1) / kPairThreads;
+      if (need <= 1) return pairs_launch<E, 1, DROP>(in, out, col_idx, rows, cols, drop, s);
+      if (need <= 2) return pairs_launch<E, 2, DROP>(in, out, col_idx, rows, cols, drop, s);
+      if (need <= 4) return pairs_launch<E, 4, DROP>(in, out, col_idx, rows, cols, drop, s);
+      if constexpr (sizeof(E) == 4)  // (at most 2048 vectors in a row of 16384 bf16)
+        return pairs_launch<E, 8, DROP>(in, out, col_idx, rows, cols, drop, s);
+    }
+  } else if (vec_ok && cols <= 65535 && nvec <= 8 * kPipeThreads && 2 * row_bytes <= 96 * 1024) {
     const int need = (nvec + kPipeThreads - 1) / kPipeThreads;
-    if (need <= 1)
-      return pipe_launch<E, 1, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
-    if (need <= 2)
-      return pipe_launch<E, 2, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
-    if (need <= 4)
-      return pipe_launch<E, 4, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
-    return pipe_launch<E, 8, DROP>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, drop, s);
+    if (need <= 1) return pipe_launch<E, 1>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    if (need <= 2) return pipe_launch<E, 2>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    if (need <= 4) return pipe_launch<E, 4>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
+    return pipe_launch<E, 8>(in, out, row_idx, col_idx, rows, cols, ld_in, ld_out, s);
   }
+  if constexpr (DROP != kDropNone) {
+    const size_t smem = pairs_any_smem<E>(cols);
+    if (smem <= kPairSmem) return pairs_any_launch<E, DROP>(in, out, col_idx, rows, cols, drop, s);
+  } else
   if (row_bytes <= (size_t)kMaxSmemRowBytes) {
     static bool attr_set[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) dev = 0;
     if (!attr_set[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(k_gather_rows_smem<E, DROP>,
+      cudaError_t e = cudaFuncSetAttribute(k_gather_rows_smem<E>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMaxSmemRowBytes);
       if (e != cudaSuccess) return e;
@@ -491,19 +686,19 @@ cudaError_t gather_impl(const void* in, void* out, const int32_t* row_idx,
     int grid = sms * per_sm;
     if (grid > rows) grid = rows;
     begin_launch("permute", s);
-    k_gather_rows_smem<E, DROP><<<grid, kGatherThreads, row_bytes, s>>>(
+    k_gather_rows_smem<E><<<grid, kGatherThreads, row_bytes, s>>>(
         static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
-        ld_out, drop);
+        ld_out);
     end_launch("permute", s);
-  } else {
-    int grid = sms * 8;
-    if (grid > rows) grid = rows;
-    begin_launch("permute", s);
-    k_gather_rows_direct<E, DROP><<<grid, 256, 0, s>>>(
-        static_cast<const E*>(in), static_cast<E*>(out), row_idx, col_idx, rows, cols, ld_in,
-        ld_out, drop);
-    end_launch("permute", s);
+    return cudaGetLastError();
   }
+  int grid = sms * 8;
+  if (grid > rows) grid = rows;
+  begin_launch("permute", s);
+  k_gather_rows_direct<E, DROP><<<grid, 256, 0, s>>>(static_cast<const E*>(in),
+                                                     static_cast<E*>(out), row_idx, col_idx, rows,
+                                                     cols, ld_in, ld_out, drop);
+  end_launch("permute", s);
   return cudaGetLastError();
 }
 

@@ -17,23 +17,31 @@ namespace poetx {
 
 // kernel-side form of poetx_dropout_desc
 struct DropArgs {
-  uint32_t k0, k1;      // seed
+  uint32_t rk0[10], rk1[10];  // round keys (the seed, advanced)
   uint32_t row0, site;
   uint32_t thr_hi;      // thr << 16
   float scale;          // 65536 / (65536 - thr)
   const unsigned long long* step;  // device counter, or nullptr for step 0
 };
 
+inline void drop_keys(DropArgs* d, uint64_t seed) {
+  for (uint32_t i = 0; i < 10; ++i) {
+    d->rk0[i] = (uint32_t)seed + i * 0x9E3779B9u;
+    d->rk1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+  }
+}
+
 namespace {
 
+// (the round keys are kernel parameters: operands of the exclusive-ors as they stand)
 __device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
-                                          uint32_t k0, uint32_t k1) {
+                                          const DropArgs& d) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ (k0 + (uint32_t)i * 0x9E3779B9u);
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ d.rk0[i];
     c1 = (uint32_t)p1;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ (k1 + (uint32_t)i * 0xBB67AE85u);
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ d.rk1[i];
     c3 = (uint32_t)p0;
   }
   return make_uint4(c0, c1, c2, c3);
@@ -44,7 +52,7 @@ __device__ __forceinline__ uint32_t drop_step(const DropArgs& d) {
 }
 __device__ __forceinline__ uint4 drop_words(const DropArgs& d, uint32_t step, uint32_t row,
                                             uint32_t col8) {
-  return philox10(col8, d.row0 + row, d.site, step, d.k0, d.k1);
+  return philox10(col8, d.row0 + row, d.site, step, d);
 }
 // bit l set: column 8 * col8 + l is kept
 __device__ __forceinline__ uint32_t drop_bits(const DropArgs& d, const uint4& w) {

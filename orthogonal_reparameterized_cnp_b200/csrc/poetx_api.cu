@@ -1468,8 +1468,7 @@ int drop_args(const poetx_dropout_desc* drop, int64_t rows, DropArgs* a, bool* o
   if (reinterpret_cast<uintptr_t>(drop->step) & 7)
     return fail(POETX_ERR_ALIGN, "dropout step counter must be 8-byte aligned");
   const uint32_t thr = (uint32_t)(drop->p * 65536.0 + 0.5);
-  a->k0 = (uint32_t)drop->seed;
-  a->k1 = (uint32_t)(drop->seed >> 32);
+  drop_keys(a, drop->seed);
   a->row0 = drop->row0;
   a->site = drop->site;
   a->thr_hi = thr << 16;

@@ -45,7 +45,7 @@ def _same(a, b):
 
 
 SHAPES = [(1, 1), (1, 5), (3, 8), (7, 33), (2, 247), (2, 248), (2, 249), (5, 1000), (129, 2048),
-          (33, 5003), (1, 65537), (1000, 3)]
+          (33, 5003), (1, 65537), (1000, 3), (3, 16384)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -89,7 +89,9 @@ def test_dropout_limits_in_place_and_tails(P, dt):
 # rows beyond shared memory (direct)
 GATHERS = [("bf16", 9, 256), ("bf16", 21, 2040), ("bf16", 17, 2048), ("bf16", 5, 13824),
            ("bf16", 6, 333), ("bf16", 2, 110000), ("bf16", 1, 8), ("f32", 9, 256),
-           ("f32", 6, 5120), ("f32", 7, 1023), ("f32", 2, 60000), ("f32", 3, 20000)]
+           ("f32", 6, 5120), ("f32", 7, 1023), ("f32", 2, 60000), ("f32", 3, 20000),
+          ("f32", 3, 14000), ("bf16", 3, 16384), ("bf16", 3, 16392), ("bf16", 3, 4101),
+          ("f32", 1, 1)]
 
 
 @pytest.mark.parametrize("dt,rows,cols", GATHERS)
