@@ -911,6 +911,11 @@ cudaError_t launch_pair_t(const CUtensorMap& ma, const CUtensorMap& mb, const CU
 
 }  // namespace
 
+bool umma_load_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld,
+                   uint32_t box_cols, uint32_t box_rows) {
+  return map2d(map, ptr, rows, cols, ld, box_cols, box_rows, false);
+}
+
 bool umma_pair_eligible(const UmmaGemm& g) {
   return g.batch == 1 && g.ksplit <= 1 && !g.A.mn_major && !g.out_f32 && g.side_rows == 0 &&
          g.N % kPairBN == 0 && g.M >= 256 && g.K >= kPairBK && g.ldd == g.N &&

@@ -1,0 +1,491 @@
+// Products with the 4-bit weight for some tens to hundreds of tokens (format in q4_dev.cuh), on
+// tcgen05 with the weight as the M operand:
+//
+//   forward      D[i, t] = sum_j W[i, j] x[t, j]        A = 128 rows of W, K-major
+//   transposed   D[j, t] = sum_i W[i, j] dy[t, i]       A = 128 columns of W, MN-major
+//
+// One CTA: 128 outputs of the weight's free axis, up to NT tokens (N of the MMA), and its share of
+// the summed axis in K chunks of 64; the shares of a tile are a cluster, whose fp32 sums are added
+// in rank order through distributed shared memory.  Each code is converted once per token tile,
+// into a bf16 operand in shared memory, whatever the number of tokens; the accumulator is in TMEM.
+//
+// Roles (12 warps):
+//   warp 0       bulk loads of codes and scales into slots (contiguous runs, see q4_dev.cuh)
+//   warp 1       TMEM allocation, MMA issue
+//   warps 2, 3   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
+//                vectors, words put together and stored by both warps
+//   warps 4..11  two groups that convert every second chunk each; then the epilogue
+// Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
+// its loop, waits for its own copies and meets the others.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "poetx_internal.h"
+#include "q4_dev.cuh"
+#include "umma_ptx.cuh"
+
+namespace poetx {
+
+// (kernels_umma2.cu) load map of a row-major bf16 matrix, 128-byte swizzle
+bool umma_load_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld,
+                   uint32_t box_cols, uint32_t box_rows);
+
+namespace {
+
+constexpr int kThreadsQ = 384;
+constexpr int kABytes = 128 * 64 * 2;
+constexpr int kGroupThreadsQ = 128;
+
+template <int NT, bool TR>
+struct QCfg {
+  static constexpr int B = NT * 128;                      // bytes of the tokens' operand a stage
+  static constexpr int STAGES = NT <= 64 ? 3 : NT == 128 ? 5 : 4;  // >= 2 converter groups
+  // forward: tiles of 128 rows x 128 columns, two chunks; transposed: 64 rows x 128 columns
+  static constexpr int SLOTS = TR ? 6 : 3;
+  static constexpr int CODES = TR ? 4096 : 8192;
+  static constexpr int SLOT = CODES + (TR ? 512 : 1024);
+  static constexpr int smem = 1024 + STAGES * (kABytes + B) + SLOTS * SLOT + 256;
+  static constexpr int sums = NT * 132 * 4;  // overlays the stages
+  static constexpr uint32_t tmem_cols = NT < 32 ? 32 : NT;
+  static constexpr int ctas = NT <= 64 ? 2 : 1;  // per SM
+};
+static_assert(QCfg<64, false>::smem <= 113 * 1024 && QCfg<64, true>::smem <= 113 * 1024, "smem");
+static_assert(QCfg<256, false>::smem <= 227 * 1024 && QCfg<128, false>::smem <= 227 * 1024 &&
+                  QCfg<256, true>::smem <= 227 * 1024 && QCfg<128, true>::smem <= 227 * 1024,
+              "smem");
+static_assert(QCfg<256, true>::sums <= 4 * (kABytes + QCfg<256, true>::B) &&
+                  QCfg<128, true>::sums <= 5 * (kABytes + QCfg<128, true>::B) &&
+                  QCfg<64, true>::sums <= 3 * (kABytes + QCfg<64, true>::B),
+              "sums fit the stages");
+
+struct ParamsQ {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const __nv_bfloat16* x;
+  __nv_bfloat16* y;
+  int T, m, n, sg;         // sg: scales per row and block
+  int K, out;              // length of the summed axis, of the output rows
+  int chunks, per_cta;     // K chunks in all, per CTA (even in the forward)
+  int bulk_scales;         // the scales of a tile are whole 16-byte runs
+  int vec;                 // rows of x are whole 16-byte vectors
+  int* err;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void bulk_load_q(uint32_t dst, const void* src, uint32_t bytes,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16q(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void named_sync_q(int id, int count) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+// AND of v over the `count` threads meeting at named barrier `id`
+__device__ __forceinline__ bool group_all_q(bool v, int id, int count) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+template <int NT, bool TR>
+__global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
+    k_umma_q4(const __grid_constant__ CUtensorMap tmX, const ParamsQ p) {
+  using C = QCfg<NT, TR>;
+  constexpr int RS = C::STAGES;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - raw);
+  const uint32_t sA = base, sB = sA + RS * kABytes, sQ = sB + RS * C::B;
+  const uint32_t sBar = sQ + C::SLOTS * C::SLOT;
+  auto full_bar = [&](int s) { return sBar + 8u * s; };
+  auto empty_bar = [&](int s) { return sBar + 8u * (RS + s); };
+  auto qfull_bar = [&](int j) { return sBar + 8u * (2 * RS + j); };
+  auto qfree_bar = [&](int j) { return sBar + 8u * (2 * RS + C::SLOTS + j); };
+  const uint32_t done_bar = sBar + 8u * (2 * RS + 2 * C::SLOTS);
+  const uint32_t tmem_slot = done_bar + 8u;
+  static_assert(8 * (2 * RS + 2 * C::SLOTS + 2) <= 256, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.x * 128;  // forward: rows of W; transposed: columns
+  const int tok0 = blockIdx.y * NT;
+  const int c_first = blockIdx.z * p.per_cta;
+  const int cnt = min(p.per_cta, p.chunks - c_first);  // K chunks of this CTA, >= 1
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < RS; ++s) {
+      // the converter group; the TMA thread (and its bytes), or the 64 token loaders
+      mbar_init(full_bar(s), 1 + (p.vec ? 1 : 64));
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int j = 0; j < C::SLOTS; ++j) {
+      mbar_init(qfull_bar(j), 1);
+      mbar_init(qfree_bar(j), TR ? 1 : 2);  // the groups that read the slot
+    }
+    mbar_init(done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - base));
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ codes and scales
+    if (lane == 0) {
+      constexpr int STEP = TR ? 1 : 2;  // chunks per tile
+      int it = 0;
+      bool ok = true;
+      for (; it < cnt; it += STEP) {
+        const int tile = it / STEP, slot = tile % C::SLOTS, use = tile / C::SLOTS;
+        if (!mbar_wait(qfree_bar(slot), (use & 1) ^ 1, p.err, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        const int k = (c_first + it) * 64;
+        // forward: rows row0 .. of block k / 128; transposed: rows k .. of block row0 / 128
+        const int64_t row = TR ? (int64_t)blockIdx.x * p.m + k : (int64_t)(k >> 7) * p.m + row0;
+        const uint32_t rows = (uint32_t)min(TR ? 64 : 128, p.m - (TR ? k : row0));
+        const uint32_t sbytes = p.bulk_scales ? rows * 2u * (uint32_t)p.sg : 0u;
+        mbar_expect_tx(qfull_bar(slot), rows * 64u + sbytes);
+        const uint32_t dst = sQ + slot * C::SLOT;
+        bulk_load_q(dst, p.codes + row * 64, rows * 64u, qfull_bar(slot));
+        if (sbytes) bulk_load_q(dst + C::CODES, p.scales + row * p.sg, sbytes, qfull_bar(slot));
+      }
+      if (!ok)  // no load may still be in flight into this CTA's shared memory when it leaves
+        for (int j = (it > C::SLOTS * STEP ? it - C::SLOTS * STEP : 0); j < it; j += STEP)
+          mbar_drain_wait(qfull_bar((j / STEP) % C::SLOTS), ((j / STEP) / C::SLOTS) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((TR ? 1u : 0u) << 15) |
+                             ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+      for (int it = 0; it < cnt; ++it) {
+        const int s = it % RS;
+        if (!mbar_wait(full_bar(s), (it / RS) & 1, p.err, p.wait_ns)) break;
+        tc_fence_after();
+        const uint32_t a = sA + s * kABytes, b = sB + s * C::B;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(tmem, TR ? make_desc(a + kk * 2048, 8192, 1024) : make_desc(a + kk * 32, 16, 1024),
+                    make_desc(b + kk * 32, 16, 1024), idesc, (it > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(empty_bar(s));
+      }
+      // every MMA issued here completes before TMEM and the stages are used again
+      umma_commit(done_bar);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ tokens
+    const int tid = threadIdx.x - 64;
+    if (p.vec) {
+      if (tid == 0) {
+        int it = 0;
+        bool ok = true;
+        for (; it < cnt; ++it) {
+          const int st = it % RS;
+          if (!mbar_wait(empty_bar(st), ((it / RS) & 1) ^ 1, p.err, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(full_bar(st), (uint32_t)C::B);
+          tma_load_2d(sB + st * C::B, &tmX, (c_first + it) * 64, tok0, full_bar(st));
+        }
+        if (!ok)  // no load may still be in flight into this CTA's shared memory when it leaves
+          for (int j = (it > RS ? it - RS : 0); j < it; ++j)
+            mbar_drain_wait(full_bar(j % RS), (j / RS) & 1);
+      }
+    } else {
+      // 8 values from any 2-byte boundary: the five aligned words around them, shifted together
+      constexpr int PER = NT * 8 / 64, GRP = PER < 8 ? PER : 8;  // 16-byte pieces a thread
+      const int64_t total = (int64_t)p.T * p.K;
+      for (int it = 0; it < cnt; ++it) {
+        const int st = it % RS;
+        const int k0 = (c_first + it) * 64;
+#pragma unroll 1
+        for (int g0 = 0; g0 < PER; g0 += GRP) {
+          uint32_t w[GRP][5];
+#pragma unroll
+          for (int i = 0; i < GRP; ++i) {
+            const int e = tid + 64 * (g0 + i), tok = e >> 3, k = k0 + 8 * (e & 7);
+            const bool on = tok0 + tok < p.T && k < p.K;
+            const int64_t first = on ? (int64_t)(tok0 + tok) * p.K + k : 0;
+            const int64_t word = first >> 1;
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+              w[i][j] = 0;
+              // whole words of x; its last value alone when the count is odd
+              ld_u32_if(w[i][j], reinterpret_cast<const uint32_t*>(p.x) + word + j,
+                        on && 2 * (word + j) + 1 < total);
+              if (on && 2 * (word + j) + 1 == total) w[i][j] = ld_u16(p.x + total - 1);
+            }
+          }
+          if (g0 == 0 && !mbar_wait(empty_bar(st), ((it / RS) & 1) ^ 1, p.err, p.wait_ns)) {
+            it = cnt;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < GRP; ++i) {
+            const int e = tid + 64 * (g0 + i), tok = e >> 3, c = e & 7, k = k0 + 8 * c;
+            const uint32_t sh = ((uint32_t)((int64_t)(tok0 + tok) * p.K + k) & 1u) * 16u;
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = __funnelshift_r(w[i][j], w[i][j + 1], sh);
+              // values past the end of the row
+              if (k + 2 * j + 1 >= p.K) v[j] &= k + 2 * j < p.K ? 0xffffu : 0u;
+            }
+            sts128(sB + st * C::B + tok * 128 + ((c ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+          }
+        }
+        if (it < cnt) {
+          fence_async_smem();
+          mbar_arrive(full_bar(st));
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ codes -> bf16 operand
+    // Group g converts chunks it = g, g + 2, ..: 512 units of two code words (16 codes).  Row r
+    // of the tile, 16-byte chunk t, columns 64 h + 8 t .. and 64 h + 32 + 8 t ..: chunks t and 4
+    // + t of the row's 64 columns in the operand (forward: row r of the stage, h the chunk's half
+    // of the tile; transposed: row r of box h).  Odd rows store their second word first, so that
+    // 8 lanes (two rows) write 8 different bank groups.
+    const int grp = (warp - 4) >> 2, gt = (threadIdx.x - 128) & (kGroupThreadsQ - 1);
+    const int bar_id = 1 + grp;
+    const uint32_t sg = (uint32_t)p.sg;
+    for (int it = grp; it < cnt; it += 2) {
+      const int s = it % RS;
+      const int tile = TR ? it : it >> 1, slot = tile % C::SLOTS, use = tile / C::SLOTS;
+      const int k = (c_first + it) * 64;
+      int got = 1;
+      if (lane == 0)
+        got = mbar_wait(qfull_bar(slot), use & 1, p.err, p.wait_ns) &&
+              mbar_wait(empty_bar(s), ((it / RS) & 1) ^ 1, p.err, p.wait_ns);
+      // every thread of the group takes the same branch (a failed wait of any warp)
+      if (!group_all_q(__shfl_sync(0xffffffffu, got, 0) != 0, bar_id, kGroupThreadsQ)) break;
+      // both phases have completed: every lane acquires them (returns at once)
+      while (!mbar_try_wait(qfull_bar(slot), use & 1)) {
+      }
+      while (!mbar_try_wait(empty_bar(s), ((it / RS) & 1) ^ 1)) {
+      }
+      const uint32_t src = sQ + slot * C::SLOT, dst = sA + s * kABytes;
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const uint32_t ch = (uint32_t)(gt + kGroupThreadsQ * jj);
+        const uint32_t t = ch & 3u, r = (ch >> 2) & (TR ? 63u : 127u);
+        const uint32_t h = TR ? ch >> 8 : (uint32_t)it & 1u;
+        const uint2 wd = lds_u2(src + r * 64u + t * 16u + h * 8u);
+        const uint32_t i0 = ((2u * h) * sg) >> 2, i1 = ((2u * h + 1u) * sg) >> 2;
+        const bool live = !TR || k + (int)r < p.m;  // rows past the sum: zero operands
+        uint32_t s0, s1;
+        if (p.bulk_scales) {
+          const uint32_t srow = src + C::CODES + r * sg * 2u;
+          s0 = lds_u16q(srow + i0 * 2u);
+          s1 = lds_u16q(srow + i1 * 2u);
+        } else {
+          const int64_t row = TR ? (int64_t)blockIdx.x * p.m + min(k + (int)r, p.m - 1)
+                                 : (int64_t)(k >> 7) * p.m + min(row0 + (int)r, p.m - 1);
+          s0 = ld_u16(p.scales + row * p.sg + i0);
+          s1 = ld_u16(p.scales + row * p.sg + i1);
+        }
+        const bool odd = (r & 1u) != 0;
+        const uint32_t row = dst + (TR ? h * 8192u : 0u) + r * 128u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool second = (i == 1) != odd;
+          // 4 s: the unpacked codes are (code - 8) / 4
+          const uint32_t s2 = bf2_mul((second ? s1 : s0) * 0x10001u, 0x40804080u);
+          uint32_t q[4];
+          q4_unpack(second ? wd.y : wd.x, q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = live ? bf2_mul(q[e], s2) : 0u;
+          const uint32_t c = ((second ? 4u : 0u) + t) ^ (r & 7u);
+          sts128(row + (c << 4), q[0], q[1], q[2], q[3]);
+        }
+      }
+      fence_async_smem();  // the generic-proxy stores, then the tensor core's reads
+      named_sync_q(bar_id, kGroupThreadsQ);
+      if (gt == 0) {
+        mbar_arrive(full_bar(s));
+        mbar_arrive(qfree_bar(slot));
+      }
+    }
+  }
+  __syncthreads();  // every role has left; its copies have landed
+  // ------------------------------------------------------------ sums
+  // (without a timeout every MMA of this CTA completes; with one the sums mean nothing, and the
+  // wait below covers the MMAs that were issued)
+  int done = 0;
+  if (warp >= 4) {
+    if (lane == 0) done = mbar_wait(done_bar, 0, p.err, p.wait_ns) ? 1 : 0;
+    done = __shfl_sync(0xffffffffu, done, 0);
+  }
+  if (warp == 1 && lane == 0) mbar_drain_wait(done_bar, 0);
+  __syncthreads();
+  float* buf = reinterpret_cast<float*>(gbase);  // [NT][132]
+  constexpr int LD = 132;
+  if (warp >= 4 && done) {
+    tc_fence_after();
+    const int q = warp & 3, half = (warp - 4) >> 2;
+#pragma unroll
+    for (int c = 0; c < NT / 2; c += 8) {
+      const int col = half * (NT / 2) + c;
+      uint32_t v[8];
+      tmem_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) buf[(col + e) * LD + q * 32 + lane] = __uint_as_float(v[e]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::tmem_cols);
+  }
+  auto store = [&](int tok, int c, float v) {
+    if (tok0 + tok < p.T && row0 + c < p.out)
+      p.y[(int64_t)(tok0 + tok) * p.out + row0 + c] = __float2bfloat16_rn(v);
+  };
+  const int splits = gridDim.z;
+  if (splits == 1) {
+    for (int o = threadIdx.x; o < NT * 128; o += kThreadsQ)
+      store(o >> 7, o & 127, buf[(o >> 7) * LD + (o & 127)]);
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+  const uint32_t local = smem_u32(buf);
+  const int toks = min(NT, p.T - tok0);
+  for (int o = (int)blockIdx.z * kThreadsQ + threadIdx.x; o < toks * 128; o += splits * kThreadsQ) {
+    float v = 0.f;
+    for (int q = 0; q < splits; ++q) {
+      uint32_t addr;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(addr) : "r"(local + 4u * (uint32_t)((o >> 7) * LD + (o & 127))), "r"(q));
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
+      v += f;
+    }
+    store(o >> 7, o & 127, v);
+  }
+  // no CTA leaves while another still reads its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
+template <int NT, bool TR>
+cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  using C = QCfg<NT, TR>;
+  auto kern = k_umma_q4<NT, TR>;
+  static bool attr_done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  ParamsQ p;
+  p.codes = w.codes;
+  p.scales = static_cast<const uint16_t*>(w.scales);
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.T = T;
+  p.m = w.m;
+  p.n = w.n;
+  p.sg = 128 / w.group;
+  p.K = TR ? w.m : w.n;
+  p.out = TR ? w.n : w.m;
+  p.chunks = (p.K + 63) / 64;
+  p.bulk_scales = ((int64_t)w.m * p.sg) % 8 == 0;
+  p.vec = p.K % 8 == 0;
+  p.err = device_error_flag();
+  if (!p.err) return cudaErrorInvalidDevice;  // the bounded waits need the flag
+  p.wait_ns = wait_limit_ns();
+  const int tiles = (p.out + 127) / 128, ttiles = (T + NT - 1) / NT;
+  // shares of the summed axis: a grid within one wave with a seventh of the places to spare (a
+  // cluster needs all its places in one group of SMs), at least 4 chunks a share, at most 8
+  const int unit = TR ? 1 : 2;
+  const int units = (p.chunks + unit - 1) / unit;
+  int64_t splits = (int64_t)C::ctas * num_sms() * 17 / 20 / ((int64_t)tiles * ttiles);
+  if (splits > p.chunks / 4) splits = p.chunks / 4;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  if (splits == 7) splits = 6;
+  const int per = (int)((units + splits - 1) / splits);
+  splits = (units + per - 1) / per;  // every share has a chunk
+  p.per_cta = per * unit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, ttiles, (unsigned)splits);
+  cfg.blockDim = dim3(kThreadsQ);
+  cfg.dynamicSmemBytes = C::smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = (unsigned)splits;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  CUtensorMap mx = {};
+  if (p.vec && !umma_load_map(&mx, x, T, p.K, p.K, 64u, (uint32_t)NT)) return cudaErrorInvalidValue;
+  begin_launch("gemm_w0", s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, p);
+  end_launch("gemm_w0", s);
+  return e;
+}
+
+template <bool TR>
+cudaError_t launch_tr(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  if (T <= 16) return launch_q<16, TR>(w, x, y, T, s);
+  if (T <= 32) return launch_q<32, TR>(w, x, y, T, s);
+  if (T <= 64) return launch_q<64, TR>(w, x, y, T, s);
+  if (T <= 128) return launch_q<128, TR>(w, x, y, T, s);
+  return launch_q<256, TR>(w, x, y, T, s);
+}
+
+}  // namespace
+
+cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
+                           cudaStream_t s) {
+  return transpose ? launch_tr<true>(w, x, y, T, s) : launch_tr<false>(w, x, y, T, s);
+}
+
+}  // namespace poetx

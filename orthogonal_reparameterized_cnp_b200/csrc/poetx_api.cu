@@ -1060,11 +1060,10 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
   g.batch = 1; g.out_f32 = 0;
   g.D = out; g.ldd = g.N;
   if (w.q4.codes) {
-    // from 256 tokens on (and whole 256-column tiles) the tensor-core kernel converts the codes
-    // on chip; other calls take the few-token kernels, in tiles of tokens
+    if (T <= 8) return launch_q4_product(w.q4, in, out, T, !forward, s);
     if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4))
       return launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
-    return launch_q4_product(w.q4, in, out, T, !forward, s);
+    return launch_umma_q4(w.q4, in, out, T, !forward, s);
   }
   if (gemm_pairs_enabled() && umma_pair_eligible(g) && n % 16 == 0) {  // converted on chip
     PairQ8 q;

@@ -106,6 +106,9 @@ cudaError_t launch_dequant_q4(const Q4Weight& w, void* out, int elem_bytes, cuda
 // y[T, m] = x[T, n] W^T, or (transpose) y[T, n] = x[T, m] W: the few-token kernels, any T
 cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                               cudaStream_t s);
+// the same on tcgen05 with the weight as the M operand (kernels_umma_q4.cu), any T
+cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
+                           cudaStream_t s);
 // few-token block products fused with their index maps (bf16; width % b == 0, b % 128 == 0):
 // out = blockdiag(G) x[:, idx]^T by rows (save_u: the gathered rows too), and y[:, idx] =
 // the block product of `in`
