@@ -330,16 +330,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
 // Slot (and its use, whose parity the barriers count) of K chunk `it` of a CTA's flat sequence.
 // 8-bit, and 4-bit backward: group it % 4 has slots 2 g and 2 g + 1 in turn.  4-bit forward: a
 // tile holds chunks 2 j and 2 j + 1; tiles go to slots 2 p and 2 p + 1, p = j % 2, in turn, and
@@ -687,38 +677,14 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
       const uint32_t src = sQ + slot * kSlotBytes;
       const uint32_t dst = sB + sb * kPairB;
       if (QB == 4) {
-        // 512 units of two code words (16 codes): row r of the tile, 16-byte chunk t, columns
-        // 64 h + 8 t .. and 64 h + 32 + 8 t ..: chunks t and 4 + t of the row's 64 columns in
-        // the operand (forward: row r of the stage, h the chunk's half of the tile; backward:
-        // row r of box h).  Odd rows store their second word first, so that 8 lanes (two rows)
-        // write 8 different bank groups.
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-          const uint32_t ch = (uint32_t)(gt + 64 * jj);
-          const uint32_t t = ch & 3u, r = (ch >> 2) & (B_MN ? 63u : 127u);
-          const uint32_t h = B_MN ? ch >> 8 : (uint32_t)it & 1u;
-          const uint2 wd = lds64(src + r * 64u + t * 16u + h * 8u);
-          const uint32_t sg = (uint32_t)p.sg4;
-          const uint32_t srow = src + kSlotCodes + r * sg * 2u;
-          const uint32_t s0 = lds_u16(srow + (((2u * h) * sg) >> 2) * 2u);
-          const uint32_t s1 = lds_u16(srow + (((2u * h + 1u) * sg) >> 2) * 2u);
-          const bool odd = (r & 1u) != 0;
-          const bool live = !B_MN || k + (int)r < p.K;  // rows past K: zero operands
-          const uint32_t row = dst + (B_MN ? h * 8192u : 0u) + r * 128u;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool second = (i == 1) != odd;
-            const uint32_t word = second ? wd.y : wd.x;
-            // 4 s: the unpacked codes are (code - 8) / 4
-            const uint32_t s2 = bf2_mul((second ? s1 : s0) * 0x10001u, 0x40804080u);
-            uint32_t q[4], o[4];
-            q4_unpack(word, q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = live ? bf2_mul(q[e], s2) : 0u;
-            const uint32_t c = ((second ? 4u : 0u) + t) ^ (r & 7u);
-            sts128(row + (c << 4), o[0], o[1], o[2], o[3]);
-          }
-        }
+        const int rows = B_MN ? min(64, p.K - k) : 128;  // rows past K: zero operands
+        const uint32_t half = (uint32_t)it & 1u;
+        if (!B_MN || rows == 64)
+          q4_convert<B_MN ? 64 : 128, kGroupThreads, true>(src, src + kSlotCodes, dst, gt, half,
+                                                           (uint32_t)p.sg4, rows, nullptr);
+        else
+          q4_convert<B_MN ? 64 : 128, kGroupThreads, false>(src, src + kSlotCodes, dst, gt, half,
+                                                            (uint32_t)p.sg4, rows, nullptr);
       } else {
 #pragma unroll
       for (int jj = 0; jj < kConvChunks; ++jj) {
@@ -816,8 +782,11 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 hh = __floats2bfloat162_rn(__uint_as_float(v[8 * kk + 2 * e]),
-                                                        __uint_as_float(v[8 * kk + 2 * e + 1]));
+              // (4-bit operands are s (code - 8) / 4)
+              constexpr float scale = QB == 4 ? 4.f : 1.f;
+              __nv_bfloat162 hh =
+                  __floats2bfloat162_rn(scale * __uint_as_float(v[8 * kk + 2 * e]),
+                                        scale * __uint_as_float(v[8 * kk + 2 * e + 1]));
               o[e] = *reinterpret_cast<uint32_t*>(&hh);
             }
             sts128(my_row + (((uint32_t)k ^ sw) << 4), o[0], o[1], o[2], o[3]);

@@ -9,12 +9,12 @@
 // in rank order through distributed shared memory.  Each code is converted once per token tile,
 // into a bf16 operand in shared memory, whatever the number of tokens; the accumulator is in TMEM.
 //
-// Roles (12 warps):
+// Roles:
 //   warp 0       bulk loads of codes and scales into slots (contiguous runs, see q4_dev.cuh)
 //   warp 1       TMEM allocation, MMA issue
 //   warps 2, 3   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
 //                vectors, words put together and stored by both warps
-//   warps 4..11  two groups that convert every second chunk each; then the epilogue
+//   warps 4 ..   G groups that convert every G-th chunk each; then the epilogue
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.
 #include <cuda.h>
@@ -32,31 +32,33 @@ bool umma_load_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols
 
 namespace {
 
-constexpr int kThreadsQ = 384;
 constexpr int kABytes = 128 * 64 * 2;
-constexpr int kGroupThreadsQ = 128;
 
+// The way of a chunk (slot, conversion, fences and barriers, MMA, commit) takes 1 to 2 us, most
+// of it waiting, so many chunks have to be on their way at once: as many groups and stages as
+// shared memory holds.  Two groups of four warps with three stages, two CTAs an SM: 16.5 us at T = 16,
+// 5120 x 5120, of which 11.5 remain without any conversion.
+//   G <= STAGES and slots visited by the same groups every time, so that no wait is two phases of
+//   its barrier ahead: SLOTS is a multiple of G / 2 tiles (forward), of G (transposed).
 template <int NT, bool TR>
 struct QCfg {
   static constexpr int B = NT * 128;                      // bytes of the tokens' operand a stage
-  static constexpr int STAGES = NT <= 64 ? 3 : NT == 128 ? 5 : 4;  // >= 2 converter groups
+  static constexpr int STAGES = NT <= 64 ? 6 : NT == 128 ? 5 : 4;
+  static constexpr int G = NT <= 64 ? 6 : NT == 128 ? 4 : 2;
+  static constexpr int GT = NT <= 64 ? 64 : NT == 128 ? 128 : 256;  // threads of a group
+  static constexpr int threads = 128 + G * GT;
   // forward: tiles of 128 rows x 128 columns, two chunks; transposed: 64 rows x 128 columns
-  static constexpr int SLOTS = TR ? 6 : 3;
+  static constexpr int SLOTS = (NT <= 64 ? 6 : NT == 128 ? 4 : 2) * (TR ? 2 : 1);
   static constexpr int CODES = TR ? 4096 : 8192;
   static constexpr int SLOT = CODES + (TR ? 512 : 1024);
-  static constexpr int smem = 1024 + STAGES * (kABytes + B) + SLOTS * SLOT + 256;
+  static constexpr int smem = 1024 + STAGES * (kABytes + B) + SLOTS * SLOT + 512;
   static constexpr int sums = NT * 132 * 4;  // overlays the stages
   static constexpr uint32_t tmem_cols = NT < 32 ? 32 : NT;
-  static constexpr int ctas = NT <= 64 ? 2 : 1;  // per SM
+  static_assert(G <= STAGES && SLOTS % (TR ? G : G / 2) == 0, "phases");
+  static_assert(smem <= 227 * 1024 && threads <= 1024, "resources");
+  static_assert(sums <= STAGES * (kABytes + B), "sums fit the stages");
+  static_assert(8 * (2 * STAGES + 2 * SLOTS + 2) <= 512, "barriers");
 };
-static_assert(QCfg<64, false>::smem <= 113 * 1024 && QCfg<64, true>::smem <= 113 * 1024, "smem");
-static_assert(QCfg<256, false>::smem <= 227 * 1024 && QCfg<128, false>::smem <= 227 * 1024 &&
-                  QCfg<256, true>::smem <= 227 * 1024 && QCfg<128, true>::smem <= 227 * 1024,
-              "smem");
-static_assert(QCfg<256, true>::sums <= 4 * (kABytes + QCfg<256, true>::B) &&
-                  QCfg<128, true>::sums <= 5 * (kABytes + QCfg<128, true>::B) &&
-                  QCfg<64, true>::sums <= 3 * (kABytes + QCfg<64, true>::B),
-              "sums fit the stages");
 
 struct ParamsQ {
   const uint8_t* codes;
@@ -78,16 +80,6 @@ __device__ __forceinline__ void bulk_load_q(uint32_t dst, const void* src, uint3
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
       ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16q(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile(
@@ -114,10 +106,10 @@ __device__ __forceinline__ bool group_all_q(bool v, int id, int count) {
 }
 
 template <int NT, bool TR>
-__global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
+__global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
     k_umma_q4(const __grid_constant__ CUtensorMap tmX, const ParamsQ p) {
   using C = QCfg<NT, TR>;
-  constexpr int RS = C::STAGES;
+  constexpr int RS = C::STAGES, G = C::G, GT = C::GT;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -130,7 +122,6 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
   auto qfree_bar = [&](int j) { return sBar + 8u * (2 * RS + C::SLOTS + j); };
   const uint32_t done_bar = sBar + 8u * (2 * RS + 2 * C::SLOTS);
   const uint32_t tmem_slot = done_bar + 8u;
-  static_assert(8 * (2 * RS + 2 * C::SLOTS + 2) <= 256, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * 128;  // forward: rows of W; transposed: columns
@@ -278,15 +269,11 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
     }
   } else {
     // ------------------------------------------------------------ codes -> bf16 operand
-    // Group g converts chunks it = g, g + 2, ..: 512 units of two code words (16 codes).  Row r
-    // of the tile, 16-byte chunk t, columns 64 h + 8 t .. and 64 h + 32 + 8 t ..: chunks t and 4
-    // + t of the row's 64 columns in the operand (forward: row r of the stage, h the chunk's half
-    // of the tile; transposed: row r of box h).  Odd rows store their second word first, so that
-    // 8 lanes (two rows) write 8 different bank groups.
-    const int grp = (warp - 4) >> 2, gt = (threadIdx.x - 128) & (kGroupThreadsQ - 1);
+    // group g converts chunks it = g, g + G, .. (q4_convert)
+    const int grp = (threadIdx.x - 128) / GT, gt = (threadIdx.x - 128) % GT;
     const int bar_id = 1 + grp;
     const uint32_t sg = (uint32_t)p.sg;
-    for (int it = grp; it < cnt; it += 2) {
+    for (int it = grp; it < cnt; it += G) {
       const int s = it % RS;
       const int tile = TR ? it : it >> 1, slot = tile % C::SLOTS, use = tile / C::SLOTS;
       const int k = (c_first + it) * 64;
@@ -295,49 +282,26 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
         got = mbar_wait(qfull_bar(slot), use & 1, p.err, p.wait_ns) &&
               mbar_wait(empty_bar(s), ((it / RS) & 1) ^ 1, p.err, p.wait_ns);
       // every thread of the group takes the same branch (a failed wait of any warp)
-      if (!group_all_q(__shfl_sync(0xffffffffu, got, 0) != 0, bar_id, kGroupThreadsQ)) break;
+      if (!group_all_q(__shfl_sync(0xffffffffu, got, 0) != 0, bar_id, GT)) break;
       // both phases have completed: every lane acquires them (returns at once)
       while (!mbar_try_wait(qfull_bar(slot), use & 1)) {
       }
       while (!mbar_try_wait(empty_bar(s), ((it / RS) & 1) ^ 1)) {
       }
       const uint32_t src = sQ + slot * C::SLOT, dst = sA + s * kABytes;
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const uint32_t ch = (uint32_t)(gt + kGroupThreadsQ * jj);
-        const uint32_t t = ch & 3u, r = (ch >> 2) & (TR ? 63u : 127u);
-        const uint32_t h = TR ? ch >> 8 : (uint32_t)it & 1u;
-        const uint2 wd = lds_u2(src + r * 64u + t * 16u + h * 8u);
-        const uint32_t i0 = ((2u * h) * sg) >> 2, i1 = ((2u * h + 1u) * sg) >> 2;
-        const bool live = !TR || k + (int)r < p.m;  // rows past the sum: zero operands
-        uint32_t s0, s1;
-        if (p.bulk_scales) {
-          const uint32_t srow = src + C::CODES + r * sg * 2u;
-          s0 = lds_u16q(srow + i0 * 2u);
-          s1 = lds_u16q(srow + i1 * 2u);
-        } else {
-          const int64_t row = TR ? (int64_t)blockIdx.x * p.m + min(k + (int)r, p.m - 1)
-                                 : (int64_t)(k >> 7) * p.m + min(row0 + (int)r, p.m - 1);
-          s0 = ld_u16(p.scales + row * p.sg + i0);
-          s1 = ld_u16(p.scales + row * p.sg + i1);
-        }
-        const bool odd = (r & 1u) != 0;
-        const uint32_t row = dst + (TR ? h * 8192u : 0u) + r * 128u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool second = (i == 1) != odd;
-          // 4 s: the unpacked codes are (code - 8) / 4
-          const uint32_t s2 = bf2_mul((second ? s1 : s0) * 0x10001u, 0x40804080u);
-          uint32_t q[4];
-          q4_unpack(second ? wd.y : wd.x, q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = live ? bf2_mul(q[e], s2) : 0u;
-          const uint32_t c = ((second ? 4u : 0u) + t) ^ (r & 7u);
-          sts128(row + (c << 4), q[0], q[1], q[2], q[3]);
-        }
+      // forward: rows past the weight's end give outputs that are not stored; transposed: rows
+      // past the end of the sum have to give zeros
+      const int rows = TR ? min(64, p.m - k) : min(128, p.m - row0);
+      if (p.bulk_scales && (!TR || rows == 64)) {
+        q4_convert<TR ? 64 : 128, GT, true>(src, src + C::CODES, dst, gt, (uint32_t)it & 1u, sg,
+                                            rows, nullptr);
+      } else {
+        const int64_t row = TR ? (int64_t)blockIdx.x * p.m + k : (int64_t)(k >> 7) * p.m + row0;
+        q4_convert<TR ? 64 : 128, GT, false>(src, src + C::CODES, dst, gt, (uint32_t)it & 1u, sg,
+                                             rows, p.bulk_scales ? nullptr : p.scales + row * p.sg);
       }
       fence_async_smem();  // the generic-proxy stores, then the tensor core's reads
-      named_sync_q(bar_id, kGroupThreadsQ);
+      named_sync_q(bar_id, GT);
       if (gt == 0) {
         mbar_arrive(full_bar(s));
         mbar_arrive(qfree_bar(slot));
@@ -349,7 +313,7 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
   // (without a timeout every MMA of this CTA completes; with one the sums mean nothing, and the
   // wait below covers the MMAs that were issued)
   int done = 0;
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 12) {
     if (lane == 0) done = mbar_wait(done_bar, 0, p.err, p.wait_ns) ? 1 : 0;
     done = __shfl_sync(0xffffffffu, done, 0);
   }
@@ -357,7 +321,7 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
   __syncthreads();
   float* buf = reinterpret_cast<float*>(gbase);  // [NT][132]
   constexpr int LD = 132;
-  if (warp >= 4 && done) {
+  if (done) {  // warps 4 .. 11
     tc_fence_after();
     const int q = warp & 3, half = (warp - 4) >> 2;
 #pragma unroll
@@ -378,11 +342,11 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
   }
   auto store = [&](int tok, int c, float v) {
     if (tok0 + tok < p.T && row0 + c < p.out)
-      p.y[(int64_t)(tok0 + tok) * p.out + row0 + c] = __float2bfloat16_rn(v);
+      p.y[(int64_t)(tok0 + tok) * p.out + row0 + c] = __float2bfloat16_rn(4.f * v);
   };
   const int splits = gridDim.z;
   if (splits == 1) {
-    for (int o = threadIdx.x; o < NT * 128; o += kThreadsQ)
+    for (int o = threadIdx.x; o < NT * 128; o += C::threads)
       store(o >> 7, o & 127, buf[(o >> 7) * LD + (o & 127)]);
     return;
   }
@@ -390,7 +354,7 @@ __global__ void __launch_bounds__(kThreadsQ, QCfg<NT, TR>::ctas)
                ::: "memory");
   const uint32_t local = smem_u32(buf);
   const int toks = min(NT, p.T - tok0);
-  for (int o = (int)blockIdx.z * kThreadsQ + threadIdx.x; o < toks * 128; o += splits * kThreadsQ) {
+  for (int o = (int)blockIdx.z * C::threads + threadIdx.x; o < toks * 128; o += splits * C::threads) {
     float v = 0.f;
     for (int q = 0; q < splits; ++q) {
       uint32_t addr;
@@ -443,7 +407,7 @@ cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStrea
   // cluster needs all its places in one group of SMs), at least 4 chunks a share, at most 8
   const int unit = TR ? 1 : 2;
   const int units = (p.chunks + unit - 1) / unit;
-  int64_t splits = (int64_t)C::ctas * num_sms() * 17 / 20 / ((int64_t)tiles * ttiles);
+  int64_t splits = (int64_t)num_sms() * 17 / 20 / ((int64_t)tiles * ttiles);
   if (splits > p.chunks / 4) splits = p.chunks / 4;
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   if (splits == 7) splits = 6;
@@ -452,7 +416,7 @@ cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStrea
   p.per_cta = per * unit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, ttiles, (unsigned)splits);
-  cfg.blockDim = dim3(kThreadsQ);
+  cfg.blockDim = dim3(C::threads);
   cfg.dynamicSmemBytes = C::smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -111,6 +111,71 @@ __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// One K chunk of the tensor-core operand from a staged tile of codes: bf16 s (code - 8) / 4 (the
+// caller's sums are 4 times too small), written in the 128-byte-swizzled layout that the MMA reads.
+// GT threads; 512 units of two code words (16 codes): row r of the tile, 16-byte chunk t, columns
+// 64 h + 8 t .. and 64 h + 32 + 8 t .., which are the 16-byte chunks t and 4 + t of the row's 64
+// columns in the operand.
+//   ROWS = 128 (K-major operand): tile of 128 rows; h = `half` of its columns; row r of the stage.
+//   ROWS = 64 (MN-major operand): tile of 64 rows; row r of box h of the stage.
+// A thread's rows are r0, r0 + GT / 4, .., which share the swizzle and the parity: odd rows store
+// their second word first, so that 8 lanes (two rows) write 8 different bank groups.
+//   FULL: every row is in the tile, and its scales are staged behind the codes at `ssrc`; else
+//   rows from `rows` on give zeros, and scales come from `gs` (global, row 0 of the tile) if given.
+template <int ROWS, int GT, bool FULL>
+__device__ __forceinline__ void q4_convert(uint32_t src, uint32_t ssrc, uint32_t dst, int gt,
+                                           uint32_t half, uint32_t sg, int rows,
+                                           const uint16_t* gs) {
+  constexpr uint32_t RSTEP = GT / 4;
+  static_assert(RSTEP % 8 == 0, "one swizzle a thread");
+  const uint32_t t = (uint32_t)gt & 3u, r0 = (uint32_t)gt >> 2;
+  const bool odd = (r0 & 1u) != 0;
+  const uint32_t c0 = ((((odd ? 4u : 0u) + t) ^ (r0 & 7u)) << 4) + r0 * 128u + dst;
+  const uint32_t c1 = ((((odd ? 0u : 4u) + t) ^ (r0 & 7u)) << 4) + r0 * 128u + dst;
+#pragma unroll
+  for (int jj = 0; jj < 512 / GT; ++jj) {
+    const uint32_t unit_rows = ROWS / RSTEP;                       // units before the next box
+    const uint32_t h = ROWS == 64 ? (uint32_t)jj / unit_rows : half;
+    const uint32_t dr = ((uint32_t)jj % unit_rows) * RSTEP, r = r0 + dr;
+    uint2 wd;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(wd.x), "=r"(wd.y)
+                 : "r"(src + r0 * 64u + t * 16u + h * 8u + dr * 64u)
+                 : "memory");
+    // scales of the unit's words (32-column groups 2 h and 2 h + 1)
+    const uint32_t i0 = (2u * h * sg) >> 2, i1 = ((2u * h + 1u) * sg) >> 2;
+    uint32_t s0, s1;
+    if (FULL || !gs) {
+      uint16_t a, b;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(ssrc + (r * sg + i0) * 2u) : "memory");
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(ssrc + (r * sg + i1) * 2u) : "memory");
+      s0 = a;
+      s1 = b;
+    } else {
+      const uint16_t* g = gs + (int64_t)min((int)r, rows - 1) * sg;
+      s0 = ld_u16(g + i0);
+      s1 = ld_u16(g + i1);
+    }
+    const uint32_t sa = (odd ? s1 : s0) * 0x10001u, sb = (odd ? s0 : s1) * 0x10001u;
+    uint32_t a[4], b[4];
+    q4_unpack(odd ? wd.y : wd.x, a);
+    q4_unpack(odd ? wd.x : wd.y, b);
+    const bool live = FULL || (int)r < rows;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = live ? bf2_mul(a[e], sa) : 0u;
+      b[e] = live ? bf2_mul(b[e], sb) : 0u;
+    }
+    const uint32_t off = dr * 128u + (ROWS == 64 ? h * 8192u : 0u);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(c0 + off), "r"(a[0]), "r"(a[1]),
+                 "r"(a[2]), "r"(a[3])
+                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(c1 + off), "r"(b[0]), "r"(b[1]),
+                 "r"(b[2]), "r"(b[3])
+                 : "memory");
+  }
+}
+
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 accumulation
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
