@@ -632,17 +632,17 @@ __global__ void __launch_bounds__(32 * kColWarps, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// Products with 8 NT tokens a CTA, both directions.  Each CTA: an output tile of 128 rows of W
-// (forward) or 256 columns (transposed), 8 NT tokens, and its share of the summed axis in steps
-// of 128; the shares of a tile are a cluster, whose partial sums are added in rank order through
-// distributed shared memory.  Warps: 4 along the tile x 2 along the summed axis.  The
+// y[t, i] = sum_j W[i, j] x[t, j] for 9 to 16 tokens.  Each CTA: 128 rows of W and its share of the
+// blocks; the shares of a tile are a cluster, whose partial sums are added in rank order through
+// distributed shared memory.  Warps: 4 along the rows (32 each) x 2 along the blocks.  The
 // activations of a step pass through shared memory (cp.async, two stages); the codes go straight
 // to registers, one step ahead.  The scale multiplies the bf16 integers (exact for scales of 5
-// significant bits).
+// significant bits).  Bound by the latency of its short loops: 20 us at 13824 x 5120, 14 at 5120 x
+// 5120 (the tcgen05 form: 28 and 14).
 constexpr int kTileThreads = 256;
 
-// adds the two half-sums and the cluster's shares, and hands every (token, column) of the
-// COLS-wide tile to `store`.  buf: [TOK][COLS + 4] floats.
+// adds the two half-sums and the cluster's shares, and hands every (token, row) of the tile to
+// `store`.  buf: [TOK][COLS + 4] floats.
 template <int TOK, int COLS, typename Put, typename Store>
 __device__ __forceinline__ void tile_reduce(float* buf, bool upper, Put put, Store store) {
   constexpr int LD = COLS + 4;
@@ -687,29 +687,16 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
                : "memory");
 }
 
-// a step of 128 values of 8 NT tokens into shared memory rows of LDB bytes; values past `len`
-// (and tokens past T) are zero
+// a step of 128 values of the tokens into shared memory rows of LDB bytes; values past `len` (and
+// tokens past T) are zero
 template <int TOK, int LDB>
-__device__ __forceinline__ void stage_tokens(unsigned char* dst, const __nv_bfloat16* x, int tok0,
-                                             int T, int k0, int len, bool vec) {
-  if (vec) {  // rows of whole 16-byte vectors
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-#pragma unroll
-    for (int e0 = 0; e0 < TOK * 16; e0 += kTileThreads) {
-      const int e = e0 + threadIdx.x;
-      if (TOK * 16 % kTileThreads != 0 && e >= TOK * 16) break;
-      const int tok = e >> 4, c = (e & 15) * 8;
-      const bool on = tok0 + tok < T && k0 + c < len;
-      const __nv_bfloat16* src = on ? x + (int64_t)(tok0 + tok) * len + k0 + c : x;
-      cp_async16_zfill(d + tok * LDB + c * 2, src, on);
-    }
-  } else {
-    for (int e = threadIdx.x; e < TOK * 128; e += kTileThreads) {
-      const int tok = e >> 7, c = e & 127;
-      __nv_bfloat16 v = __ushort_as_bfloat16(0);
-      if (tok0 + tok < T && k0 + c < len) v = x[(int64_t)(tok0 + tok) * len + k0 + c];
-      *reinterpret_cast<__nv_bfloat16*>(dst + tok * LDB + c * 2) = v;
-    }
+__device__ __forceinline__ void stage_tokens(unsigned char* dst, const __nv_bfloat16* x, int T,
+                                             int k0, int len) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  for (int e = threadIdx.x; e < TOK * 16; e += kTileThreads) {
+    const int tok = e >> 4, c = (e & 15) * 8;
+    const bool on = tok < T && k0 + c < len;
+    cp_async16_zfill(d + tok * LDB + c * 2, on ? x + (int64_t)tok * len + k0 + c : x, on);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -718,12 +705,7 @@ constexpr int tile_row_smem(int nt) {
   const int stages = 2 * 2 * nt * 8 * 320, sums = nt * 8 * (128 + 4) * 4;
   return stages > sums ? stages : sums;
 }
-constexpr int tile_col_smem(int nt) {
-  const int stages = 2 * nt * 8 * 288, sums = nt * 8 * (256 + 4) * 4;
-  return stages > sums ? stages : sums;
-}
-
-// forward: warp (rw, kw) takes rows 32 rw .. 32 rw + 31 of the tile and every second block
+// warp (rw, kw) takes rows 32 rw .. 32 rw + 31 of the tile and every second block
 template <int NT, int GS>
 __global__ void __launch_bounds__(kTileThreads, 2)
     k_q4_tile_rows(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
@@ -734,7 +716,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   constexpr int SG = 128 / GS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rw = warp & 3, kw = warp >> 2;
-  const int row0 = blockIdx.x * 128 + rw * 32, tok0 = blockIdx.y * TOK;
+  const int row0 = blockIdx.x * 128 + rw * 32;
   const int nb = n / 128;
   const int kb_first = blockIdx.z * blocks_per_cta;
   const int kb_last = min(nb, kb_first + blocks_per_cta);
@@ -767,8 +749,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   auto stage = [&](int it) {  // both blocks of iteration `it`
     unsigned char* d = tile_raw + (it & 1) * 2 * STAGE;
     const int k0 = (kb_first + 2 * it) * 128;
-    stage_tokens<TOK, LDB>(d, x, tok0, T, k0, n, true);
-    stage_tokens<TOK, LDB>(d + STAGE, x, tok0, T, k0 + 128, n, true);
+    stage_tokens<TOK, LDB>(d, x, T, k0, n);
+    stage_tokens<TOK, LDB>(d + STAGE, x, T, k0 + 128, n);
   };
   if (iters > 0) {
     stage(0);
@@ -833,127 +815,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   tile_reduce<TOK, 128>(reinterpret_cast<float*>(tile_raw), kw == 1, put,
                         [&](int tok, int c, float v) {
                           const int r = blockIdx.x * 128 + c;
-                          if (tok0 + tok < T && r < m)
-                            y[(int64_t)(tok0 + tok) * m + r] = __float2bfloat16_rn(4.f * v);
-                        });
-}
-
-// transposed: dx[t, j] = sum_i W[i, j] dy[t, i].  Warp (cw, kw) takes code words 8 cw .. 8 cw + 7
-// of the tile's 32 (64 columns) and half of the 128 rows of a step, 16 rows an MMA: lane (g, t)
-// loads word g of rows 4 t .. 4 t + 3; halves of two rows' words side by side give bf16 pairs
-// along the rows, which the MMA sums over.
-template <int NT, int GS>
-__global__ void __launch_bounds__(kTileThreads, NT <= 4 ? 2 : 1)
-    k_q4_tile_cols(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
-                   const __nv_bfloat16* __restrict__ dy, __nv_bfloat16* __restrict__ dx, int T,
-                   int m, int n, int steps_per_cta) {
-  extern __shared__ __align__(16) unsigned char tile_raw[];
-  constexpr int TOK = 8 * NT, LDB = 288, STAGE = TOK * LDB;
-  constexpr int SG = 128 / GS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int cw = warp & 3, kw = warp >> 2;
-  const int tok0 = blockIdx.y * TOK;
-  const int L = min((int)blockIdx.x * 32 + cw * 8 + g, n / 8 - 1);  // code word of the lane
-  const int blk = L >> 4, wi = L & 15;
-  const int64_t base = (int64_t)blk * m;
-  const uint32_t* c32 = reinterpret_cast<const uint32_t*>(codes) + base * 16 + wi;
-  const uint16_t* sc16 =
-      reinterpret_cast<const uint16_t*>(scales) + base * SG + (wi & 3) / (GS / 32);
-  const int nsteps = (m + 127) / 128;
-  const int s_first = blockIdx.z * steps_per_cta;
-  const int iters = max(0, min(nsteps, s_first + steps_per_cta) - s_first);
-  const bool vec = m % 8 == 0;
-  float acc[NT][4][4];
-#pragma unroll
-  for (int a = 0; a < NT; ++a)
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[a][p][c] = 0.f;
-  uint32_t cd[4][4];
-  uint16_t sc[4][4];
-  auto load_codes = [&](int it) {
-    const int i0 = (s_first + it) * 128 + kw * 64 + 4 * t;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        // rows past the end: zero dy; the last row's word and scale again (its own group, so
-        // nothing enters that is not there already)
-        const int64_t row = min(i0 + 16 * q + r, m - 1);
-        cd[q][r] = __ldg(c32 + row * 16);
-        sc[q][r] = __ldg(sc16 + row * SG);
-      }
-  };
-  auto stage = [&](int it) {
-    stage_tokens<TOK, LDB>(tile_raw + (it & 1) * STAGE, dy, tok0, T, (s_first + it) * 128, m, vec);
-  };
-  if (iters > 0) {
-    stage(0);
-    load_codes(0);
-  }
-  for (int it = 0; it < iters; ++it) {
-    if (it + 1 < iters) {
-      stage(it + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    __syncthreads();
-    uint32_t cur[4][4], s01[4], s23[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) cur[q][r] = cd[q][r];
-      s01[q] = sc[q][0] | ((uint32_t)sc[q][1] << 16);
-      s23[q] = sc[q][2] | ((uint32_t)sc[q][3] << 16);
-    }
-    if (it + 1 < iters) load_codes(it + 1);
-    const unsigned char* xs = tile_raw + (it & 1) * STAGE + kw * 128 + t * 8;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t lo01 = __byte_perm(cur[q][0], cur[q][1], 0x5410);
-      const uint32_t hi01 = __byte_perm(cur[q][0], cur[q][1], 0x7632);
-      const uint32_t lo23 = __byte_perm(cur[q][2], cur[q][3], 0x5410);
-      const uint32_t hi23 = __byte_perm(cur[q][2], cur[q][3], 0x7632);
-      uint2 b[NT];
-#pragma unroll
-      for (int a = 0; a < NT; ++a)
-        b[a] = *reinterpret_cast<const uint2*>(xs + (a * 8 + g) * LDB + q * 32);
-      uint32_t e0[4], e1[4], e2[4], e3[4];
-      q4_unpack(lo01, e0);
-      q4_unpack(hi01, e1);
-      q4_unpack(lo23, e2);
-      q4_unpack(hi23, e3);
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t a0 = bf2_mul(e0[p], s01[q]), a1 = bf2_mul(e1[p], s01[q]);
-        const uint32_t a2 = bf2_mul(e2[p], s23[q]), a3 = bf2_mul(e3[p], s23[q]);
-#pragma unroll
-        for (int a = 0; a < NT; ++a) mma16816(acc[a][p], a0, a1, a2, a3, b[a].x, b[a].y);
-      }
-    }
-    __syncthreads();
-  }
-  // lane's value (a, p, c): token 8 a + 2 t + (c & 1), column 2 p + (c >> 1) of word 8 cw + g
-  auto put = [&](float* buf, int ld, bool add) {
-#pragma unroll
-    for (int a = 0; a < NT; ++a)
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float* q = buf + (a * 8 + 2 * t + (c & 1)) * ld + 8 * (8 * cw + g) + 2 * p + (c >> 1);
-          *q = add ? acc[a][p][c] + *q : acc[a][p][c];
-        }
-  };
-  tile_reduce<TOK, 256>(reinterpret_cast<float*>(tile_raw), kw == 1, put,
-                        [&](int tok, int c, float v) {
-                          // word l of the row: columns 128 (l / 16) + 32 (l % 4) + 8 (l / 4 % 4)
-                          const int l = blockIdx.x * 32 + c / 8;
-                          const int j = (l >> 4) * 128 + 32 * (l & 3) + 8 * ((l >> 2) & 3) + (c & 7);
-                          if (tok0 + tok < T && l < n / 8)
-                            dx[(int64_t)(tok0 + tok) * n + j] = __float2bfloat16_rn(4.f * v);
+                          if (tok < T && r < m)
+                            y[(int64_t)tok * m + r] = __float2bfloat16_rn(4.f * v);
                         });
 }
 
@@ -1158,12 +1021,11 @@ cudaError_t cols8(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream
   return e;
 }
 
-// A tile kernel with its summed axis split over a cluster: as many shares (at most 8) as keep
-// the grid within one wave of `per_sm` CTAs an SM, and at least `min_steps` steps a share.
-template <typename Kern>
-cudaError_t launch_tiles(Kern kern, const Q4Weight& w, const void* x, void* y, int T, int tiles,
-                         int tok, int steps, int min_steps, int per_sm, int smem, bool* attr_done,
-                         cudaStream_t s) {
+template <int GS>
+cudaError_t rows16(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  auto kern = k_q4_tile_rows<2, GS>;
+  constexpr int smem = tile_row_smem(2);
+  static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
@@ -1173,14 +1035,15 @@ cudaError_t launch_tiles(Kern kern, const Q4Weight& w, const void* x, void* y, i
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  const int ttiles = (T + tok - 1) / tok;
-  int64_t splits = (int64_t)per_sm * num_sms() / ((int64_t)tiles * ttiles);
-  if (splits > steps / min_steps) splits = steps / min_steps;
+  // shares of the blocks: one wave of two CTAs an SM, at least two blocks a share
+  const int tiles = (w.m + 127) / 128, steps = w.n / 128;
+  int64_t splits = 2ll * num_sms() / tiles;
+  if (splits > steps / 2) splits = steps / 2;
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   const int per = (int)((steps + splits - 1) / splits);
-  splits = (steps + per - 1) / per;  // every share has a step
+  splits = (steps + per - 1) / per;  // every share has a block
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, ttiles, (unsigned)splits);
+  cfg.gridDim = dim3(tiles, 1, (unsigned)splits);
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -1197,33 +1060,6 @@ cudaError_t launch_tiles(Kern kern, const Q4Weight& w, const void* x, void* y, i
       static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), T, w.m, w.n, per);
   end_launch("gemm_w0", s);
   return e;
-}
-
-template <int NT, int GS>
-cudaError_t tile_rows_t(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  static bool attr_done[64] = {false};
-  return launch_tiles(k_q4_tile_rows<NT, GS>, w, x, y, T, (w.m + 127) / 128, 8 * NT, w.n / 128, 2,
-                      2, tile_row_smem(NT), attr_done, s);
-}
-template <int NT, int GS>
-cudaError_t tile_cols_t(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
-  static bool attr_done[64] = {false};
-  return launch_tiles(k_q4_tile_cols<NT, GS>, w, dy, dx, T, (w.n + 255) / 256, 8 * NT,
-                      (w.m + 127) / 128, 1, NT <= 4 ? 2 : 1, tile_col_smem(NT), attr_done, s);
-}
-template <int GS>
-cudaError_t rows_gs(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  if (T <= 8) return rows8<GS>(w, x, y, T, s);
-  if (T <= 16) return tile_rows_t<2, GS>(w, x, y, T, s);
-  if (T <= 32) return tile_rows_t<4, GS>(w, x, y, T, s);
-  return tile_rows_t<8, GS>(w, x, y, T, s);
-}
-template <int GS>
-cudaError_t cols_gs(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream_t s) {
-  if (T <= 8) return cols8<GS>(w, dy, dx, T, s);
-  if (T <= 16) return tile_cols_t<2, GS>(w, dy, dx, T, s);
-  if (T <= 32) return tile_cols_t<4, GS>(w, dy, dx, T, s);
-  return tile_cols_t<8, GS>(w, dy, dx, T, s);
 }
 
 template <int NT, bool GATHER>
@@ -1275,17 +1111,19 @@ cudaError_t launch_dequant_q4(const Q4Weight& w, void* out, int elem_bytes, cuda
 #undef Q4_DEQ
 }
 
+#define Q4_BY_GROUP(f)                                                            \
+  (w.group == 32 ? f<32>(w, x, y, T, s) : w.group == 64 ? f<64>(w, x, y, T, s) \
+                                                        : f<128>(w, x, y, T, s))
 cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                               cudaStream_t s) {
   if (T <= 0 || w.m <= 0 || w.n <= 0) return cudaSuccess;
-  if (!transpose)
-    return w.group == 32   ? rows_gs<32>(w, x, y, T, s)
-           : w.group == 64 ? rows_gs<64>(w, x, y, T, s)
-                           : rows_gs<128>(w, x, y, T, s);
-  return w.group == 32   ? cols_gs<32>(w, x, y, T, s)
-         : w.group == 64 ? cols_gs<64>(w, x, y, T, s)
-                         : cols_gs<128>(w, x, y, T, s);
+  if (T <= 8) return transpose ? Q4_BY_GROUP(cols8) : Q4_BY_GROUP(rows8);
+  // 9 to 16 tokens on many rows: the warp-level form (13824 x 5120: 20 us against 28, where the
+  // tcgen05 form's tiles leave a quarter of the SMs idle; 5120 x 5120: 14 both)
+  if (!transpose && T <= 16 && w.m >= 64 * 128) return Q4_BY_GROUP(rows16);
+  return launch_umma_q4(w, x, y, T, transpose, s);
 }
+#undef Q4_BY_GROUP
 
 cudaError_t launch_bd_gather(const void* G, const void* x, void* out, void* save_u,
                              const int32_t* idx, int T, int width, int b, cudaStream_t s) {

@@ -15,6 +15,8 @@
 //   warps 2, 3   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
 //                vectors, words put together and stored by both warps
 //   warps 4 ..   G groups that convert every G-th chunk each; then the epilogue
+// A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
+// chunk took with a commit each, conversion aside) come once for both.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.
 #include <cuda.h>
@@ -38,25 +40,25 @@ constexpr int kABytes = 128 * 64 * 2;
 // of it waiting, so many chunks have to be on their way at once: as many groups and stages as
 // shared memory holds.  Two groups of four warps with three stages, two CTAs an SM: 16.5 us at T = 16,
 // 5120 x 5120, of which 11.5 remain without any conversion.
-//   G <= STAGES and slots visited by the same groups every time, so that no wait is two phases of
-//   its barrier ahead: SLOTS is a multiple of G / 2 tiles (forward), of G (transposed).
+//   G <= chunks in the stages, and SLOTS a multiple of G / 2 (a slot is visited by the same two
+//   groups every time), so that no wait is two phases of its barrier ahead.
 template <int NT, bool TR>
 struct QCfg {
-  static constexpr int B = NT * 128;                      // bytes of the tokens' operand a stage
-  static constexpr int STAGES = NT <= 64 ? 6 : NT == 128 ? 5 : 4;
-  static constexpr int G = NT <= 64 ? 6 : NT == 128 ? 4 : 2;
+  static constexpr int B = NT * 128;                      // bytes of the tokens' operand a chunk
+  static constexpr int STAGES = NT <= 32 ? 4 : NT <= 128 ? 3 : 2;  // of two chunks
+  static constexpr int G = NT <= 32 ? 8 : NT == 64 ? 6 : NT == 128 ? 4 : 2;
   static constexpr int GT = NT <= 64 ? 64 : NT == 128 ? 128 : 256;  // threads of a group
   static constexpr int threads = 128 + G * GT;
-  // forward: tiles of 128 rows x 128 columns, two chunks; transposed: 64 rows x 128 columns
-  static constexpr int SLOTS = (NT <= 64 ? 6 : NT == 128 ? 4 : 2) * (TR ? 2 : 1);
-  static constexpr int CODES = TR ? 4096 : 8192;
-  static constexpr int SLOT = CODES + (TR ? 512 : 1024);
-  static constexpr int smem = 1024 + STAGES * (kABytes + B) + SLOTS * SLOT + 512;
+  // tiles of 128 rows x 128 columns: two chunks in either direction
+  static constexpr int SLOTS = NT <= 32 ? 4 : NT == 64 ? 6 : 2;
+  static constexpr int CODES = 8192;
+  static constexpr int SLOT = CODES + 1024;
+  static constexpr int smem = 1024 + 2 * STAGES * (kABytes + B) + SLOTS * SLOT + 512;
   static constexpr int sums = NT * 132 * 4;  // overlays the stages
   static constexpr uint32_t tmem_cols = NT < 32 ? 32 : NT;
-  static_assert(G <= STAGES && SLOTS % (TR ? G : G / 2) == 0, "phases");
+  static_assert(G <= 2 * STAGES && SLOTS % (G / 2) == 0, "phases");
   static_assert(smem <= 227 * 1024 && threads <= 1024, "resources");
-  static_assert(sums <= STAGES * (kABytes + B), "sums fit the stages");
+  static_assert(sums <= 2 * STAGES * (kABytes + B), "sums fit the stages");
   static_assert(8 * (2 * STAGES + 2 * SLOTS + 2) <= 512, "barriers");
 };
 
@@ -67,7 +69,7 @@ struct ParamsQ {
   __nv_bfloat16* y;
   int T, m, n, sg;         // sg: scales per row and block
   int K, out;              // length of the summed axis, of the output rows
-  int chunks, per_cta;     // K chunks in all, per CTA (even in the forward)
+  int chunks, per_cta;     // K chunks in all, per CTA (even)
   int bulk_scales;         // the scales of a tile are whole 16-byte runs
   int vec;                 // rows of x are whole 16-byte vectors
   int* err;
@@ -91,20 +93,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
 __device__ __forceinline__ void named_sync_q(int id, int count) {
   asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-// AND of v over the `count` threads meeting at named barrier `id`
-__device__ __forceinline__ bool group_all_q(bool v, int id, int count) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
 template <int NT, bool TR>
 __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
     k_umma_q4(const __grid_constant__ CUtensorMap tmX, const ParamsQ p) {
@@ -114,7 +102,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* gbase = smem_raw + (base - raw);
-  const uint32_t sA = base, sB = sA + RS * kABytes, sQ = sB + RS * C::B;
+  const uint32_t sA = base, sB = sA + 2 * RS * kABytes, sQ = sB + 2 * RS * C::B;
   const uint32_t sBar = sQ + C::SLOTS * C::SLOT;
   auto full_bar = [&](int s) { return sBar + 8u * s; };
   auto empty_bar = [&](int s) { return sBar + 8u * (RS + s); };
@@ -127,17 +115,18 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   const int row0 = blockIdx.x * 128;  // forward: rows of W; transposed: columns
   const int tok0 = blockIdx.y * NT;
   const int c_first = blockIdx.z * p.per_cta;
-  const int cnt = min(p.per_cta, p.chunks - c_first);  // K chunks of this CTA, >= 1
+  // K chunks of this CTA, a whole number of pairs (the last one may lie past the sum: zeros)
+  const int cnt = min(p.per_cta, (p.chunks - c_first + 1) / 2 * 2);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < RS; ++s) {
-      // the converter group; the TMA thread (and its bytes), or the 64 token loaders
-      mbar_init(full_bar(s), 1 + (p.vec ? 1 : 64));
+      // the converter groups of its chunks; the TMA thread (and its bytes), or the 64 token loaders
+      mbar_init(full_bar(s), 2 + (p.vec ? 1 : 64));
       mbar_init(empty_bar(s), 1);
     }
     for (int j = 0; j < C::SLOTS; ++j) {
       mbar_init(qfull_bar(j), 1);
-      mbar_init(qfree_bar(j), TR ? 1 : 2);  // the groups that read the slot
+      mbar_init(qfree_bar(j), 2);  // the groups that read the slot
     }
     mbar_init(done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -156,19 +145,18 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ codes and scales
     if (lane == 0) {
-      constexpr int STEP = TR ? 1 : 2;  // chunks per tile
-      int it = 0;
+      int tile = 0;
       bool ok = true;
-      for (; it < cnt; it += STEP) {
-        const int tile = it / STEP, slot = tile % C::SLOTS, use = tile / C::SLOTS;
+      for (; tile < cnt / 2; ++tile) {
+        const int slot = tile % C::SLOTS, use = tile / C::SLOTS;
         if (!mbar_wait(qfree_bar(slot), (use & 1) ^ 1, p.err, p.wait_ns)) {
           ok = false;
           break;
         }
-        const int k = (c_first + it) * 64;
+        const int k = (c_first + 2 * tile) * 64;
         // forward: rows row0 .. of block k / 128; transposed: rows k .. of block row0 / 128
         const int64_t row = TR ? (int64_t)blockIdx.x * p.m + k : (int64_t)(k >> 7) * p.m + row0;
-        const uint32_t rows = (uint32_t)min(TR ? 64 : 128, p.m - (TR ? k : row0));
+        const uint32_t rows = (uint32_t)min(128, p.m - (TR ? k : row0));
         const uint32_t sbytes = p.bulk_scales ? rows * 2u * (uint32_t)p.sg : 0u;
         mbar_expect_tx(qfull_bar(slot), rows * 64u + sbytes);
         const uint32_t dst = sQ + slot * C::SLOT;
@@ -176,23 +164,25 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
         if (sbytes) bulk_load_q(dst + C::CODES, p.scales + row * p.sg, sbytes, qfull_bar(slot));
       }
       if (!ok)  // no load may still be in flight into this CTA's shared memory when it leaves
-        for (int j = (it > C::SLOTS * STEP ? it - C::SLOTS * STEP : 0); j < it; j += STEP)
-          mbar_drain_wait(qfull_bar((j / STEP) % C::SLOTS), ((j / STEP) / C::SLOTS) & 1);
+        for (int j = (tile > C::SLOTS ? tile - C::SLOTS : 0); j < tile; ++j)
+          mbar_drain_wait(qfull_bar(j % C::SLOTS), (j / C::SLOTS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((TR ? 1u : 0u) << 15) |
                              ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-      for (int it = 0; it < cnt; ++it) {
+      for (int it = 0; it < cnt / 2; ++it) {
         const int s = it % RS;
         if (!mbar_wait(full_bar(s), (it / RS) & 1, p.err, p.wait_ns)) break;
         tc_fence_after();
-        const uint32_t a = sA + s * kABytes, b = sB + s * C::B;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16(tmem, TR ? make_desc(a + kk * 2048, 8192, 1024) : make_desc(a + kk * 32, 16, 1024),
-                    make_desc(b + kk * 32, 16, 1024), idesc, (it > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t a = sA + (2 * s + kk / 4) * kABytes, b = sB + (2 * s + kk / 4) * C::B;
+          const uint32_t k4 = kk & 3;
+          umma_bf16(tmem, TR ? make_desc(a + k4 * 2048, 8192, 1024) : make_desc(a + k4 * 32, 16, 1024),
+                    make_desc(b + k4 * 32, 16, 1024), idesc, (it > 0 || kk > 0) ? 1u : 0u);
+        }
         umma_commit(empty_bar(s));
       }
       // every MMA issued here completes before TMEM and the stages are used again
@@ -205,66 +195,86 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
       if (tid == 0) {
         int it = 0;
         bool ok = true;
-        for (; it < cnt; ++it) {
+        for (; it < cnt / 2; ++it) {
           const int st = it % RS;
           if (!mbar_wait(empty_bar(st), ((it / RS) & 1) ^ 1, p.err, p.wait_ns)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(full_bar(st), (uint32_t)C::B);
-          tma_load_2d(sB + st * C::B, &tmX, (c_first + it) * 64, tok0, full_bar(st));
+          mbar_expect_tx(full_bar(st), 2u * (uint32_t)C::B);
+          const int k = (c_first + 2 * it) * 64;
+          tma_load_2d(sB + 2 * st * C::B, &tmX, k, tok0, full_bar(st));
+          tma_load_2d(sB + (2 * st + 1) * C::B, &tmX, k + 64, tok0, full_bar(st));
         }
         if (!ok)  // no load may still be in flight into this CTA's shared memory when it leaves
           for (int j = (it > RS ? it - RS : 0); j < it; ++j)
             mbar_drain_wait(full_bar(j % RS), (j / RS) & 1);
       }
     } else {
-      // 8 values from any 2-byte boundary: the five aligned words around them, shifted together
-      constexpr int PER = NT * 8 / 64, GRP = PER < 8 ? PER : 8;  // 16-byte pieces a thread
-      const int64_t total = (int64_t)p.T * p.K;
-      for (int it = 0; it < cnt; ++it) {
-        const int st = it % RS;
-        const int k0 = (c_first + it) * 64;
-#pragma unroll 1
-        for (int g0 = 0; g0 < PER; g0 += GRP) {
-          uint32_t w[GRP][5];
+      // 8 values from any 2-byte boundary: the five aligned words around them, shifted together;
+      // a run of up to 8 such pieces a thread is loaded while the run before it is stored
+      constexpr int PER = NT * 8 / 64, RUN = PER < 8 ? PER : 8, RUNS = PER / RUN;  // a chunk
+      // The thread's pieces are column chunk c of tokens t0, t0 + 8, ..: 4 K words apart, so they
+      // start on the same side of a word.
+      const int t0 = tid >> 3, c = tid & 7;
+      const int64_t total = (int64_t)p.T * p.K, whole = total >> 1;  // values; whole words
+      const int64_t row = (int64_t)(tok0 + t0) * p.K;
+      const uint32_t sh = ((uint32_t)row & 1u) * 16u;
+      const uint32_t* x32 = reinterpret_cast<const uint32_t*>(p.x);
+      auto load = [&](int n, uint32_t (&w)[RUN][5]) {
+        const int k = (c_first + n / RUNS) * 64 + 8 * c;
+        const int i0 = (n % RUNS) * RUN;
+        int64_t word = ((row + k) >> 1) + (int64_t)i0 * 4 * p.K;
+        const bool col_on = n < cnt * RUNS && k < p.K;
 #pragma unroll
-          for (int i = 0; i < GRP; ++i) {
-            const int e = tid + 64 * (g0 + i), tok = e >> 3, k = k0 + 8 * (e & 7);
-            const bool on = tok0 + tok < p.T && k < p.K;
-            const int64_t first = on ? (int64_t)(tok0 + tok) * p.K + k : 0;
-            const int64_t word = first >> 1;
+        for (int i = 0; i < RUN; ++i) {
+          const bool on = col_on && tok0 + t0 + 8 * (i0 + i) < p.T;
+          const int have = on ? (int)min((int64_t)5, whole - word) : 0;
 #pragma unroll
-            for (int j = 0; j < 5; ++j) {
-              w[i][j] = 0;
-              // whole words of x; its last value alone when the count is odd
-              ld_u32_if(w[i][j], reinterpret_cast<const uint32_t*>(p.x) + word + j,
-                        on && 2 * (word + j) + 1 < total);
-              if (on && 2 * (word + j) + 1 == total) w[i][j] = ld_u16(p.x + total - 1);
-            }
+          for (int j = 0; j < 5; ++j) {
+            w[i][j] = 0;
+            ld_u32_if(w[i][j], x32 + word + j, j < have);
           }
-          if (g0 == 0 && !mbar_wait(empty_bar(st), ((it / RS) & 1) ^ 1, p.err, p.wait_ns)) {
-            it = cnt;
-            break;
-          }
+          // the last value of x alone when their count is odd
+          if (on && have < 5 && (total & 1)) {
 #pragma unroll
-          for (int i = 0; i < GRP; ++i) {
-            const int e = tid + 64 * (g0 + i), tok = e >> 3, c = e & 7, k = k0 + 8 * c;
-            const uint32_t sh = ((uint32_t)((int64_t)(tok0 + tok) * p.K + k) & 1u) * 16u;
-            uint32_t v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = __funnelshift_r(w[i][j], w[i][j + 1], sh);
-              // values past the end of the row
-              if (k + 2 * j + 1 >= p.K) v[j] &= k + 2 * j < p.K ? 0xffffu : 0u;
-            }
-            sts128(sB + st * C::B + tok * 128 + ((c ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 5; ++j) ld_u16_if(w[i][j], p.x + total - 1, word + j == whole);
           }
+          word += 4 * (int64_t)p.K;
         }
-        if (it < cnt) {
+      };
+      bool ok = true;
+      auto put = [&](int n, const uint32_t (&w)[RUN][5]) {
+        const int it = n / RUNS, st = (it >> 1) % RS;
+        if (n % (2 * RUNS) == 0)
+          ok = ok && mbar_wait(empty_bar(st), (((it >> 1) / RS) & 1) ^ 1, p.err, p.wait_ns);
+        if (!ok) return;
+        const uint32_t dst = sB + (2 * st + (it & 1)) * C::B;
+        const int k0 = (c_first + it) * 64;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+          const int tok = t0 + 8 * ((n % RUNS) * RUN + i), k = k0 + 8 * c;
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j] = __funnelshift_r(w[i][j], w[i][j + 1], sh);
+            // values past the end of the row
+            if (k + 2 * j + 1 >= p.K) v[j] &= k + 2 * j < p.K ? 0xffffu : 0u;
+          }
+          sts128(dst + tok * 128 + ((c ^ (tok & 7)) << 4), v[0], v[1], v[2], v[3]);
+        }
+        if (n % (2 * RUNS) == 2 * RUNS - 1) {  // both chunks of the stage are written
           fence_async_smem();
           mbar_arrive(full_bar(st));
         }
+      };
+      uint32_t wa[RUN][5], wb[RUN][5];
+      load(0, wa);
+      for (int n = 0; n < cnt * RUNS; n += 2) {  // (cnt is even)
+        load(n + 1, wb);
+        put(n, wa);
+        load(n + 2, wa);
+        put(n + 1, wb);
       }
     }
   } else {
@@ -273,36 +283,36 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
     const int grp = (threadIdx.x - 128) / GT, gt = (threadIdx.x - 128) % GT;
     const int bar_id = 1 + grp;
     const uint32_t sg = (uint32_t)p.sg;
+    bool ok = true;
     for (int it = grp; it < cnt; it += G) {
-      const int s = it % RS;
-      const int tile = TR ? it : it >> 1, slot = tile % C::SLOTS, use = tile / C::SLOTS;
+      const int s = (it >> 1) % RS;
+      const int tile = it >> 1, slot = tile % C::SLOTS, use = tile / C::SLOTS;
       const int k = (c_first + it) * 64;
-      int got = 1;
-      if (lane == 0)
-        got = mbar_wait(qfull_bar(slot), use & 1, p.err, p.wait_ns) &&
-              mbar_wait(empty_bar(s), ((it / RS) & 1) ^ 1, p.err, p.wait_ns);
-      // every thread of the group takes the same branch (a failed wait of any warp)
-      if (!group_all_q(__shfl_sync(0xffffffffu, got, 0) != 0, bar_id, GT)) break;
-      // both phases have completed: every lane acquires them (returns at once)
-      while (!mbar_try_wait(qfull_bar(slot), use & 1)) {
-      }
-      while (!mbar_try_wait(empty_bar(s), ((it / RS) & 1) ^ 1)) {
-      }
-      const uint32_t src = sQ + slot * C::SLOT, dst = sA + s * kABytes;
-      // forward: rows past the weight's end give outputs that are not stored; transposed: rows
-      // past the end of the sum have to give zeros
+      // (every thread of a group goes through every chunk, so that the group's barrier always
+      // meets; once a wait has run out the others end at once, and nothing more is announced)
+      ok = ok && mbar_wait(qfull_bar(slot), use & 1, p.err, p.wait_ns) &&
+           mbar_wait(empty_bar(s), (((it >> 1) / RS) & 1) ^ 1, p.err, p.wait_ns);
+      const uint32_t dst = sA + (2 * s + (it & 1)) * kABytes;
+      // forward: the chunk is half of the tile's columns; rows past the weight's end give outputs
+      // that are not stored.  transposed: it is half of the tile's rows; rows past the end of the
+      // sum have to give zeros.
+      const uint32_t first = TR ? 64u * ((uint32_t)it & 1u) : 0u;  // row of the tile
+      const uint32_t src = sQ + slot * C::SLOT + first * 64u;
+      const uint32_t ssrc = sQ + slot * C::SLOT + C::CODES + first * sg * 2u;
       const int rows = TR ? min(64, p.m - k) : min(128, p.m - row0);
-      if (p.bulk_scales && (!TR || rows == 64)) {
-        q4_convert<TR ? 64 : 128, GT, true>(src, src + C::CODES, dst, gt, (uint32_t)it & 1u, sg,
-                                            rows, nullptr);
+      if (!ok) {
+      } else if (p.bulk_scales && (!TR || rows == 64)) {
+        q4_convert<TR ? 64 : 128, GT, true>(src, ssrc, dst, gt, (uint32_t)it & 1u, sg, rows, nullptr);
       } else {
-        const int64_t row = TR ? (int64_t)blockIdx.x * p.m + k : (int64_t)(k >> 7) * p.m + row0;
-        q4_convert<TR ? 64 : 128, GT, false>(src, src + C::CODES, dst, gt, (uint32_t)it & 1u, sg,
-                                             rows, p.bulk_scales ? nullptr : p.scales + row * p.sg);
+        // (a chunk past the sum: rows <= 0, zeros; its scales' place is the last row's)
+        const int64_t row = TR ? (int64_t)blockIdx.x * p.m + min(k, p.m - 1)
+                               : (int64_t)(k >> 7) * p.m + row0;
+        q4_convert<TR ? 64 : 128, GT, false>(src, ssrc, dst, gt, (uint32_t)it & 1u, sg, rows,
+                                             p.bulk_scales ? nullptr : p.scales + row * p.sg);
       }
       fence_async_smem();  // the generic-proxy stores, then the tensor core's reads
       named_sync_q(bar_id, GT);
-      if (gt == 0) {
+      if (gt == 0 && ok) {
         mbar_arrive(full_bar(s));
         mbar_arrive(qfree_bar(slot));
       }
@@ -405,15 +415,14 @@ cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStrea
   const int tiles = (p.out + 127) / 128, ttiles = (T + NT - 1) / NT;
   // shares of the summed axis: a grid within one wave with a seventh of the places to spare (a
   // cluster needs all its places in one group of SMs), at least 4 chunks a share, at most 8
-  const int unit = TR ? 1 : 2;
-  const int units = (p.chunks + unit - 1) / unit;
+  const int units = (p.chunks + 1) / 2;  // pairs of chunks
   int64_t splits = (int64_t)num_sms() * 17 / 20 / ((int64_t)tiles * ttiles);
   if (splits > p.chunks / 4) splits = p.chunks / 4;
   splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   if (splits == 7) splits = 6;
   const int per = (int)((units + splits - 1) / splits);
   splits = (units + per - 1) / per;  // every share has a chunk
-  p.per_cta = per * unit;
+  p.per_cta = per * 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, ttiles, (unsigned)splits);
   cfg.blockDim = dim3(C::threads);
@@ -440,7 +449,8 @@ template <bool TR>
 cudaError_t launch_tr(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
   if (T <= 16) return launch_q<16, TR>(w, x, y, T, s);
   if (T <= 32) return launch_q<32, TR>(w, x, y, T, s);
-  if (T <= 64) return launch_q<64, TR>(w, x, y, T, s);
+  // (rows that the 64 loader threads put together: small token tiles)
+  if (T <= 64 || (TR ? w.m : w.n) % 8 != 0) return launch_q<64, TR>(w, x, y, T, s);
   if (T <= 128) return launch_q<128, TR>(w, x, y, T, s);
   return launch_q<256, TR>(w, x, y, T, s);
 }

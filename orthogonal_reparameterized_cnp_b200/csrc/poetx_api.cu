@@ -1060,10 +1060,13 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
   g.batch = 1; g.out_f32 = 0;
   g.D = out; g.ldd = g.N;
   if (w.q4.codes) {
-    if (T <= 8) return launch_q4_product(w.q4, in, out, T, !forward, s);
-    if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4))
+    // the CTA-pair kernel where its 256 x 256 tiles fill half of the pairs (T x out x sum: 512 x
+    // 5120 x 5120 takes 47 us on it and 44 with the weight as the M operand, 256 tokens 45 and 25,
+    // 1024 tokens 83 and 85, 1024 x 13824 x 5120 125 and 133)
+    if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4) &&
+        4ll * ((T + 255) / 256) * (g.N / 256) > num_sms())
       return launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
-    return launch_umma_q4(w.q4, in, out, T, !forward, s);
+    return launch_q4_product(w.q4, in, out, T, !forward, s);
   }
   if (gemm_pairs_enabled() && umma_pair_eligible(g) && n % 16 == 0) {  // converted on chip
     PairQ8 q;

@@ -103,10 +103,10 @@ struct Q4Weight {
 cudaError_t launch_merge_q4(const void* W0, const int32_t* perm_R, const int32_t* perm_P,
                             const Q4Weight& w, int elem_bytes, cudaStream_t s);
 cudaError_t launch_dequant_q4(const Q4Weight& w, void* out, int elem_bytes, cudaStream_t s);
-// y[T, m] = x[T, n] W^T, or (transpose) y[T, n] = x[T, m] W: the few-token kernels, any T
+// y[T, m] = x[T, n] W^T, or (transpose) y[T, n] = x[T, m] W; any T
 cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                               cudaStream_t s);
-// the same on tcgen05 with the weight as the M operand (kernels_umma_q4.cu), any T
+// the same on tcgen05 with the weight as the M operand (kernels_umma_q4.cu)
 cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                            cudaStream_t s);
 // few-token block products fused with their index maps (bf16; width % b == 0, b % 128 == 0):

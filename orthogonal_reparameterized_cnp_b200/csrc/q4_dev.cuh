@@ -152,7 +152,7 @@ __device__ __forceinline__ void q4_convert(uint32_t src, uint32_t ssrc, uint32_t
       s0 = a;
       s1 = b;
     } else {
-      const uint16_t* g = gs + (int64_t)min((int)r, rows - 1) * sg;
+      const uint16_t* g = gs + (int64_t)min((int)r, max(rows - 1, 0)) * sg;
       s0 = ld_u16(g + i0);
       s1 = ld_u16(g + i1);
     }

@@ -157,7 +157,11 @@ def test_few_token_products(P, m, n, group, transpose):
                                                (777, 768, 1024, 64, True),
                                                (1000, 520, 768, 128, True),
                                                (513, 999, 640, 32, True),
-                                               (600, 512, 512, 64, False)])
+                                               (600, 512, 512, 64, False),
+                                               (1030, 2560, 2560, 64, True),
+                                               (1100, 2560, 2816, 32, True),
+                                               (1300, 2304, 2560, 128, True),
+                                               (150, 1001, 384, 64, True)])
 def test_many_token_products(P, T, m, n, group, pairs, transpose):
     import torch
     q, s, W = _packed(P, m, n, group, T + m)
@@ -316,10 +320,11 @@ def test_layer_step_matches_the_oracle(P, T, n, m, b, group):
     assert torch.equal(yd, y)
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
-def test_layer_equals_the_bf16_layer_on_the_dequantised_weight(P, T):
+@pytest.mark.parametrize("T,n,m", [(1, 512, 512), (40, 512, 512), (300, 512, 512),
+                                   (1300, 2048, 2048)])
+def test_layer_equals_the_bf16_layer_on_the_dequantised_weight(P, T, n, m):
     import torch
-    n, m, b, group = 512, 512, 256, 64
+    b, group = 256, 64
     inp, L, pP, pR = _layer(P, T, n, m, b, group)
     x, dy = tensor(inp.x, torch.bfloat16), tensor(inp.dy, torch.bfloat16)
     y, dx = torch.empty_like(dy), torch.empty_like(x)
@@ -335,7 +340,7 @@ def test_layer_equals_the_bf16_layer_on_the_dequantised_weight(P, T):
     P.linear_fwd(L.desc, x, GP, GR, W, y0, U, Ws, ws)
     P.linear_bwd(L.desc, x, dy, GP, GR, W, U, Ws, dx0, dGP, dGR, 0, ws)
     assert torch.equal(L.U, U)  # gathered bit for bit in either form
-    if T >= 256:  # the same tensor-core kernel on the same operands
+    if T >= 1024:  # the same tensor-core kernel on the same operands
         assert torch.equal(y, y0) and torch.equal(dx, dx0)
         assert torch.equal(L.dG[: L.nP], dGP) and torch.equal(L.dG[L.nP:], dGR)
     else:
