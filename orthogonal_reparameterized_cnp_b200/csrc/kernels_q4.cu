@@ -360,11 +360,14 @@ struct RowScales<4> {
   }
 };
 
-template <int GS, int WARPS>
+// HL: x comes and y goes as the sum of two bf16 numbers, hi + lo (16 significant bits), an MMA
+// each: the layer's intermediates of a few tokens are then not rounded to bf16.
+template <int GS, int WARPS, bool HL>
 __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     k_q4_rows(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
-              const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y, int T, int m,
-              int n) {
+              const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y,
+              const __nv_bfloat16* __restrict__ x_lo, __nv_bfloat16* __restrict__ y_lo, int T,
+              int m, int n) {
   constexpr int SG = 128 / GS, D = kRowD;  // SG: scales per row and block
   extern __shared__ __align__(16) unsigned char row_ring[];
   uint4 (*ring)[WARPS][64] = reinterpret_cast<uint4 (*)[WARPS][64]>(row_ring);  // [D]
@@ -378,8 +381,9 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
   uint32_t os = ((uint32_t)warp * (uint32_t)m + (uint32_t)ra) * SG;
   const uint32_t dc = (uint32_t)(rb - ra) * 4u, ds = (uint32_t)(rb - ra) * SG;
   const uint32_t step = (uint32_t)WARPS * (uint32_t)m;
-  const uint4* xp =
-      reinterpret_cast<const uint4*>(x + (int64_t)min(g, T - 1) * n) + warp * 16 + t;
+  const int64_t x0 = (int64_t)min(g, T - 1) * n + warp * 128 + t * 8;
+  const uint4* xp = reinterpret_cast<const uint4*>(x + x0);
+  const uint4* xlp = HL ? reinterpret_cast<const uint4*>(x_lo + x0) : nullptr;
   RowScales<SG> sa[2], sb[2];
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(&ring[0][warp][lane]);
   int left = cnt;  // blocks whose loads are to be issued
@@ -397,12 +401,18 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     sb[b].load(scales + (os + ds), on);
     os += step * SG;
   };
-  pdl_trigger();
-  pdl_wait();
   constexpr uint32_t kSlot = WARPS * 1024u;  // bytes of a ring stage
+  if (!HL) {
+    pdl_trigger();
+    pdl_wait();
+  }
 #pragma unroll
   for (int d = 0; d < D; ++d) load(slot0 + d * kSlot);
   load_scales(0, cnt > 0);
+  if (HL) {  // behind k_bd_rows, which lets this launch begin once all before it has ended
+    pdl_wait();
+    pdl_trigger();
+  }
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t slot = slot0;
   auto compute = [&](int b) {
@@ -410,6 +420,12 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
 #pragma unroll
     for (int w = 0; w < 4; ++w) xv[w] = ld_u4(xp + w * 4);
     xp += WARPS * 16;
+    uint4 xl[4];
+    if (HL) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) xl[w] = ld_u4(xlp + w * 4);
+      xlp += WARPS * 16;
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     const uint4 ca = lds_u4(slot), cb = lds_u4(slot + 512u);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
@@ -425,6 +441,10 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
       } else {
         mma16816(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
         mma16816(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
+      }
+      if (HL) {
+        mma16816(part, qa[0], qb[0], qa[1], qb[1], xl[w].x, xl[w].y);
+        mma16816(odd, qa[2], qb[2], qa[3], qb[3], xl[w].z, xl[w].w);
       }
       if ((w + 1) % (GS / 32) == 0) {
         const float a = sa[b].at(w / (GS / 32)), c = sb[b].at(w / (GS / 32));
@@ -455,7 +475,10 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += red[w][tok][r];  // fixed order
-    y[(int64_t)tok * m + row0 + r] = __float2bfloat16_rn(4.f * v);
+    const int64_t o = (int64_t)tok * m + row0 + r;
+    const __nv_bfloat16 hi = __float2bfloat16_rn(4.f * v);
+    y[o] = hi;
+    if (HL) y_lo[o] = __float2bfloat16_rn(4.f * v - __bfloat162float(hi));
   }
 }
 
@@ -821,82 +844,104 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// Block-diagonal product of a few tokens with its index map:
-//   out[t, o(jb + i)] = sum_k G_j[i, k] in[t, c(jb + k)]
-// gather: c = idx (U = X[:, p_P], V_j = U_j G_P,j^T; U is also written when `save` is given);
-// scatter: o = idx (Z_j = W_j G_R,j^T, Y[:, p_R[i]] = Z[:, i]).  One CTA: 16 rows of one block,
-// 8 NT tokens; its four warps split k and add their sums in a fixed order.
+// Block-diagonal product of up to 8 tokens with its index map, between the layer's unrounded
+// intermediates (hi + lo, see k_q4_rows):
+//   gather:  V_j = U_j G_P,j^T, U = X[:, p_P] (also written when `save` is given), V = out + lo;
+//   scatter: Z_j = W_j G_R,j^T, W = in + lo, Y[:, p_R[i]] = Z[:, i].
+// One CTA: 16 rows of one block; its four warps split k and add their sums in a fixed order.  A
+// lane reads the operands of its MMAs straight from global memory - 8 columns of its token, for
+// the gather by their indices - with everything of a warp in flight at once (KI = b / 128 steps).
+// Bound by latency: the layer's three launches overlap by what each can read before its
+// predecessor ends (G and the indices here, the codes in k_q4_rows).
 constexpr int kBdWarps = 4;
 
-template <int NT, bool GATHER>
+template <int KI, bool GATHER>
 __global__ void __launch_bounds__(32 * kBdWarps)
     k_bd_rows(const __nv_bfloat16* __restrict__ G, const __nv_bfloat16* __restrict__ in,
-              __nv_bfloat16* __restrict__ out, __nv_bfloat16* __restrict__ save,
-              const int32_t* __restrict__ idx, int T, int width, int b) {
-  extern __shared__ __align__(16) unsigned char bd_raw[];
-  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(bd_raw);  // [8 NT][b + 8]
-  __shared__ float red[kBdWarps][NT * 8][17];
-  pdl_trigger();
-  pdl_wait();
+              __nv_bfloat16* __restrict__ out, __nv_bfloat16* __restrict__ lo,
+              __nv_bfloat16* __restrict__ save, const int32_t* __restrict__ idx, int T,
+              int width) {
+  constexpr int b = 128 * KI, tiles = b / 16;
+  __shared__ float red[kBdWarps][8][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tiles = b / 16;
   const int j = blockIdx.x / tiles, i0 = (blockIdx.x - j * tiles) * 16;
-  const int tok0 = blockIdx.y * (8 * NT);
-  const int ld = b + 8;
-  for (int e = threadIdx.x; e < NT * 8 * b; e += 32 * kBdWarps) {
-    const int tok = e / b, k = e - tok * b;
-    __nv_bfloat16 v = __ushort_as_bfloat16(0);
-    if (tok0 + tok < T) {
-      unsigned c = (unsigned)(j * b + k);
-      if (GATHER) {
-        c = ld_u32(idx + c);
-        c = c < (unsigned)width ? c : (unsigned)width - 1;
-      }
-      v = __ushort_as_bfloat16((uint16_t)ld_u16(in + (int64_t)(tok0 + tok) * width + c));
-      if (GATHER && save && i0 == 0) save[(int64_t)(tok0 + tok) * width + j * b + k] = v;
+  const int k0 = warp * (32 * KI) + 8 * t;  // columns k0 + 32 i .. + 7 of the block
+  const int tok = min(g, T - 1);
+  if (GATHER) {
+    pdl_wait();
+    pdl_trigger();  // after the wait: what the next launch reads early was there before this one
+  }
+  uint4 ga[KI], gb[KI], xv[KI], xl[KI];
+  const __nv_bfloat16* gp = G + ((int64_t)j * b + i0 + g) * b + k0;
+  uint32_t c_out = 0;
+  if (GATHER) {
+    uint4 ci[KI][2];
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      ci[i][0] = ld_u4(idx + j * b + k0 + 32 * i);
+      ci[i][1] = ld_u4(idx + j * b + k0 + 32 * i + 4);
     }
-    xs[tok * ld + k] = v;
-  }
-  __syncthreads();
-  float acc[NT][4];
 #pragma unroll
-  for (int a = 0; a < NT; ++a)
+    for (int i = 0; i < KI; ++i) {
+      ga[i] = ld_u4(gp + 32 * i);
+      gb[i] = ld_u4(gp + 8 * b + 32 * i);
+    }
+    const __nv_bfloat16* x = in + (int64_t)tok * width;
+    uint32_t e[KI][8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[a][c] = 0.f;
-  const __nv_bfloat16* ga = G + ((int64_t)j * b + i0 + g) * b;
-  const __nv_bfloat16* gb = ga + 8 * (int64_t)b;
-  const int kw = b / kBdWarps;  // 32, 64 or 128
-  for (int k = warp * kw; k < (warp + 1) * kw; k += 32) {
-    const uint4 a = ld_u4(ga + k + 8 * t);
-    const uint4 c = ld_u4(gb + k + 8 * t);
+    for (int i = 0; i < KI; ++i) {
+      const uint32_t c[8] = {ci[i][0].x, ci[i][0].y, ci[i][0].z, ci[i][0].w,
+                             ci[i][1].x, ci[i][1].y, ci[i][1].z, ci[i][1].w};
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const uint4 xv = *reinterpret_cast<const uint4*>(xs + (q * 8 + g) * ld + k + 8 * t);
-      mma16816(acc[q], a.x, c.x, a.y, c.y, xv.x, xv.y);
-      mma16816(acc[q], a.z, c.z, a.w, c.w, xv.z, xv.w);
+      for (int q = 0; q < 8; ++q) e[i][q] = ld_u16(x + min(c[q], (uint32_t)width - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      xv[i] = make_uint4(e[i][0] | e[i][1] << 16, e[i][2] | e[i][3] << 16,
+                         e[i][4] | e[i][5] << 16, e[i][6] | e[i][7] << 16);
+      if (save && i0 == 0 && g < T)
+        *reinterpret_cast<uint4*>(save + (int64_t)g * width + j * b + k0 + 32 * i) = xv[i];
+    }
+  } else {
+    c_out = ld_u32(idx + j * b + i0 + (threadIdx.x & 15));
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      ga[i] = ld_u4(gp + 32 * i);
+      gb[i] = ld_u4(gp + 8 * b + 32 * i);
+    }
+    pdl_trigger();
+    pdl_wait();
+    const int64_t o = (int64_t)tok * width + j * b + k0;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      xv[i] = ld_u4(in + o + 32 * i);
+      xl[i] = ld_u4(lo + o + 32 * i);
     }
   }
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    red[warp][q * 8 + 2 * t][g] = acc[q][0];
-    red[warp][q * 8 + 2 * t + 1][g] = acc[q][1];
-    red[warp][q * 8 + 2 * t][g + 8] = acc[q][2];
-    red[warp][q * 8 + 2 * t + 1][g + 8] = acc[q][3];
-  }
-  __syncthreads();
-  for (int o = threadIdx.x; o < NT * 8 * 16; o += 32 * kBdWarps) {
-    const int tok = o >> 4, r = o & 15;
-    if (tok0 + tok >= T) continue;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kBdWarps; ++w) v += red[w][tok][r];
-    unsigned c = (unsigned)(j * b + i0 + r);
+  for (int i = 0; i < KI; ++i) {
+    mma16816(acc, ga[i].x, gb[i].x, ga[i].y, gb[i].y, xv[i].x, xv[i].y);
+    mma16816(acc, ga[i].z, gb[i].z, ga[i].w, gb[i].w, xv[i].z, xv[i].w);
     if (!GATHER) {
-      c = ld_u32(idx + c);
-      c = c < (unsigned)width ? c : (unsigned)width - 1;
+      mma16816(acc, ga[i].x, gb[i].x, ga[i].y, gb[i].y, xl[i].x, xl[i].y);
+      mma16816(acc, ga[i].z, gb[i].z, ga[i].w, gb[i].w, xl[i].z, xl[i].w);
     }
-    out[(int64_t)(tok0 + tok) * width + c] = __float2bfloat16_rn(v);
   }
+  red[warp][2 * t][g] = acc[0];
+  red[warp][2 * t + 1][g] = acc[1];
+  red[warp][2 * t][g + 8] = acc[2];
+  red[warp][2 * t + 1][g + 8] = acc[3];
+  __syncthreads();
+  const int ot = threadIdx.x >> 4, r = threadIdx.x & 15;  // an output each
+  if (ot >= T) return;
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kBdWarps; ++w) v += red[w][ot][r];
+  const uint32_t c = GATHER ? (uint32_t)(j * b + i0 + r) : min(c_out, (uint32_t)width - 1);
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  out[(int64_t)ot * width + c] = hi;
+  if (GATHER) lo[(int64_t)ot * width + c] = __float2bfloat16_rn(v - __bfloat162float(hi));
 }
 
 template <typename E, int GS, int MAXW>
@@ -969,23 +1014,29 @@ cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m
   return cudaGetLastError();
 }
 
-template <int GS, int WARPS>
-cudaError_t rows8_t(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  constexpr int smem = kRowD * WARPS * 1024;
+template <int GS, int WARPS, bool HL>
+cudaError_t rows8_t(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo, int T,
+                    cudaStream_t s) {
+  using B = __nv_bfloat16;
   begin_launch("gemm_w0", s);
   const cudaError_t e = launch_pdl(
-      k_q4_rows<GS, WARPS>, dim3((w.m + 15) / 16), dim3(32 * WARPS), smem, s, w.codes,
-      static_cast<const uint16_t*>(w.scales), static_cast<const __nv_bfloat16*>(x),
-      static_cast<__nv_bfloat16*>(y), T, w.m, w.n);
+      k_q4_rows<GS, WARPS, HL>, dim3((w.m + 15) / 16), dim3(32 * WARPS), kRowD * WARPS * 1024, s,
+      w.codes, static_cast<const uint16_t*>(w.scales), static_cast<const B*>(x),
+      static_cast<B*>(y), static_cast<const B*>(x_lo), static_cast<B*>(y_lo), T, w.m, w.n);
   end_launch("gemm_w0", s);
   return e;
 }
+template <int GS, bool HL>
+cudaError_t rows8_hl(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo,
+                     int T, cudaStream_t s) {
+  // eight warps share a row tile where four would leave fewer than 16 warps on an SM (5120 x 5120:
+  // 6.6 us against 9.4; 13824 x 5120: 12.6 against 11.6)
+  if ((w.m + 15) / 16 < 4 * num_sms()) return rows8_t<GS, 8, HL>(w, x, y, x_lo, y_lo, T, s);
+  return rows8_t<GS, 4, HL>(w, x, y, x_lo, y_lo, T, s);
+}
 template <int GS>
 cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  // eight warps share a row tile where four would leave fewer than 16 warps on an SM
-  const int tiles = (w.m + 15) / 16;
-  if (tiles < 4 * num_sms()) return rows8_t<GS, 8>(w, x, y, T, s);
-  return rows8_t<GS, 4>(w, x, y, T, s);
+  return rows8_hl<GS, false>(w, x, y, nullptr, nullptr, T, s);
 }
 
 template <int GS>
@@ -1062,28 +1113,27 @@ cudaError_t rows16(const Q4Weight& w, const void* x, void* y, int T, cudaStream_
   return e;
 }
 
-template <int NT, bool GATHER>
-cudaError_t bd_t(const void* G, const void* in, void* out, void* save, const int32_t* idx, int T,
-                 int width, int b, cudaStream_t s) {
-  auto kern = k_bd_rows<NT, GATHER>;
-  const size_t smem = (size_t)NT * 8 * (b + 8) * 2;
-  static bool attr_done[64] = {false};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) dev = 0;
-  if (!attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NT * 8 * (512 + 8) * 2);
-    if (e != cudaSuccess) return e;
-    attr_done[dev] = true;
-  }
+template <int KI, bool GATHER>
+cudaError_t bd_t(const void* G, const void* in, void* out, void* lo, void* save,
+                 const int32_t* idx, int T, int width, cudaStream_t s) {
+  using B = __nv_bfloat16;
   begin_launch("gemm_blockdiag", s);
-  const cudaError_t e = launch_pdl(
-      kern, dim3(width / 16, (T + 8 * NT - 1) / (8 * NT)), dim3(32 * kBdWarps), smem, s,
-      static_cast<const __nv_bfloat16*>(G), static_cast<const __nv_bfloat16*>(in),
-      static_cast<__nv_bfloat16*>(out), static_cast<__nv_bfloat16*>(save), idx, T, width, b);
+  const cudaError_t e =
+      launch_pdl(k_bd_rows<KI, GATHER>, dim3(width / 16), dim3(32 * kBdWarps), 0, s,
+                 static_cast<const B*>(G), static_cast<const B*>(in), static_cast<B*>(out),
+                 static_cast<B*>(lo), static_cast<B*>(save), idx, T, width);
   end_launch("gemm_blockdiag", s);
   return e;
+}
+template <bool GATHER>
+cudaError_t bd(const void* G, const void* in, void* out, void* lo, void* save, const int32_t* idx,
+               int T, int width, int b, cudaStream_t s) {
+  switch (b) {
+    case 128: return bd_t<1, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    case 256: return bd_t<2, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    case 512: return bd_t<4, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
@@ -1125,19 +1175,18 @@ cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, 
 }
 #undef Q4_BY_GROUP
 
-cudaError_t launch_bd_gather(const void* G, const void* x, void* out, void* save_u,
-                             const int32_t* idx, int T, int width, int b, cudaStream_t s) {
-  if (T <= 0) return cudaSuccess;
-  if (T <= 8) return bd_t<1, true>(G, x, out, save_u, idx, T, width, b, s);
-  if (T <= 16) return bd_t<2, true>(G, x, out, save_u, idx, T, width, b, s);
-  return bd_t<4, true>(G, x, out, save_u, idx, T, width, b, s);
-}
-cudaError_t launch_bd_scatter(const void* G, const void* in, void* y, const int32_t* idx, int T,
-                              int width, int b, cudaStream_t s) {
-  if (T <= 0) return cudaSuccess;
-  if (T <= 8) return bd_t<1, false>(G, in, y, nullptr, idx, T, width, b, s);
-  if (T <= 16) return bd_t<2, false>(G, in, y, nullptr, idx, T, width, b, s);
-  return bd_t<4, false>(G, in, y, nullptr, idx, T, width, b, s);
+cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
+                             void* y, void* U, void* V, void* V_lo, void* W, void* W_lo,
+                             const int32_t* perm_P, const int32_t* perm_R, int T, int b,
+                             cudaStream_t s) {
+  if (T <= 0 || T > 8) return cudaErrorInvalidValue;
+  cudaError_t e = bd<true>(G_P, x, V, V_lo, U, perm_P, T, w.n, b, s);
+  if (e != cudaSuccess) return e;
+  e = w.group == 32   ? rows8_hl<32, true>(w, V, W, V_lo, W_lo, T, s)
+      : w.group == 64 ? rows8_hl<64, true>(w, V, W, V_lo, W_lo, T, s)
+                      : rows8_hl<128, true>(w, V, W, V_lo, W_lo, T, s);
+  if (e != cudaSuccess || !y) return e;
+  return bd<false>(G_R, W, y, W_lo, nullptr, perm_R, T, w.m, b, s);
 }
 
 }  // namespace poetx

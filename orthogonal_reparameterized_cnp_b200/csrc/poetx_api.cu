@@ -1009,7 +1009,8 @@ cudaError_t bf16_w0(const void* in, const void* W0p, void* out, int T, int n, in
 // The merged weight of a layer call: bf16 W0' (q == nullptr), or its int8 codes with per-row
 // scales (the int8 layer) plus one bf16 panel buffer for the shapes that the CTA-pair kernel
 // does not take.
-// A 4-bit weight is given by q4.codes (the other members unused).
+// A 4-bit weight is given by q4.codes; up to kFewTokens tokens v_lo and w_lo then hold the second
+// halves of V and W.
 struct W0Ref {
   const void* bf16 = nullptr;
   const int8_t* q = nullptr;
@@ -1017,6 +1018,8 @@ struct W0Ref {
   void* panel = nullptr;
   int panel_f = 0, panel_b = 0;  // panel widths (along N) of the forward / backward GEMMs
   Q4Weight q4;
+  void* v_lo = nullptr;
+  void* w_lo = nullptr;
   const void* ptr() const { return q4.codes ? (const void*)q4.codes : q ? (const void*)q : bf16; }
 };
 
@@ -1107,9 +1110,11 @@ cudaError_t gather_x(const poetx_linear_desc* d, const DropArgs* drop, const voi
   return launch_gather(x, U, nullptr, d->perm_P, d->T, d->n, d->n, d->n, es, s);
 }
 
-// Tokens up to which the layer on a 4-bit weight takes the few-token kernels (three launches:
-// gather + block product, weight product, block product + scatter).
-constexpr int kFewTokens = 64;
+// Tokens up to which the layer on a 4-bit weight takes the few-token kernels: three launches, with
+// V and W between them as hi + lo of two bf16 numbers each.  More tokens keep the five launches
+// (a form of the three for up to 64 tokens gathered x once for every 16 rows of a block: 5120 x
+// 5120, b = 256: 16 tokens 44 us against 34, 64 tokens 71 against 37).
+constexpr int kFewTokens = 8;
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
 // Writes U (if U != x-gather target), V, W; Z and y only when y != nullptr.
@@ -1121,10 +1126,9 @@ int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, con
   const bool bf = d->dtype == POETX_BF16;
   const int es = bf ? 2 : 4;
   if (w0.q4.codes && !drop && T <= kFewTokens) {
-    POETX_CUDA(launch_bd_gather(G_P, x, V, U, d->perm_P, T, n, b, s), "gather + blockdiag G_P");
-    POETX_CUDA(w0_gemm(V, w0, W, T, n, m, true, s), "W0' product");
-    if (y)
-      POETX_CUDA(launch_bd_scatter(G_R, W, y, d->perm_R, T, m, b, s), "blockdiag G_R + scatter");
+    POETX_CUDA(launch_q4_layer8(G_P, G_R, w0.q4, x, y, U, V, w0.v_lo, W, w0.w_lo, d->perm_P,
+                                d->perm_R, T, b, s),
+               "few-token layer");
     return POETX_OK;
   }
   POETX_CUDA(gather_x(d, drop, x, U, s), "gather x");
@@ -1480,8 +1484,14 @@ int drop_args(const poetx_dropout_desc* drop, int64_t rows, DropArgs* a, bool* o
   return POETX_OK;
 }
 
+// Scratch of the 4-bit layer: the second halves of V and W of a few tokens.
+size_t q4_scratch(const poetx_linear_desc* d) {
+  if (d->T <= 0 || d->T > kFewTokens) return 0;
+  return align_up((size_t)d->T * d->n * 2) + align_up((size_t)d->T * d->m * 2);
+}
+
 // The weight of a poetx_linear_{fwd,bwd}_ex call as a W0Ref; the int8 form takes its panel
-// buffer from the head of ws.
+// buffer from the head of ws, the 4-bit form its second halves.
 int ex_weight(const poetx_linear_desc* d, const poetx_linear_weight* w, void* ws, size_t ws_bytes,
               W0Ref* r, void** rest, size_t* rest_bytes) {
   if (!w) return fail(POETX_ERR_INVALID_ARG, "weight is NULL");
@@ -1506,6 +1516,16 @@ int ex_weight(const poetx_linear_desc* d, const poetx_linear_weight* w, void* ws
   r->q4.m = d->m;
   r->q4.n = d->n;
   r->q4.group = w->group;
+  const size_t head = q4_scratch(d);
+  if (!head) return POETX_OK;
+  if (ws_bytes < head) return fail(POETX_ERR_WORKSPACE, "scratch too small (4-bit weight)");
+  if (!ws) return fail(POETX_ERR_INVALID_ARG, "scratch is NULL");
+  if ((st = check_opt(ws)) != POETX_OK) return st;
+  Carve cv(ws);
+  r->v_lo = cv.take((size_t)d->T * d->n * 2);
+  r->w_lo = cv.take((size_t)d->T * d->m * 2);
+  *rest = static_cast<char*>(ws) + head;
+  *rest_bytes = ws_bytes - head;
   return POETX_OK;
 }
 
@@ -1627,7 +1647,9 @@ size_t poetx_linear_ex_workspace(const poetx_linear_desc* d, const poetx_linear_
   if (!d || !w || d->T < 0 || d->n < 1 || d->m < 1 || d->b < 1) return 0;
   const size_t f = fwd_layout(d, has_save_u, has_save_w).total;
   const size_t g = bwd_layout(d, has_save_u, has_save_w).total;
-  const size_t extra = w->kind == POETX_WEIGHT_Q8 ? poetx_linear_q8_scratch(d) : 0;
+  const size_t extra = w->kind == POETX_WEIGHT_Q8   ? poetx_linear_q8_scratch(d)
+                       : w->kind == POETX_WEIGHT_Q4 ? q4_scratch(d)
+                                                    : 0;
   return extra + (f > g ? f : g);
 }
 

@@ -43,6 +43,8 @@ size_t cnp_fixed_bytes();
 // while the previous kernel on the stream is still finishing.  Every kernel launched this
 // way calls pdl_wait() before its first access to global memory: that waits until the
 // previous kernel has completed and its writes are visible, so stream order is kept.
+// (Behind a kernel that triggers only after its own wait, the next one may read before its wait
+// what neither of the two writes: all launches before them have completed then.)
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args&&... args) {
@@ -109,13 +111,13 @@ cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, 
 // the same on tcgen05 with the weight as the M operand (kernels_umma_q4.cu)
 cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                            cudaStream_t s);
-// few-token block products fused with their index maps (bf16; width % b == 0, b % 128 == 0):
-// out = blockdiag(G) x[:, idx]^T by rows (save_u: the gathered rows too), and y[:, idx] =
-// the block product of `in`
-cudaError_t launch_bd_gather(const void* G, const void* x, void* out, void* save_u,
-                             const int32_t* idx, int T, int width, int b, cudaStream_t s);
-cudaError_t launch_bd_scatter(const void* G, const void* in, void* y, const int32_t* idx, int T,
-                              int width, int b, cudaStream_t s);
+// The layer's forward on up to 8 tokens (b % 128 == 0, no dropout) in three launches: gather +
+// block product, weight product, block product + scatter (left out when y is NULL).  V and W go
+// between them as hi + lo, two bf16 numbers each; U is written if given.
+cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
+                             void* y, void* U, void* V, void* V_lo, void* W, void* W_lo,
+                             const int32_t* perm_P, const int32_t* perm_R, int T, int b,
+                             cudaStream_t s);
 
 // ---- dropout (kernels_dropout.cu, kernels_perm.cu; generator in philox_dev.cuh) ------
 struct DropArgs;

@@ -472,11 +472,13 @@ def dequantize_q4(q, scales, out, group: int, stream=None):
 def matmul_q4(x, q, scales, y, group: int, transpose: bool = False, stream=None):
     """y = x W^T (or, transpose, y = x W) with the 4-bit weight W [m, n]; bf16, T >= 0 rows."""
     import torch
-    _require_cuda()
-    m, n = (x.shape[1], y.shape[1]) if transpose else (y.shape[1], x.shape[1])
-    T = x.shape[0]
-    _require(y.shape[0] == T, "x and y must have the same number of rows")
-    _require(x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be bfloat16")
+    T, k = x.shape
+    Ty, o = y.shape
+    m, n = (k, o) if transpose else (o, k)
+    if Ty != T:
+        raise ValueError("x and y must have the same number of rows")
+    if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16:
+        raise ValueError("x and y must be bfloat16")
     _check_q4(q, scales, m, n, group)
     _on_current_device(x, q, scales, y)
     _check(_load().poetx_matmul_q4(_ptr(x), _ptr(q), _ptr(scales), _ptr(y), T, m, n, group,
@@ -685,8 +687,10 @@ class CnpBuffers:
                       self.b, self.k, self.ws, stream)
 
 
-def _layer_scratch_bytes(desc, save: bool, int8: bool) -> int:
-    """(The 4-bit layer needs no scratch beyond the bf16 layer's.)"""
+def _layer_scratch_bytes(desc, save: bool, int8: bool, int4_group: int = 0) -> int:
+    if int4_group:
+        w = LinearWeight(POETX_WEIGHT_Q4, int4_group, None, None)
+        return max(linear_ex_workspace(desc, w, save, save), 16)
     q8 = linear_q8_scratch(desc) if int8 else 0
     return max(linear_fwd_workspace(desc, save, save), linear_bwd_workspace(desc, save, save),
                16) + q8
@@ -771,7 +775,7 @@ class PoetxLinear:
             self.scales = torch.empty(ss, dtype=torch.bfloat16, device=dev)
         self.dropout = dropout
         self.training = True
-        need = _layer_scratch_bytes(self.desc, self.save, int8_weight)
+        need = _layer_scratch_bytes(self.desc, self.save, int8_weight, int4_group)
         if ws is None:
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
         elif ws.numel() * ws.element_size() < need:
@@ -872,7 +876,7 @@ class PoetxLinearGroup:
         for W in W0s:
             m, n = W.shape
             d = LinearDesc(T, n, m, b, POETX_BF16 if bf16 else POETX_F32, None, None, None, None)
-            need = max(need, _layer_scratch_bytes(d, save_activations, int8_weight))
+            need = max(need, _layer_scratch_bytes(d, save_activations, int8_weight, int4_group))
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
         self.layers = []
         off = 0

@@ -376,3 +376,73 @@ def test_decoding_in_a_graph_while_a_step_runs(P):
         M.step(x2, dy2, y2, dx2, s2)
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(y2, want2[0]) and torch.equal(dx2, want2[1])
+
+
+@pytest.mark.parametrize("T,n,m,b,group", [(1, 512, 768, 128, 64), (3, 1024, 512, 256, 32),
+                                           (7, 512, 2048, 512, 128), (8, 2560, 256, 256, 128)])
+def test_few_token_layer_rounds_only_its_result(P, T, n, m, b, group):
+    """Up to 8 tokens V and W go between the products as sums of two bf16 numbers: each is off by
+    2^-16 of its magnitude (a half step of a half step), y by half a step, and the fp32 sums of
+    b, n and b products by at most 2^-23 for each of their (2 b + n) / 16 + 3 * 64 roundings."""
+    import torch
+    _, L, pP, pR = _layer(P, T, n, m, b, group, save=False)
+    rng = np.random.default_rng(T)
+    x = rng.standard_normal((T, n))
+    xd = tensor(x, torch.bfloat16)
+    GP = tensor(rng.standard_normal((n // b, b, b)) / 16, torch.bfloat16)
+    GR = tensor(rng.standard_normal((m // b, b, b)) / 16, torch.bfloat16)
+    y = torch.full((T, m), 7.0, dtype=torch.bfloat16, device="cuda")
+    U, V = torch.empty_like(xd), torch.empty_like(y)
+    ws = torch.empty(P.linear_ex_workspace(L.desc, L.weight, True, True), dtype=torch.uint8,
+                     device="cuda")
+    P.linear_fwd_ex(L.desc, L.weight, None, xd, GP, GR, y, U, V, ws)
+    W = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    P.dequantize_q4(L.W0q, L.scales, W, group)
+    maps = [np.asarray(p) for p in (pP, pR)]
+
+    def layer(f):
+        u = f(host(xd))[:, maps[0]]
+        v = np.einsum("tjk,jik->tji", u.reshape(T, -1, b), f(host(GP))).reshape(T, n)
+        w = v @ f(host(W)).T
+        z = np.einsum("tjk,jik->tji", w.reshape(T, -1, b), f(host(GR))).reshape(T, m)
+        out = np.empty_like(z)
+        out[:, maps[1]] = z
+        return u, w, out
+
+    u_ref, w_ref, y_ref = layer(lambda a: a.astype(np.float64))
+    _, w_mag, y_mag = layer(lambda a: np.abs(a.astype(np.float64)))
+    assert np.array_equal(host(U), u_ref)
+    sums = ((2 * b + n) / 16 + 192) * 2.0 ** -23
+    w_err, y_err = np.abs(host(V) - w_ref), np.abs(host(y) - y_ref)
+    assert np.all(w_err <= 2.0 ** -8 * np.abs(w_ref) + (2.0 ** -16 + sums) * 1.01 * w_mag)
+    assert np.all(y_err <= 2.0 ** -8 * np.abs(y_ref) + (2.0 ** -15 + sums) * 1.01 * y_mag)
+
+
+def test_decoding_right_behind_new_weights_and_rotations(P):
+    """The launches of a decoding pass overlap: what it reads early was written by the launches
+    just before it, merges and rotations that nothing waits for."""
+    import torch
+    T, n, m, b = 2, 512, 512, 256
+    _, L, pP, pR = _layer(P, T, n, m, b, 64, save=False)
+    torch.manual_seed(0)
+    x = torch.randn(T, n, device="cuda").bfloat16()
+    Ws = [torch.randn(m, n, device="cuda").bfloat16() for _ in range(6)]
+    Gs = [torch.randn(2, n // b, b, b, device="cuda").bfloat16() for _ in range(6)]
+    GP, GR = (torch.empty(n // b, b, b, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def run(i, wait):
+        y = torch.empty(T, m, dtype=torch.bfloat16, device="cuda")
+        GP.copy_(Gs[i][0])
+        GR.copy_(Gs[i][1])
+        P.quantize_q4(Ws[i], L.W0q, L.scales, 64)
+        if wait:
+            torch.cuda.synchronize()
+        P.linear_fwd_ex(L.desc, L.weight, None, x, GP, GR, y, None, None, L.ws)
+        return y
+
+    want = [run(i, True) for i in range(6)]
+    torch.cuda.synchronize()
+    got = [run(i % 6, False) for i in range(60)]
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 6])
