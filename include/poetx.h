@@ -428,8 +428,9 @@ int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, v
  *   POETX_WEIGHT_Q8     w = int8 codes, scales fp32 [m] (poetx_merge_perm_q8)
  *   POETX_WEIGHT_Q4     w = 4-bit codes, scales bf16, group (poetx_merge_perm_q4); bf16 layer.
  *                       Up to 8 tokens without dropout run as three launches (gather + block
- *                       product, weight product, block product + scatter) and keep V and W
- *                       between them as sums of two bf16 numbers; save_w receives W in bf16.
+ *                       product, weight product, block product + scatter); up to 4 tokens V
+ *                       and W go between them as sums of two bf16 numbers (save_w receives W
+ *                       in bf16).
  * Without dropout the first two give the results of poetx_linear_{fwd,bwd}{,_q8} bit for bit.
  * ws: at least poetx_linear_ex_workspace bytes (enough for either direction).  Other arguments
  * and errors as poetx_linear_fwd / poetx_linear_bwd.

@@ -360,9 +360,21 @@ struct RowScales<4> {
   }
 };
 
-// HL: x comes and y goes as the sum of two bf16 numbers, hi + lo (16 significant bits), an MMA
-// each: the layer's intermediates of a few tokens are then not rounded to bf16.
-template <int GS, int WARPS, bool HL>
+// The row of column g of an MMA of up to 8 tokens: token g, or of up to 4 tokens (hi + lo) token
+// g % 4 of hi (g < 4) or lo; behind the last token, that one again.
+__device__ __forceinline__ const __nv_bfloat16* few_row(const __nv_bfloat16* hi,
+                                                        const __nv_bfloat16* lo, int g, int T,
+                                                        int width) {
+  if (T > 4) return hi + (int64_t)min(g, T - 1) * width;
+  return (g < 4 ? hi : lo) + (int64_t)min(g & 3, T - 1) * width;
+}
+
+// In the layer (LAYER) up to 4 tokens come and go as sums of two bf16 numbers, hi + lo (16
+// significant bits): lo takes the MMAs' columns 4 to 7, which are idle then, so that the
+// intermediates of so few tokens are not rounded to bf16 at no cost.  (A form with MMAs of their
+// own for lo, up to 8 tokens, read x twice as often as the codes: 5120 x 13824, 8 tokens, layer
+// 36 us against 29.)
+template <int GS, int WARPS, bool LAYER>
 __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     k_q4_rows(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
               const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y,
@@ -381,9 +393,8 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
   uint32_t os = ((uint32_t)warp * (uint32_t)m + (uint32_t)ra) * SG;
   const uint32_t dc = (uint32_t)(rb - ra) * 4u, ds = (uint32_t)(rb - ra) * SG;
   const uint32_t step = (uint32_t)WARPS * (uint32_t)m;
-  const int64_t x0 = (int64_t)min(g, T - 1) * n + warp * 128 + t * 8;
-  const uint4* xp = reinterpret_cast<const uint4*>(x + x0);
-  const uint4* xlp = HL ? reinterpret_cast<const uint4*>(x_lo + x0) : nullptr;
+  const uint4* xp = reinterpret_cast<const uint4*>(
+      (LAYER ? few_row(x, x_lo, g, T, n) : x + (int64_t)min(g, T - 1) * n) + warp * 128 + t * 8);
   RowScales<SG> sa[2], sb[2];
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(&ring[0][warp][lane]);
   int left = cnt;  // blocks whose loads are to be issued
@@ -402,14 +413,14 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     os += step * SG;
   };
   constexpr uint32_t kSlot = WARPS * 1024u;  // bytes of a ring stage
-  if (!HL) {
+  if (!LAYER) {
     pdl_trigger();
     pdl_wait();
   }
 #pragma unroll
   for (int d = 0; d < D; ++d) load(slot0 + d * kSlot);
   load_scales(0, cnt > 0);
-  if (HL) {  // behind k_bd_rows, which lets this launch begin once all before it has ended
+  if (LAYER) {  // behind k_bd_rows, which lets this launch begin once all before it has ended
     pdl_wait();
     pdl_trigger();
   }
@@ -420,12 +431,6 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
 #pragma unroll
     for (int w = 0; w < 4; ++w) xv[w] = ld_u4(xp + w * 4);
     xp += WARPS * 16;
-    uint4 xl[4];
-    if (HL) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) xl[w] = ld_u4(xlp + w * 4);
-      xlp += WARPS * 16;
-    }
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     const uint4 ca = lds_u4(slot), cb = lds_u4(slot + 512u);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
@@ -441,10 +446,6 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
       } else {
         mma16816(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
         mma16816(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
-      }
-      if (HL) {
-        mma16816(part, qa[0], qb[0], qa[1], qb[1], xl[w].x, xl[w].y);
-        mma16816(odd, qa[2], qb[2], qa[3], qb[3], xl[w].z, xl[w].w);
       }
       if ((w + 1) % (GS / 32) == 0) {
         const float a = sa[b].at(w / (GS / 32)), c = sb[b].at(w / (GS / 32));
@@ -475,10 +476,14 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += red[w][tok][r];  // fixed order
+    if (LAYER && T <= 4) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) v += red[w][tok + 4][r];
+    }
     const int64_t o = (int64_t)tok * m + row0 + r;
     const __nv_bfloat16 hi = __float2bfloat16_rn(4.f * v);
     y[o] = hi;
-    if (HL) y_lo[o] = __float2bfloat16_rn(4.f * v - __bfloat162float(hi));
+    if (LAYER && T <= 4) y_lo[o] = __float2bfloat16_rn(4.f * v - __bfloat162float(hi));
   }
 }
 
@@ -844,8 +849,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// Block-diagonal product of up to 8 tokens with its index map, between the layer's unrounded
-// intermediates (hi + lo, see k_q4_rows):
+// Block-diagonal product of up to 8 tokens with its index map; V and W of up to 4 tokens are
+// hi + lo (see k_q4_rows):
 //   gather:  V_j = U_j G_P,j^T, U = X[:, p_P] (also written when `save` is given), V = out + lo;
 //   scatter: Z_j = W_j G_R,j^T, W = in + lo, Y[:, p_R[i]] = Z[:, i].
 // One CTA: 16 rows of one block; its four warps split k and add their sums in a fixed order.  A
@@ -855,23 +860,22 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 // predecessor ends (G and the indices here, the codes in k_q4_rows).
 constexpr int kBdWarps = 4;
 
-template <int KI, bool GATHER>
+template <int KI, int RT, bool GATHER>
 __global__ void __launch_bounds__(32 * kBdWarps)
     k_bd_rows(const __nv_bfloat16* __restrict__ G, const __nv_bfloat16* __restrict__ in,
               __nv_bfloat16* __restrict__ out, __nv_bfloat16* __restrict__ lo,
               __nv_bfloat16* __restrict__ save, const int32_t* __restrict__ idx, int T,
               int width) {
-  constexpr int b = 128 * KI, tiles = b / 16;
-  __shared__ float red[kBdWarps][8][17];
+  constexpr int b = 128 * KI, tiles = b / (16 * RT);
+  __shared__ float red[RT][kBdWarps][8][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int j = blockIdx.x / tiles, i0 = (blockIdx.x - j * tiles) * 16;
+  const int j = blockIdx.x / tiles, i0 = (blockIdx.x - j * tiles) * (16 * RT);
   const int k0 = warp * (32 * KI) + 8 * t;  // columns k0 + 32 i .. + 7 of the block
-  const int tok = min(g, T - 1);
   if (GATHER) {
     pdl_wait();
     pdl_trigger();  // after the wait: what the next launch reads early was there before this one
   }
-  uint4 ga[KI], gb[KI], xv[KI], xl[KI];
+  uint4 ga[RT][KI], gb[RT][KI], xv[KI];
   const __nv_bfloat16* gp = G + ((int64_t)j * b + i0 + g) * b + k0;
   uint32_t c_out = 0;
   if (GATHER) {
@@ -882,11 +886,13 @@ __global__ void __launch_bounds__(32 * kBdWarps)
       ci[i][1] = ld_u4(idx + j * b + k0 + 32 * i + 4);
     }
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      ga[i] = ld_u4(gp + 32 * i);
-      gb[i] = ld_u4(gp + 8 * b + 32 * i);
-    }
-    const __nv_bfloat16* x = in + (int64_t)tok * width;
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        ga[r][i] = ld_u4(gp + 16 * r * b + 32 * i);
+        gb[r][i] = ld_u4(gp + (16 * r + 8) * b + 32 * i);
+      }
+    const __nv_bfloat16* x = in + (int64_t)min(g, T - 1) * width;
     uint32_t e[KI][8];
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
@@ -905,43 +911,51 @@ __global__ void __launch_bounds__(32 * kBdWarps)
   } else {
     c_out = ld_u32(idx + j * b + i0 + (threadIdx.x & 15));
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      ga[i] = ld_u4(gp + 32 * i);
-      gb[i] = ld_u4(gp + 8 * b + 32 * i);
-    }
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        ga[r][i] = ld_u4(gp + 16 * r * b + 32 * i);
+        gb[r][i] = ld_u4(gp + (16 * r + 8) * b + 32 * i);
+      }
     pdl_trigger();
     pdl_wait();
-    const int64_t o = (int64_t)tok * width + j * b + k0;
+    const __nv_bfloat16* w = few_row(in, lo, g, T, width) + j * b + k0;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) xv[i] = ld_u4(w + 32 * i);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
-      xv[i] = ld_u4(in + o + 32 * i);
-      xl[i] = ld_u4(lo + o + 32 * i);
+      const uint4 a = ga[r][i], c = gb[r][i];
+      mma16816(acc, a.x, c.x, a.y, c.y, xv[i].x, xv[i].y);
+      mma16816(acc, a.z, c.z, a.w, c.w, xv[i].z, xv[i].w);
     }
+    red[r][warp][2 * t][g] = acc[0];
+    red[r][warp][2 * t + 1][g] = acc[1];
+    red[r][warp][2 * t][g + 8] = acc[2];
+    red[r][warp][2 * t + 1][g + 8] = acc[3];
   }
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < KI; ++i) {
-    mma16816(acc, ga[i].x, gb[i].x, ga[i].y, gb[i].y, xv[i].x, xv[i].y);
-    mma16816(acc, ga[i].z, gb[i].z, ga[i].w, gb[i].w, xv[i].z, xv[i].w);
-    if (!GATHER) {
-      mma16816(acc, ga[i].x, gb[i].x, ga[i].y, gb[i].y, xl[i].x, xl[i].y);
-      mma16816(acc, ga[i].z, gb[i].z, ga[i].w, gb[i].w, xl[i].z, xl[i].w);
-    }
-  }
-  red[warp][2 * t][g] = acc[0];
-  red[warp][2 * t + 1][g] = acc[1];
-  red[warp][2 * t][g + 8] = acc[2];
-  red[warp][2 * t + 1][g + 8] = acc[3];
   __syncthreads();
-  const int ot = threadIdx.x >> 4, r = threadIdx.x & 15;  // an output each
+  const int ot = threadIdx.x >> 4, row = threadIdx.x & 15;  // an output of each row tile
   if (ot >= T) return;
-  float v = 0.f;
 #pragma unroll
-  for (int w = 0; w < kBdWarps; ++w) v += red[w][ot][r];
-  const uint32_t c = GATHER ? (uint32_t)(j * b + i0 + r) : min(c_out, (uint32_t)width - 1);
-  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-  out[(int64_t)ot * width + c] = hi;
-  if (GATHER) lo[(int64_t)ot * width + c] = __float2bfloat16_rn(v - __bfloat162float(hi));
+  for (int r = 0; r < RT; ++r) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBdWarps; ++w) v += red[r][w][ot][row];
+    if (!GATHER && T <= 4) {
+#pragma unroll
+      for (int w = 0; w < kBdWarps; ++w) v += red[r][w][ot + 4][row];
+    }
+    const uint32_t c =
+        GATHER ? (uint32_t)(j * b + i0 + 16 * r + row) : min(c_out, (uint32_t)width - 1);
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    out[(int64_t)ot * width + c] = hi;
+    if (GATHER && T <= 4)
+      lo[(int64_t)ot * width + c] = __float2bfloat16_rn(v - __bfloat162float(hi));
+  }
 }
 
 template <typename E, int GS, int MAXW>
@@ -1014,29 +1028,29 @@ cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m
   return cudaGetLastError();
 }
 
-template <int GS, int WARPS, bool HL>
+template <int GS, int WARPS, bool LAYER>
 cudaError_t rows8_t(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo, int T,
                     cudaStream_t s) {
   using B = __nv_bfloat16;
   begin_launch("gemm_w0", s);
   const cudaError_t e = launch_pdl(
-      k_q4_rows<GS, WARPS, HL>, dim3((w.m + 15) / 16), dim3(32 * WARPS), kRowD * WARPS * 1024, s,
+      k_q4_rows<GS, WARPS, LAYER>, dim3((w.m + 15) / 16), dim3(32 * WARPS), kRowD * WARPS * 1024, s,
       w.codes, static_cast<const uint16_t*>(w.scales), static_cast<const B*>(x),
       static_cast<B*>(y), static_cast<const B*>(x_lo), static_cast<B*>(y_lo), T, w.m, w.n);
   end_launch("gemm_w0", s);
   return e;
 }
-template <int GS, bool HL>
-cudaError_t rows8_hl(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo,
+template <int GS, bool LAYER>
+cudaError_t rows8_layer(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo,
                      int T, cudaStream_t s) {
   // eight warps share a row tile where four would leave fewer than 16 warps on an SM (5120 x 5120:
   // 6.6 us against 9.4; 13824 x 5120: 12.6 against 11.6)
-  if ((w.m + 15) / 16 < 4 * num_sms()) return rows8_t<GS, 8, HL>(w, x, y, x_lo, y_lo, T, s);
-  return rows8_t<GS, 4, HL>(w, x, y, x_lo, y_lo, T, s);
+  if ((w.m + 15) / 16 < 4 * num_sms()) return rows8_t<GS, 8, LAYER>(w, x, y, x_lo, y_lo, T, s);
+  return rows8_t<GS, 4, LAYER>(w, x, y, x_lo, y_lo, T, s);
 }
 template <int GS>
 cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  return rows8_hl<GS, false>(w, x, y, nullptr, nullptr, T, s);
+  return rows8_layer<GS, false>(w, x, y, nullptr, nullptr, T, s);
 }
 
 template <int GS>
@@ -1113,13 +1127,13 @@ cudaError_t rows16(const Q4Weight& w, const void* x, void* y, int T, cudaStream_
   return e;
 }
 
-template <int KI, bool GATHER>
+template <int KI, int RT, bool GATHER>
 cudaError_t bd_t(const void* G, const void* in, void* out, void* lo, void* save,
                  const int32_t* idx, int T, int width, cudaStream_t s) {
   using B = __nv_bfloat16;
   begin_launch("gemm_blockdiag", s);
   const cudaError_t e =
-      launch_pdl(k_bd_rows<KI, GATHER>, dim3(width / 16), dim3(32 * kBdWarps), 0, s,
+      launch_pdl(k_bd_rows<KI, RT, GATHER>, dim3(width / (16 * RT)), dim3(32 * kBdWarps), 0, s,
                  static_cast<const B*>(G), static_cast<const B*>(in), static_cast<B*>(out),
                  static_cast<B*>(lo), static_cast<B*>(save), idx, T, width);
   end_launch("gemm_blockdiag", s);
@@ -1128,10 +1142,13 @@ cudaError_t bd_t(const void* G, const void* in, void* out, void* lo, void* save,
 template <bool GATHER>
 cudaError_t bd(const void* G, const void* in, void* out, void* lo, void* save, const int32_t* idx,
                int T, int width, int b, cudaStream_t s) {
+  // The gather takes two tiles of rows a CTA: half the 2-byte reads of x (8 tokens at 5120 x 5120,
+  // b = 256: layer 18.8 us against 16.0; one token 12.4 against 12.6).
+  constexpr int RT = GATHER ? 2 : 1;
   switch (b) {
-    case 128: return bd_t<1, GATHER>(G, in, out, lo, save, idx, T, width, s);
-    case 256: return bd_t<2, GATHER>(G, in, out, lo, save, idx, T, width, s);
-    case 512: return bd_t<4, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    case 128: return bd_t<1, RT, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    case 256: return bd_t<2, RT, GATHER>(G, in, out, lo, save, idx, T, width, s);
+    case 512: return bd_t<4, RT, GATHER>(G, in, out, lo, save, idx, T, width, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1182,9 +1199,9 @@ cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w
   if (T <= 0 || T > 8) return cudaErrorInvalidValue;
   cudaError_t e = bd<true>(G_P, x, V, V_lo, U, perm_P, T, w.n, b, s);
   if (e != cudaSuccess) return e;
-  e = w.group == 32   ? rows8_hl<32, true>(w, V, W, V_lo, W_lo, T, s)
-      : w.group == 64 ? rows8_hl<64, true>(w, V, W, V_lo, W_lo, T, s)
-                      : rows8_hl<128, true>(w, V, W, V_lo, W_lo, T, s);
+  e = w.group == 32   ? rows8_layer<32, true>(w, V, W, V_lo, W_lo, T, s)
+      : w.group == 64 ? rows8_layer<64, true>(w, V, W, V_lo, W_lo, T, s)
+                      : rows8_layer<128, true>(w, V, W, V_lo, W_lo, T, s);
   if (e != cudaSuccess || !y) return e;
   return bd<false>(G_R, W, y, W_lo, nullptr, perm_R, T, w.m, b, s);
 }

@@ -1009,7 +1009,7 @@ cudaError_t bf16_w0(const void* in, const void* W0p, void* out, int T, int n, in
 // The merged weight of a layer call: bf16 W0' (q == nullptr), or its int8 codes with per-row
 // scales (the int8 layer) plus one bf16 panel buffer for the shapes that the CTA-pair kernel
 // does not take.
-// A 4-bit weight is given by q4.codes; up to kFewTokens tokens v_lo and w_lo then hold the second
+// A 4-bit weight is given by q4.codes; up to kHiLoTokens tokens v_lo and w_lo then hold the second
 // halves of V and W.
 struct W0Ref {
   const void* bf16 = nullptr;
@@ -1111,10 +1111,10 @@ cudaError_t gather_x(const poetx_linear_desc* d, const DropArgs* drop, const voi
 }
 
 // Tokens up to which the layer on a 4-bit weight takes the few-token kernels: three launches, with
-// V and W between them as hi + lo of two bf16 numbers each.  More tokens keep the five launches
+// V and W of up to kHiLoTokens tokens between them as hi + lo of two bf16 numbers each.  More keep the five launches
 // (a form of the three for up to 64 tokens gathered x once for every 16 rows of a block: 5120 x
 // 5120, b = 256: 16 tokens 44 us against 34, 64 tokens 71 against 37).
-constexpr int kFewTokens = 8;
+constexpr int kFewTokens = 8, kHiLoTokens = 4;
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
 // Writes U (if U != x-gather target), V, W; Z and y only when y != nullptr.
@@ -1486,7 +1486,7 @@ int drop_args(const poetx_dropout_desc* drop, int64_t rows, DropArgs* a, bool* o
 
 // Scratch of the 4-bit layer: the second halves of V and W of a few tokens.
 size_t q4_scratch(const poetx_linear_desc* d) {
-  if (d->T <= 0 || d->T > kFewTokens) return 0;
+  if (d->T <= 0 || d->T > kHiLoTokens) return 0;
   return align_up((size_t)d->T * d->n * 2) + align_up((size_t)d->T * d->m * 2);
 }
 
