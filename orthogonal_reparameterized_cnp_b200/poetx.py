@@ -43,6 +43,7 @@ class LinearDesc(ctypes.Structure):
 class DropoutDesc(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", _c_u64), ("site", ctypes.c_uint32),
                 ("row0", ctypes.c_uint32), ("step", _vp)]
+    keep = None  # the tensor of the step counter (dropout_desc)
 
 
 POETX_WEIGHT_DENSE = 0
@@ -52,6 +53,7 @@ POETX_WEIGHT_Q4 = 2
 
 class LinearWeight(ctypes.Structure):
     _fields_ = [("kind", _c_i32), ("group", _c_i32), ("w", _vp), ("scales", _vp)]
+    keep = ()  # the tensors of the weight (linear_weight_dense, _q8, _q4)
 
 
 _descp = ctypes.POINTER(LinearDesc)
@@ -403,13 +405,23 @@ def _require(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_current_device(*tensors):
-    """The calls below launch on the current device's stream: their tensors must live there."""
+def _ptrs(*tensors):
+    """Device pointers of contiguous tensors on the current device (None -> NULL); the calls below
+    launch on that device's stream.  (Checked here once, in plain ifs: a decoding call's time on
+    the host counts.)"""
     import torch
     dev = torch.cuda.current_device()
+    out = []
     for t in tensors:
-        if t is not None and t.get_device() != dev:  # (-1 for a CPU tensor)
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:  # (-1 for a CPU tensor)
             raise ValueError(f"expected tensors on the current CUDA device ({dev}), got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
 
 
 def q4_shapes(m: int, n: int, group: int):
@@ -440,8 +452,7 @@ def quantize_q4(W, q, scales, group: int, stream=None):
     _require_cuda()
     m, n = W.shape
     _check_q4(q, scales, m, n, group)
-    _on_current_device(W, q, scales)
-    _check(_load().poetx_quantize_q4(_ptr(W), _ptr(q), _ptr(scales), m, n, group, _dtype_code(W),
+    _check(_load().poetx_quantize_q4(*_ptrs(W, q, scales), m, n, group, _dtype_code(W),
                                      _stream(stream)), "poetx_quantize_q4")
 
 
@@ -453,10 +464,9 @@ def merge_perm_q4(W0, q, scales, perm_R, perm_P, group: int, stream=None):
     _check_q4(q, scales, m, n, group)
     _check_map(perm_R, m, "perm_R")
     _check_map(perm_P, n, "perm_P")
-    _on_current_device(W0, q, scales, perm_R, perm_P)
-    _check(_load().poetx_merge_perm_q4(_ptr(W0), _ptr(q), _ptr(scales), m, n, _ptr(perm_R),
-                                       _ptr(perm_P), group, _dtype_code(W0), _stream(stream)),
-           "poetx_merge_perm_q4")
+    w, c, sc, pR, pP = _ptrs(W0, q, scales, perm_R, perm_P)
+    _check(_load().poetx_merge_perm_q4(w, c, sc, m, n, pR, pP, group, _dtype_code(W0),
+                                       _stream(stream)), "poetx_merge_perm_q4")
 
 
 def dequantize_q4(q, scales, out, group: int, stream=None):
@@ -464,9 +474,8 @@ def dequantize_q4(q, scales, out, group: int, stream=None):
     _require_cuda()
     m, n = out.shape
     _check_q4(q, scales, m, n, group)
-    _on_current_device(q, scales, out)
-    _check(_load().poetx_dequantize_q4(_ptr(q), _ptr(scales), _ptr(out), m, n, group,
-                                       _dtype_code(out), _stream(stream)), "poetx_dequantize_q4")
+    _check(_load().poetx_dequantize_q4(*_ptrs(q, scales, out), m, n, group, _dtype_code(out),
+                                       _stream(stream)), "poetx_dequantize_q4")
 
 
 def matmul_q4(x, q, scales, y, group: int, transpose: bool = False, stream=None):
@@ -480,9 +489,8 @@ def matmul_q4(x, q, scales, y, group: int, transpose: bool = False, stream=None)
     if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16:
         raise ValueError("x and y must be bfloat16")
     _check_q4(q, scales, m, n, group)
-    _on_current_device(x, q, scales, y)
-    _check(_load().poetx_matmul_q4(_ptr(x), _ptr(q), _ptr(scales), _ptr(y), T, m, n, group,
-                                   int(bool(transpose)), _stream(stream)), "poetx_matmul_q4")
+    _check(_load().poetx_matmul_q4(*_ptrs(x, q, scales, y), T, m, n, group, 1 if transpose else 0,
+                                   _stream(stream)), "poetx_matmul_q4")
 
 
 # ------------------------------------------------------------------------ dropout
@@ -504,9 +512,9 @@ def dropout(drop: DropoutDesc, x, out, stream=None):
     _require_cuda()
     rows, cols = x.shape
     _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
-    _on_current_device(x, out, drop.keep)
-    _check(_load().poetx_dropout(ctypes.byref(drop), _ptr(x), _ptr(out), rows, cols,
-                                 _dtype_code(x), _stream(stream)), "poetx_dropout")
+    a, o, _ = _ptrs(x, out, drop.keep)
+    _check(_load().poetx_dropout(ctypes.byref(drop), a, o, rows, cols, _dtype_code(x),
+                                 _stream(stream)), "poetx_dropout")
 
 
 def permute_cols_dropout(drop: DropoutDesc, x, out, idx, mask_output: bool = False, stream=None):
@@ -516,9 +524,9 @@ def permute_cols_dropout(drop: DropoutDesc, x, out, idx, mask_output: bool = Fal
     rows, cols = x.shape
     _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
     _check_map(idx, cols, "idx")
-    _on_current_device(x, out, idx, drop.keep)
-    _check(_load().poetx_permute_cols_dropout(ctypes.byref(drop), _ptr(x), _ptr(out), _ptr(idx),
-                                              rows, cols, int(bool(mask_output)), _dtype_code(x),
+    a, o, i, _ = _ptrs(x, out, idx, drop.keep)
+    _check(_load().poetx_permute_cols_dropout(ctypes.byref(drop), a, o, i, rows, cols,
+                                              1 if mask_output else 0, _dtype_code(x),
                                               _stream(stream)), "poetx_permute_cols_dropout")
 
 
@@ -570,6 +578,9 @@ def linear_weight_q4(W0q, scales, group: int) -> LinearWeight:
 
 
 def _check_weight(desc: LinearDesc, w: LinearWeight):
+    if not w.keep:
+        raise ValueError("a weight comes from linear_weight_dense, linear_weight_q8 or "
+                         "linear_weight_q4")
     if w.kind == POETX_WEIGHT_Q4:
         _check_q4(*w.keep, desc.m, desc.n, w.group)
     elif w.kind == POETX_WEIGHT_Q8:
@@ -579,7 +590,9 @@ def _check_weight(desc: LinearDesc, w: LinearWeight):
                  tuple(s.shape) == (desc.m,) and s.dtype == torch.float32,
                  "the int8 weight is int8 [m, n] with float32 scales [m]")
     else:
-        _require(tuple(w.keep[0].shape) == (desc.m, desc.n), "the merged weight is [m, n]")
+        _require(tuple(w.keep[0].shape) == (desc.m, desc.n) and
+                 _dtype_code(w.keep[0]) == desc.dtype, "the merged weight is [m, n], of the "
+                 "layer's type")
 
 
 def _drop_ref(drop):
@@ -593,34 +606,46 @@ def linear_ex_workspace(desc: LinearDesc, weight: LinearWeight, has_save_u=True,
                                                  int(has_save_u), int(has_save_w)))
 
 
+def _check_layer(desc, weight, outer, G_P, G_R):
+    """outer: pairs of a tensor [T, width] and its width (the tensor None: not given)."""
+    import torch
+    _check_weight(desc, weight)
+    T, dt = desc.T, torch.bfloat16 if desc.dtype == POETX_BF16 else torch.float32
+    for t, width in outer:
+        if t is not None and (t.shape != (T, width) or t.dtype is not dt):
+            raise ValueError(f"expected a {dt} tensor [{T}, {width}], got {t.dtype} "
+                             f"{list(t.shape)}")
+    for t, width in ((G_P, desc.n), (G_R, desc.m)):
+        if t.numel() != width * desc.b or t.dtype is not dt:
+            raise ValueError(f"G_P and G_R are {dt}, [n/b, b, b] and [m/b, b, b]")
+
+
 def linear_fwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, G_P, G_R, y, save_u, save_w,
                   ws, stream=None):
     """Layer forward on any form of the merged weight, with dropout of x (drop or None)."""
-    _require_cuda()
-    _check_weight(desc, weight)
-    _on_current_device(x, y, G_P, G_R, save_u, save_w, ws, *weight.keep)
-    _require(tuple(x.shape) == (desc.T, desc.n) and tuple(y.shape) == (desc.T, desc.m),
-             "x must be [T, n] and y [T, m]")
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    n, m = desc.n, desc.m
+    _check_layer(desc, weight, ((x, n), (y, m), (save_u, n), (save_w, m)), G_P, G_R)
+    ptrs = _ptrs(x, G_P, G_R, y, save_u, save_w, ws, *weight.keep,
+                 None if drop is None else drop.keep)
     _check(_load().poetx_linear_fwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
-                                       _ptr(x), _ptr(G_P), _ptr(G_R), _ptr(y), _ptr(save_u),
-                                       _ptr(save_w), _ptr(ws), ws_bytes, _stream(stream)),
-           "poetx_linear_fwd_ex")
+                                       *ptrs[:7], 0 if ws is None else ws.nbytes,
+                                       _stream(stream)), "poetx_linear_fwd_ex")
 
 
 def linear_bwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, dy, G_P, G_R, save_u, save_w,
                   dx, dG_P, dG_R, accumulate: int, ws, stream=None):
     """Layer backward on any form of the merged weight; drop as in the forward."""
-    _require_cuda()
-    _check_weight(desc, weight)
-    _on_current_device(x, dy, dx, G_P, G_R, save_u, save_w, dG_P, dG_R, ws, *weight.keep)
-    _require(tuple(dx.shape) == (desc.T, desc.n) and tuple(dy.shape) == (desc.T, desc.m),
-             "dx must be [T, n] and dy [T, m]")
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    import torch
+    n, m = desc.n, desc.m
+    _check_layer(desc, weight, ((x, n), (dy, m), (save_u, n), (save_w, m), (dx, n)), G_P, G_R)
+    for t, G in ((dG_P, G_P), (dG_R, G_R)):
+        if t.numel() != G.numel() or t.dtype is not torch.float32:
+            raise ValueError("dG_P and dG_R are float32, [n/b, b, b] and [m/b, b, b]")
+    ptrs = _ptrs(x, dy, G_P, G_R, save_u, save_w, dx, dG_P, dG_R, ws, *weight.keep,
+                 None if drop is None else drop.keep)
     _check(_load().poetx_linear_bwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
-                                       _ptr(x), _ptr(dy), _ptr(G_P), _ptr(G_R), _ptr(save_u),
-                                       _ptr(save_w), _ptr(dx), _ptr(dG_P), _ptr(dG_R),
-                                       int(accumulate), _ptr(ws), ws_bytes, _stream(stream)),
+                                       *ptrs[:9], int(accumulate), ptrs[9],
+                                       0 if ws is None else ws.nbytes, _stream(stream)),
            "poetx_linear_bwd_ex")
 
 

@@ -449,3 +449,33 @@ def test_decoding_right_behind_new_weights_and_rotations(P):
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 6])
+
+
+def test_layer_call_refuses_tensors_that_are_not_the_layer_s(P):
+    import torch
+    T, n, m, b = 3, 256, 512, 128
+    _, L, _, _ = _layer(P, T, n, m, b, 64)
+    GP, GR = L.G_ops()
+    x, y = (torch.zeros(T, c, dtype=torch.bfloat16, device="cuda") for c in (n, m))
+    good = dict(x=x, G_P=GP, G_R=GR, y=y, save_u=L.U, save_w=L.Wsave, ws=L.ws, w=L.weight)
+
+    def fwd(**bad):
+        a = {**good, **bad}
+        P.linear_fwd_ex(L.desc, a["w"], None, a["x"], a["G_P"], a["G_R"], a["y"], a["save_u"],
+                        a["save_w"], a["ws"])
+
+    fwd()
+    for bad in (dict(x=x.float()), dict(x=x[:2]), dict(x=x.cpu()), dict(y=y[:, :n].contiguous()),
+                dict(y=y.half()), dict(G_P=GR), dict(G_R=GR.float()), dict(save_u=L.Wsave),
+                dict(save_w=L.Wsave.float()), dict(w=P.LinearWeight(P.POETX_WEIGHT_Q4, 64, 0, 0)),
+                dict(w=P.linear_weight_dense(torch.zeros(m, n, device="cuda"))),
+                dict(w=P.linear_weight_q4(L.W0q, L.scales, 128)),
+                dict(x=torch.zeros(n, T, dtype=torch.bfloat16, device="cuda").t())):
+        with pytest.raises(ValueError):
+            fwd(**bad)
+    with pytest.raises(P.PoetxError):
+        fwd(ws=L.ws[:64])
+    dx, dG = torch.zeros_like(x), [L.dG[: L.nP], L.dG[L.nP:]]
+    for bad in ([dG[1], dG[0]], [dG[0].bfloat16(), dG[1]]):
+        with pytest.raises(ValueError):
+            P.linear_bwd_ex(L.desc, L.weight, None, x, y, GP, GR, L.U, L.Wsave, dx, *bad, 0, L.ws)
