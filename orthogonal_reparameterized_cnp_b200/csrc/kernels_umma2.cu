@@ -38,14 +38,15 @@
 // reading the codes straight from global memory (less shared-memory traffic) and a 512 x 128
 // pair tile (half the conversions per FLOP, more shared-memory traffic) did not raise it.
 //
-// 4-bit merged weight (Q4 instantiation; format in q4_dev.cuh): the same roles with the tiles
-// loaded as 4-bit codes.  The weight is stored in runs of rows per 128-column block, so a tile
-// and its scales are two contiguous runs, fetched with untiled bulk copies.  Forward: one 8 KB
-// tile (128 rows x 128 columns) holds two K chunks, converted by two groups that share its slot;
-// backward: 4 KB tiles (64 rows x 128 columns), one per chunk.  Converting costs about 1.7
-// instructions a code (q4_unpack and half a multiplication in packed bf16, all exact for the
-// quantiser's scales) against 2.8 for int8, and the smaller slots
-// leave room for a fifth operand stage.
+// 4-bit merged weight (Q4 instantiation; format in q4_dev.cuh): three stages of two K chunks, each
+// filled by a group of four converter warps of its own, which load the codes and scales of the
+// stage after next into registers (contiguous runs of a 128-column block: no staging slots, and
+// no loading warp).  Converting costs about 1.9 instructions a code (q4_unpack and half a
+// multiplication in packed bf16, exact for the quantiser's scales) against 2.8 for int8.
+// Measured at 13824 x 5120, forward / transposed, 4096 tokens: 414 / 440 us (1.40 / 1.32
+// PFLOP/s), 8192 tokens 830 / 910.  Stages of one chunk, with the codes through slots of shared
+// memory: 473 / 525 and 955 / 1030 (one chunk in registers: 562 / 524; groups of two warps: 435 /
+// 481; eight epilogue warps and other rasters: the same).
 //
 // Every mbarrier wait is bounded (Params2::wait_ns): on a timeout the waiting role records
 // POETX_ERR_TIMEOUT in the device flag and leaves its loop; the CTAs then drain what they can
@@ -85,27 +86,33 @@ constexpr int kGroupThreads = 32 * kGroupWarps;
 constexpr int kTileChunks = kQ8Bytes / 16;                 // 16-code chunks per int8 tile
 constexpr int kConvChunks = (kTileChunks + kGroupThreads - 1) / kGroupThreads;  // per thread
 
+// 4-bit weight: converter groups (one a stage) and their threads
+constexpr int kQ4Groups = 3, kQ4GT = 128;
+
 // Per instantiation: RA stages of A and RB stages of B (with the bf16 weight one ring that
 // TMA fills; with the int8 weight A's stages are filled by TMA and B's by the converters, each
-// with barriers of its own, and four of each leave room for the staging slots), epilogue
-// warps, staging slots, threads and shared memory.
+// with barriers of its own, and four of each leave room for the staging slots; with the 4-bit
+// weight three of two chunks each), epilogue warps, staging slots, threads and shared memory.
 // QB: bits of the stored weight's codes (0: bf16 weight, no conversion).
 template <int QB>
 struct PairCfg {
   static constexpr bool conv = QB != 0;
-  static constexpr int RA = QB == 0 ? 6 : QB == 8 ? 4 : 5;
+  // K chunks per stage: the tensor core loses a little time at each stage's commit
+  static constexpr int CH = QB == 4 ? 2 : 1;
+  static constexpr int RA = QB == 8 ? 4 : QB == 4 ? 3 : 6;
   static constexpr int RB = RA;
-  static constexpr int EPI = conv ? PAIR_Q8_EPI : 8;
-  static constexpr bool ld32 = conv && kConvWarps > 8;  // epilogue loads of 32 columns
-  static constexpr int SLOTS = conv ? 2 * kConvGroups : 0;
-  // 8-bit: a tile of codes per slot; 4-bit: 4 slots of 8 KB + 1 KB of scales (forward) or 8 of
-  // 4 KB + 512 B (backward)
-  static constexpr int slot_total = QB == 8 ? SLOTS * kQ8Bytes : QB == 4 ? 8 * 4608 : 0;
-  static constexpr int threads = 64 + 32 * EPI + (conv ? 32 + 32 * kConvWarps : 0);
+  static constexpr int EPI = QB == 0 ? 8 : QB == 8 ? PAIR_Q8_EPI : 4;
+  static constexpr bool ld32 = QB == 8 && kConvWarps > 8;  // epilogue loads of 32 columns
+  static constexpr int SLOTS = QB == 8 ? 2 * kConvGroups : 0;  // (a tile of int8 codes each)
+  static constexpr int slot_total = SLOTS * kQ8Bytes;
+  // 8-bit: a warp of loads and the converters; 4-bit: the converters
+  static constexpr int threads =
+      64 + 32 * EPI + (QB == 8 ? 32 + 32 * kConvWarps : QB == 4 ? kQ4Groups * kQ4GT : 0);
   // with a converted weight and RA == RB one set of stage barriers serves both operands
   static constexpr bool split = conv && RA != RB;
   static constexpr int nbar = 2 * RA + (split ? 2 * RB : 0) + 6 + 2 * SLOTS;
-  static constexpr int smem = 1024 + RA * kPairA + RB * kPairB + slot_total + EPI * 4096 + 512;
+  static constexpr int smem =
+      1024 + CH * (RA * kPairA + RB * kPairB) + slot_total + EPI * 4096 + 512;
 };
 static_assert(PairCfg<0>::smem <= 227 * 1024 && PairCfg<8>::smem <= 227 * 1024 &&
                   PairCfg<4>::smem <= 227 * 1024,
@@ -113,10 +120,8 @@ static_assert(PairCfg<0>::smem <= 227 * 1024 && PairCfg<8>::smem <= 227 * 1024 &
 static_assert(PairCfg<0>::nbar * 8 <= 512 && PairCfg<8>::nbar * 8 <= 512 &&
                   PairCfg<4>::nbar * 8 <= 512,
               "barriers");
-static_assert(PairCfg<4>::slot_total % 1024 == 0, "epilogue staging alignment");
 // a group's waits on the converted-operand ring see consecutive phases
-static_assert(kConvGroups <= PairCfg<8>::RB && kConvGroups <= PairCfg<4>::RB, "converter groups");
-static_assert(kConvGroups == 4, "the 4-bit tiles are shared by groups 2 p and 2 p + 1");
+static_assert(kConvGroups <= PairCfg<8>::RB && kQ4Groups <= PairCfg<4>::RB, "converter groups");
 static_assert(PairCfg<8>::threads <= 1024 && PairCfg<4>::threads <= 1024, "threads");
 constexpr uint32_t kPairTmemCols = 2 * kPairBN;
 
@@ -323,24 +328,6 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
 }
 
 // untiled bulk copy of contiguous bytes into this CTA's shared memory
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-// Slot (and its use, whose parity the barriers count) of K chunk `it` of a CTA's flat sequence.
-// 8-bit, and 4-bit backward: group it % 4 has slots 2 g and 2 g + 1 in turn.  4-bit forward: a
-// tile holds chunks 2 j and 2 j + 1; tiles go to slots 2 p and 2 p + 1, p = j % 2, in turn, and
-// groups 2 p and 2 p + 1 read it.
-template <bool PAIRED>
-__device__ __forceinline__ int slot_of(int it, int& use) {
-  const int u = it / kConvGroups;
-  use = u >> 1;
-  return PAIRED ? 2 * ((it >> 1) & 1) + (u & 1) : 2 * (it % kConvGroups) + (u & 1);
-}
-
 template <bool B_MN>
 __device__ __forceinline__ uint32_t make_idesc_pair() {
   return (1u << 4)                              // D format: f32
@@ -361,16 +348,13 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
                      const __grid_constant__ CUtensorMap tmD, const Params2 p) {
   using C = PairCfg<QB>;
   constexpr bool CONV = C::conv;
-  constexpr bool PAIRED = QB == 4 && !B_MN;  // two chunks per loaded tile
-  constexpr int kSlotBytes = QB == 8 ? kQ8Bytes : B_MN ? 4608 : 9216;
-  constexpr int kSlotCodes = QB == 8 ? kQ8Bytes : B_MN ? 4096 : 8192;
   constexpr int RA = C::RA, RB = C::RB, EPI = C::EPI;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t sA = base;                                   // RA x 16 KB
-  const uint32_t sB = sA + RA * kPairA;                       // RB x 16 KB
-  const uint32_t sQ = sB + RB * kPairB;                       // slots of codes
+  const uint32_t sB = sA + C::CH * RA * kPairA;                       // RB x 16 KB
+  const uint32_t sQ = sB + C::CH * RB * kPairB;                       // slots of codes
   const uint32_t sEpi = sQ + C::slot_total;                   // 1024-aligned staging tiles
   const uint32_t sBar = sEpi + EPI * 4096;
   // A ring (with the bf16 weight: the common ring of A and B)
@@ -395,6 +379,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int stages = (p.total_kc + C::CH - 1) / C::CH;  // of a tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < RA; ++s) {
@@ -412,7 +397,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
       }
       for (int j = 0; j < C::SLOTS; ++j) {
         mbar_init(q8full_bar(j), 1);
-        mbar_init(q8free_bar(j), PAIRED ? 2 : 1);  // the groups that read the slot
+        mbar_init(q8free_bar(j), 1);
       }
     }
     for (int a = 0; a < 2; ++a) {
@@ -445,7 +430,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
       pair_tile(p, item, tm, tn);
       const int m0 = tm * 256 + (int)rank * kPairBM;
       const int n0 = tn * kPairBN + (int)rank * (kPairBN / 2);
-      for (int kc = 0; kc < p.total_kc; ++kc, ++it) {
+      for (int kc = 0; kc < stages; ++kc, ++it) {
         const int s = it % RA, r = it / RA;
         if (!mbar_wait(emptyA(s), (r & 1) ^ 1, p.err, p.wait_ns)) {
           ok = false;
@@ -464,8 +449,10 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
             tma_load_2d_pair(b_dst + 8192, &tmB, n0 + 64, k, fb);
           }
         } else {  // A only: the converter groups fill the B ring
-          if (leader) mbar_expect_tx(fullA(s), 2u * kPairA);
-          tma_load_2d_pair(sA + s * kPairA, &tmA, k, m0, fb);
+          if (leader) mbar_expect_tx(fullA(s), C::CH * 2u * kPairA);
+#pragma unroll
+          for (int c = 0; c < C::CH; ++c)  // (columns past K: zeros)
+            tma_load_2d_pair(sA + (C::CH * s + c) * kPairA, &tmA, k * C::CH + 64 * c, m0, fb);
         }
       }
     }
@@ -489,7 +476,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kPairBN);
-      for (int kc = 0; kc < p.total_kc; ++kc, ++it) {
+      for (int kc = 0; kc < stages; ++kc, ++it) {
         const int s = it % RA, r = it / RA;
         const int sb = CONV ? it % RB : s;
         // (converter arrivals come from both CTAs: cluster-scope acquire)
@@ -500,14 +487,17 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t a_addr = sA + s * kPairA;
-        const uint32_t b_addr = sB + sb * kPairB;
 #pragma unroll
-        for (int kk = 0; kk < kPairBK / 16; ++kk) {
-          const uint64_t adesc = make_desc(a_addr + kk * 32, 16, 1024);
-          const uint64_t bdesc = B_MN ? make_desc(b_addr + kk * 2048, 8192, 1024)
-                                      : make_desc(b_addr + kk * 32, 16, 1024);
-          umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+        for (int c = 0; c < C::CH; ++c) {
+          const uint32_t a_addr = sA + (C::CH * s + c) * kPairA;
+          const uint32_t b_addr = sB + (C::CH * sb + c) * kPairB;
+#pragma unroll
+          for (int kk = 0; kk < kPairBK / 16; ++kk) {
+            const uint64_t adesc = make_desc(a_addr + kk * 32, 16, 1024);
+            const uint64_t bdesc = B_MN ? make_desc(b_addr + kk * 2048, 8192, 1024)
+                                        : make_desc(b_addr + kk * 32, 16, 1024);
+            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kc > 0 || c > 0 || kk > 0) ? 1u : 0u);
+          }
         }
         umma_commit_pair_mc(emptyA(s), (uint16_t)0x3);  // both CTAs' stage s is free
         if (C::split) umma_commit_pair_mc(emptyB(sb), (uint16_t)0x3);
@@ -518,50 +508,106 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
     // every MMA issued here completes before TMEM is released
     umma_commit_pair(drain_bar);
     mbar_drain_wait(drain_bar, 0);
-  } else if (QB == 4 && warp == 2 + EPI) {
-    // ------------------------------------------------------------ 4-bit tile loads
-    // Codes and scales of one tile: two contiguous runs, one barrier.  (A failed wait leaves
-    // loads in flight as in the int8 form below: they are drained before the CTA ends.)
-    if (lane == 0) {
-      constexpr int STEP = PAIRED ? 2 : 1;  // chunks per tile
-      const int total = ((p.num_items - cid + nclusters - 1) / nclusters) * p.total_kc;
-      int ir = 0, kc = 0, n0 = 0, last_ir = -1, it = 0;
-      bool ok = true;
-      for (; it < total; it += STEP) {
-        if (ir != last_ir) {
-          int tm, tn;
-          pair_tile(p, cid + ir * nclusters, tm, tn);
-          n0 = tn * kPairBN + (int)rank * (kPairBN / 2);
-          last_ir = ir;
-        }
-        int use;
-        const int slot = slot_of<PAIRED>(it, use);
-        if (!mbar_wait(q8free_bar(slot), (use & 1) ^ 1, p.err, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        const int k = kc * kPairBK;
-        // forward: rows n0 .. n0 + 127 of block k / 128; backward: rows k .. of block n0 / 128
-        const int64_t row = PAIRED ? (int64_t)(k >> 7) * p.rows4 + n0
-                                   : (int64_t)(n0 >> 7) * p.rows4 + k;
-        const uint32_t rows = PAIRED ? 128u : (uint32_t)min(64, p.K - k);
-        mbar_expect_tx(q8full_bar(slot), rows * (64u + 2u * (uint32_t)p.sg4));
-        const uint32_t dst = sQ + slot * kSlotBytes;
-        bulk_load(dst, p.codes4 + row * 64, rows * 64u, q8full_bar(slot));
-        bulk_load(dst + kSlotCodes, p.scales4 + row * p.sg4, rows * 2u * (uint32_t)p.sg4,
-                  q8full_bar(slot));
-        kc += STEP;
-        if (kc == p.total_kc) {
-          kc = 0;
-          ++ir;
+  } else if (QB == 4 && warp >= 2 + EPI) {
+    // ------------------------------------------------------------ 4-bit codes -> bf16 operands
+    // Group g converts stages g, g + G, ... of the CTA's flat sequence: 128 rows of 128 columns
+    // (forward: N rows, two chunks of columns; backward: two chunks of 64 K rows).  A thread has
+    // 16-byte chunk t of UN rows: words 2 h and 2 h + 1 are chunks t and 4 + t of half h of the
+    // columns (forward: chunk h of the stage; backward: box h of the row's chunk).  The 8 lanes
+    // of a store phase have 8 consecutive rows, so the swizzle spreads them over all banks.  The
+    // codes come straight into registers, loaded one tile ahead.
+    constexpr int G = kQ4Groups, GT = kQ4GT, UN = 512 / GT, RS = GT / 4;
+    const int cw = threadIdx.x - 32 * (2 + EPI);
+    const int grp = cw / GT, gt = cw % GT;
+    const int bar_id = 1 + grp;  // named barrier of the group
+    const int t = lane >> 3, r0 = (gt >> 5) * 8 + (lane & 7);
+    const uint32_t sw = (uint32_t)(lane & 7);
+    const int total = ((p.num_items - cid + nclusters - 1) / nclusters) * stages;
+    const int sg = p.sg4;
+    uint32_t pick[4];  // byte permutation that repeats the scale of word w
+#pragma unroll
+    for (int w = 0; w < 4; ++w) pick[w] = 0x1010u + 0x2222u * (uint32_t)((w * sg) >> 2);
+    auto tile_n0 = [&](int r) {
+      int tm, tn;
+      pair_tile(p, cid + r * nclusters, tm, tn);
+      return tn * kPairBN + (int)rank * (kPairBN / 2);
+    };
+    // the tile to load next: stage kc of item round ir, first row or column n0 of its half of N
+    int lit = grp, kc = grp, ir = 0;
+    auto settle = [&]() {
+      while (kc >= stages) {
+        kc -= stages;
+        ++ir;
+      }
+    };
+    settle();
+    int n0 = lit < total ? tile_n0(ir) : 0;
+    uint4 nq[UN];
+    uint2 ns[UN];
+    auto load = [&]() {
+      const int k = kc * 128;
+      const int64_t row = B_MN ? (int64_t)(n0 >> 7) * p.rows4 + k
+                               : (int64_t)(k >> 7) * p.rows4 + n0;
+      const int rows = lit >= total ? 0 : B_MN ? (n0 < p.N ? p.K - k : 0) : p.rows4 - n0;
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int r = r0 + RS * u;
+        const bool on = r < rows;  // (rows past the operand: scale 0)
+        nq[u] = make_uint4(0, 0, 0, 0);
+        ns[u] = make_uint2(0, 0);
+        ld_u4_stream_if(nq[u], p.codes4 + (row + r) * 64 + t * 16, on);
+        const uint16_t* sp = p.scales4 + (row + r) * sg;
+        ld_u16_if(ns[u].x, sp, on && sg == 1);
+        ld_u32_if(ns[u].x, sp, on && sg == 2);
+        ld_u2_if(ns[u], sp, on && sg == 4);
+      }
+      lit += G;
+      kc += G;
+      if (kc >= stages) {
+        settle();
+        if (lit < total) n0 = tile_n0(ir);
+      }
+    };
+    load();
+    for (int it = grp; it < total; it += G) {
+      uint4 q[UN];
+      uint2 sc[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        q[u] = nq[u];
+        sc[u] = ns[u];
+      }
+      load();
+      const int sb = it % RB, use = it / RB;
+      int got = 1;
+      if (lane == 0) got = mbar_wait(emptyB(sb), (use & 1) ^ 1, p.err, p.wait_ns);
+      // every thread of the group takes the same branch (a failed wait of any warp)
+      if (!group_all(__shfl_sync(0xffffffffu, got, 0) != 0, bar_id, GT)) break;
+      while (!mbar_try_wait(emptyB(sb), (use & 1) ^ 1)) {  // completed: returns at once
+      }
+      const uint32_t dst = sB + sb * (2 * kPairB) + (uint32_t)r0 * 128u;
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const uint32_t words[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+        // (backward: the second chunk's rows follow 16 KB, not 8, behind the first's)
+        const uint32_t row = (uint32_t)(RS * u) * 128u + (B_MN && RS * u >= 64 ? 8192u : 0u);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t s2 = __byte_perm(sc[u].x, sc[u].y, pick[w]);
+          uint32_t o[4];
+          q4_unpack(words[w], o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = bf2_mul(o[e], s2);
+          sts128(dst + row + (uint32_t)(w >> 1) * (B_MN ? 8192u : (uint32_t)kPairB) +
+                     ((((uint32_t)(w & 1) * 4u + (uint32_t)t) ^ sw) << 4),
+                 o[0], o[1], o[2], o[3]);
         }
       }
-      if (!ok)
-        for (int j = (it > C::SLOTS ? it - C::SLOTS : 0); j < it; j += STEP) {
-          int use;
-          const int slot = slot_of<PAIRED>(j, use);
-          mbar_drain_wait(q8full_bar(slot), use & 1);
-        }
+      fence_async_smem();      // the generic-proxy stores, then the tensor core's reads
+      named_sync(bar_id, GT);  // the whole stage is written
+      if (gt == 0)             // (CTA-scope release: see the int8 form)
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(fullB(sb), 0))
+                     : "memory");
     }
   } else if (QB == 8 && warp == 2 + EPI) {
     // ------------------------------------------------------------ int8 tile loads
@@ -606,7 +652,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
         }
       }
     }
-  } else if (CONV && warp > 2 + EPI) {
+  } else if (QB == 8 && warp > 2 + EPI) {
     // ------------------------------------------------------------ codes -> bf16 operands
     // Group g takes chunks it = g + G u (u = 0, 1, ...): it waits for the chunk's int8 tile
     // (slot 2 g + (u & 1)) and for B stage it % RB to be free, converts, completes the stage with one
@@ -637,8 +683,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
     bool ok = true;
     for (int u = 0; it < total; ++u) {
       const int k = kc * kPairBK;
-      if (QB == 4) {  // (the scales come with the tile)
-      } else if (!B_MN) {  // the scale follows the operand row n: fixed while the tile is
+      if (!B_MN) {  // the scale follows the operand row n: fixed while the tile is
         if (n0 != scale_n0) {
 #pragma unroll
           for (int jj = 0; jj < kConvChunks; ++jj) {
@@ -657,8 +702,7 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
           sc[jj] = (o < p.K && gt + kGroupThreads * jj < kTileChunks) ? __ldg(p.scales + o) : 0.f;
         }
       }
-      int use;
-      const int sb = it % RB, slot = slot_of<PAIRED>(it, use);
+      const int sb = it % RB, slot = 2 * grp + (u & 1), use = u >> 1;
       int got = 1;
       if (lane == 0) {
         got = mbar_wait(q8full_bar(slot), use & 1, p.err, p.wait_ns) &&
@@ -674,18 +718,8 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
       }
       while (!mbar_try_wait(emptyB(sb), ((it / RB) & 1) ^ 1)) {
       }
-      const uint32_t src = sQ + slot * kSlotBytes;
+      const uint32_t src = sQ + slot * kQ8Bytes;
       const uint32_t dst = sB + sb * kPairB;
-      if (QB == 4) {
-        const int rows = B_MN ? min(64, p.K - k) : 128;  // rows past K: zero operands
-        const uint32_t half = (uint32_t)it & 1u;
-        if (!B_MN || rows == 64)
-          q4_convert<B_MN ? 64 : 128, kGroupThreads, true>(src, src + kSlotCodes, dst, gt, half,
-                                                           (uint32_t)p.sg4, rows, nullptr);
-        else
-          q4_convert<B_MN ? 64 : 128, kGroupThreads, false>(src, src + kSlotCodes, dst, gt, half,
-                                                            (uint32_t)p.sg4, rows, nullptr);
-      } else {
 #pragma unroll
       for (int jj = 0; jj < kConvChunks; ++jj) {
         const int ch = gt + kGroupThreads * jj;
@@ -709,7 +743,6 @@ __global__ void __launch_bounds__(PairCfg<QB>::threads, 1)
         }
         sts128(row + (c0 << 4), o[0], o[1], o[2], o[3]);
         sts128(row + (c1 << 4), o[4], o[5], o[6], o[7]);
-      }
       }
       fence_async_smem();  // the generic-proxy stores, then the tensor core's reads
       named_sync(bar_id, kGroupThreads);  // the whole tile is written and the slot read
