@@ -347,9 +347,9 @@ int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* d
  * With 5 bits in the scale, s q is exactly a bf16 number: nothing in the library rounds the
  * dequantised weight, and the few-token and the tensor-core products use the same weight.
  * Other bf16 scales (written by the caller) are accepted: s q is then rounded to bf16, except
- * in the forward few-token products, which scale fp32 sums.
+ * in forward products of up to 16 tokens, which may scale fp32 sums instead.
  *
- * Layout (n % 128 == 0, any m): blocks of 128 columns, each with every row's part side by side:
+ * Layout (n % 128 == 0, any m, m n < 2^36): blocks of 128 columns, each with every row's part side by side:
  *   q       uint8 [n/128, m, 64]: a row's 64 bytes of a block are four 16-byte chunks t of four
  *           little-endian 32-bit words w; word (t, w) holds columns 32 w + 8 t + e (e < 8) of
  *           the block, column e as q + 8 in bits [4 p, 4 p + 4), p = e / 2 + 4 (e % 2).

@@ -281,35 +281,37 @@ __global__ void __launch_bounds__(kThreads)
     k_dequant_q4(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
                  E* __restrict__ out, int m, int n) {
   const int64_t v = blockIdx.x * (int64_t)kThreads + threadIdx.x;
-  const int blk = blockIdx.y, t = (int)(v & 3);
+  const int t = (int)(v & 3);
   const int64_t i = v >> 2;
   if (i >= m) return;
-  const int64_t r = (int64_t)blk * m + i;
-  const uint4 cd = __ldg(reinterpret_cast<const uint4*>(codes + r * 64) + t);
-  const uint32_t words[4] = {cd.x, cd.y, cd.z, cd.w};
-  E* o = out + i * n + blk * 128 + 8 * t;
+  for (int blk = blockIdx.y; blk < n / 128; blk += gridDim.y) {
+    const int64_t r = (int64_t)blk * m + i;
+    const uint4 cd = __ldg(reinterpret_cast<const uint4*>(codes + r * 64) + t);
+    const uint32_t words[4] = {cd.x, cd.y, cd.z, cd.w};
+    E* o = out + i * n + blk * 128 + 8 * t;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float s = __bfloat162float(scales[r * (128 / GS) + w / (GS / 32)]);
-    uint32_t q[4];
-    q4_unpack(words[w], q);
-    float f[8];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      f[2 * p] = s * (4.f * bf_lo(q[p]));
-      f[2 * p + 1] = s * (4.f * bf_hi(q[p]));
-    }
-    if constexpr (sizeof(E) == 2) {
-      uint32_t h[4];
+    for (int w = 0; w < 4; ++w) {
+      const float s = __bfloat162float(scales[r * (128 / GS) + w / (GS / 32)]);
+      uint32_t q[4];
+      q4_unpack(words[w], q);
+      float f[8];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * p], f[2 * p + 1]);
-        h[p] = *reinterpret_cast<const uint32_t*>(&b);
+        f[2 * p] = s * (4.f * bf_lo(q[p]));
+        f[2 * p + 1] = s * (4.f * bf_hi(q[p]));
       }
-      *reinterpret_cast<uint4*>(o + 32 * w) = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-      reinterpret_cast<float4*>(o + 32 * w)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(o + 32 * w)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      if constexpr (sizeof(E) == 2) {
+        uint32_t h[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * p], f[2 * p + 1]);
+          h[p] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(o + 32 * w) = make_uint4(h[0], h[1], h[2], h[3]);
+      } else {
+        reinterpret_cast<float4*>(o + 32 * w)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(o + 32 * w)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      }
     }
   }
 }
@@ -1020,7 +1022,8 @@ cudaError_t merge_t(const void* W0, const int32_t* pR, const int32_t* pP, uint8_
 template <typename E, int GS>
 cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m, int n,
                       cudaStream_t s) {
-  const dim3 grid((unsigned)((4ll * m + kThreads - 1) / kThreads), (unsigned)(n / 128));
+  const dim3 grid((unsigned)((4ll * m + kThreads - 1) / kThreads),
+                  (unsigned)(n / 128 < 65535 ? n / 128 : 65535));
   begin_launch("quant", s);
   k_dequant_q4<E, GS><<<grid, kThreads, 0, s>>>(
       codes, static_cast<const __nv_bfloat16*>(scales), static_cast<E*>(out), m, n);

@@ -459,7 +459,18 @@ cudaError_t launch_tr(const Q4Weight& w, const void* x, void* y, int T, cudaStre
 
 cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                            cudaStream_t s) {
-  return transpose ? launch_tr<true>(w, x, y, T, s) : launch_tr<false>(w, x, y, T, s);
+  // (gridDim.y counts tiles of 64 or more tokens: 2^21 tokens a launch)
+  constexpr int kMost = 1 << 21;
+  const int64_t in = transpose ? w.m : w.n, out = transpose ? w.n : w.m;
+  for (int64_t t0 = 0; t0 < T; t0 += kMost) {
+    const char* xs = static_cast<const char*>(x) + t0 * in * 2;
+    char* ys = static_cast<char*>(y) + t0 * out * 2;
+    const int now = T - t0 < kMost ? (int)(T - t0) : kMost;
+    const cudaError_t e =
+        transpose ? launch_tr<true>(w, xs, ys, now, s) : launch_tr<false>(w, xs, ys, now, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace poetx

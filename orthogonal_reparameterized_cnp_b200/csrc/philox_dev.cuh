@@ -47,8 +47,12 @@ __device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2,
   return make_uint4(c0, c1, c2, c3);
 }
 
+// (The low half of the counter; a volatile load stays behind the wait for the previous kernel,
+// which may have moved the counter.)
 __device__ __forceinline__ uint32_t drop_step(const DropArgs& d) {
-  return d.step ? (uint32_t)__ldg(d.step) : 0u;
+  uint32_t v = 0;
+  if (d.step) asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(d.step) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint4 drop_words(const DropArgs& d, uint32_t step, uint32_t row,
                                             uint32_t col8) {

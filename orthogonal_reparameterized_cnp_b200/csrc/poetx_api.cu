@@ -1460,6 +1460,9 @@ int q4_validate(int32_t m, int32_t n, int32_t group) {
   if (group != 32 && group != 64 && group != 128)
     return fail(POETX_ERR_SHAPE, "group must be 32, 64 or 128");
   if (n % 128) return fail(POETX_ERR_SHAPE, "n must be a multiple of 128 (4-bit weight)");
+  // (the few-token kernels count 8-byte code words and scales in 32 bits)
+  if ((int64_t)m * (n / 128) >= 1ll << 29)
+    return fail(POETX_ERR_SHAPE, "m * n must be below 2^36 (4-bit weight)");
   return POETX_OK;
 }
 

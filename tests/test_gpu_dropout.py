@@ -298,3 +298,25 @@ def test_group_gives_each_linear_its_own_site_and_one_counter(P):
     G.train(False)
     G.step([x, x], [x, x], ys, dxs)
     assert int(drop.step) == 1 and _same(ys[0], ys[1])
+
+
+def test_step_counter_moved_by_the_launch_just_before(P):
+    """The kernels read the counter when they run, behind the launch that moved it."""
+    import torch
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    d = P.dropout_desc(0.5, 99, 3, 0, step)
+    x = torch.ones(64, 512, dtype=torch.bfloat16, device="cuda")
+    idx = torch.arange(512, dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(x) for _ in range(60)]
+    for o in outs[:30]:
+        P.permute_cols_dropout(d, x, o, idx)
+        step.add_(1)
+    torch.cuda.synchronize()
+    step.zero_()
+    for o in outs[30:]:
+        P.dropout(d, x, o)
+        step.add_(1)
+        torch.cuda.synchronize()
+    for a, b in zip(outs[:30], outs[30:]):
+        assert torch.equal(a, b)
+    assert not torch.equal(outs[0], outs[1])

@@ -479,3 +479,27 @@ def test_layer_call_refuses_tensors_that_are_not_the_layer_s(P):
     for bad in ([dG[1], dG[0]], [dG[0].bfloat16(), dG[1]]):
         with pytest.raises(ValueError):
             P.linear_bwd_ex(L.desc, L.weight, None, x, y, GP, GR, L.U, L.Wsave, dx, *bad, 0, L.ws)
+
+
+def test_more_blocks_and_token_tiles_than_a_grid_has(P):
+    import torch
+    m, n = 1, 128 * 65537
+    q, s = _buffers(P, m, n, 32)
+    q.copy_(torch.randint(0, 256, q.shape, dtype=torch.uint8, device="cuda"))
+    s.fill_(0.5)
+    out = torch.zeros(m, n, device="cuda")
+    P.dequantize_q4(q, s, out, 32)
+    one_q, one_s = q[-1:].clone(), s[-1:].clone()
+    one = torch.zeros(1, 128, device="cuda")
+    P.dequantize_q4(one_q, one_s, one, 32)
+    assert torch.equal(out[:, -128:], one) and bool((out != 0).any(1).all())
+    # rows of one value: the form for any row count, tiles of 64 tokens
+    T = (1 << 21) + 5
+    x = torch.randn(T, 1, device="cuda").bfloat16()
+    y = torch.full((T, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.matmul_q4(x, one_q, one_s, y, 32, transpose=True)
+    for part in (slice(0, 300), slice(T - 300, T)):
+        ref_y = x[part].double() * one.double()
+        assert bool(((y[part].double() - ref_y).abs() <= 2.0 ** -8 * ref_y.abs()).all())
+    torch.cuda.synchronize()
+    assert P.device_status() == P.POETX_OK

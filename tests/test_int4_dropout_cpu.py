@@ -116,6 +116,10 @@ def test_q4_weight_refusals():
     assert merge(n=51328, dt=P.POETX_F32) == P.POETX_ERR_SHAPE  # rows above 200 KB
     assert merge(m=0) == P.POETX_OK and merge(n=0) == P.POETX_OK
     assert L.poetx_quantize_q4(F, F, F, 4, 100, 32, P.POETX_F32, None) == P.POETX_ERR_SHAPE
+    big = (1 << 20, 1 << 16)  # 2^36 values: past the 32-bit offsets
+    assert L.poetx_quantize_q4(F, F, F, *big, 32, P.POETX_BF16, None) == P.POETX_ERR_SHAPE
+    assert L.poetx_dequantize_q4(F, F, F, *big, 32, P.POETX_BF16, None) == P.POETX_ERR_SHAPE
+    assert L.poetx_matmul_q4(F, F, F, F, 1, *big, 32, 0, None) == P.POETX_ERR_SHAPE
     assert L.poetx_dequantize_q4(F, F, None, 4, 128, 32, P.POETX_F32, None) == \
         P.POETX_ERR_INVALID_ARG
     assert L.poetx_dequantize_q4(F, ODD, F, 4, 128, 32, P.POETX_F32, None) == P.POETX_ERR_ALIGN
