@@ -1063,12 +1063,27 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
   g.batch = 1; g.out_f32 = 0;
   g.D = out; g.ldd = g.N;
   if (w.q4.codes) {
-    // the CTA-pair kernel where its 256 x 256 tiles fill half of the pairs (T x out x sum: 512 x
-    // 5120 x 5120 takes 47 us on it and 44 with the weight as the M operand, 256 tokens 45 and 25,
-    // 1024 tokens 83 and 85, 1024 x 13824 x 5120 125 and 133)
-    if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4) &&
-        4ll * ((T + 255) / 256) * (g.N / 256) > num_sms())
-      return launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
+    // The CTA-pair kernel where its 256 x 256 tiles fill half of the pairs (tokens x outputs x
+    // sum: 512 x 5120 x 5120 takes 40 us on it and 44 with the weight as the M operand, 256 x
+    // 13824 x 5120 41 and 43, 256 x 5120 x 13824 92 and 45).
+    const int tm = (T + 255) / 256, tn = g.N / 256, pairs = num_sms() / 2;
+    if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4) && 4ll * tm * tn > num_sms()) {
+      // A last round of few tiles takes as long as a full one; where it is only the last 256
+      // tokens' (and those are at most 0.3 of a round) the other kernel takes them: 1024 x 5120 x
+      // 13824 170 us -> 137, 1100 x 4096 x 4096 72 -> 63 (2048 x 7168 x 2048, 0.4 of a round:
+      // 70 -> 81).
+      const int64_t tiles = (int64_t)tm * ((g.N + 255) / 256), full = tiles / pairs * pairs;
+      const bool split = full > 0 && full < tiles && 10 * tn <= 3 * pairs &&
+                         (int64_t)(tm - 1) * ((g.N + 255) / 256) <= full;
+      if (!split) return launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
+      g.M = (tm - 1) * 256;
+      g.A = act_kmajor(in, g.M, g.K, 0);
+      const cudaError_t e = launch_umma_gemm_pair_q4(g, w.q4, "gemm_w0", s);
+      if (e != cudaSuccess) return e;
+      return launch_q4_product(w.q4, static_cast<const char*>(in) + (int64_t)g.M * g.K * 2,
+                               static_cast<char*>(out) + (int64_t)g.M * g.N * 2, T - g.M, !forward,
+                               s);
+    }
     return launch_q4_product(w.q4, in, out, T, !forward, s);
   }
   if (gemm_pairs_enabled() && umma_pair_eligible(g) && n % 16 == 0) {  // converted on chip

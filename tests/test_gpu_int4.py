@@ -503,3 +503,24 @@ def test_more_blocks_and_token_tiles_than_a_grid_has(P):
         assert bool(((y[part].double() - ref_y).abs() <= 2.0 ** -8 * ref_y.abs()).all())
     torch.cuda.synchronize()
     assert P.device_status() == P.POETX_OK
+
+
+@pytest.mark.parametrize("T,m,n,group,transpose", [(1100, 4096, 256, 64, False),
+                                                   (1281, 264, 4096, 32, True),
+                                                   (2049, 2560, 128, 128, False)])
+def test_product_whose_last_tokens_take_the_other_kernel(P, T, m, n, group, transpose):
+    import torch
+    torch.manual_seed(T)
+    W = torch.randn(m, n, device="cuda")
+    q, s = _buffers(P, m, n, group)
+    P.quantize_q4(W, q, s, group)
+    P.dequantize_q4(q, s, W, group)
+    K, N = (m, n) if transpose else (n, m)
+    x = torch.randn(T, K, device="cuda").bfloat16()
+    y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.matmul_q4(x, q, s, y[:T], group, transpose=transpose)
+    Wd = W.double() if transpose else W.double().t()
+    want, mag = x.double() @ Wd, x.double().abs() @ Wd.abs()
+    bound = 2.0 ** -8 * want.abs() + 1.01 * (K / 16 + 64) * 2.0 ** -23 * mag
+    assert bool(((y[:T].double() - want).abs() <= bound).all())
+    assert bool((y[T] == 7.0).all())
