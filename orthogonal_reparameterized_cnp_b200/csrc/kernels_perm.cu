@@ -479,7 +479,8 @@ cudaError_t pairs_launch(const void* in, void* out, const int32_t* col_idx, int 
   const int nvec = cols / (16 / (int)sizeof(E));
   const int threads = (nvec + MAXV * 32 - 1) / (MAXV * 32) * 32;
   int per_sm = (int)(kPairSmem / (smem + 1024));
-  if (per_sm > 1536 / threads) per_sm = 1536 / threads;
+  // (at 64 registers a thread all CTAs then run at once: 8192 x 5120 bf16 38.5 us against 40.3)
+  if (per_sm > 1024 / threads) per_sm = 1024 / threads;
   per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
   int grid = num_sms() * per_sm;
   if (grid > (rows + 1) / 2) grid = (rows + 1) / 2;

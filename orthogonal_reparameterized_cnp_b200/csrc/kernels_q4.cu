@@ -977,7 +977,9 @@ cudaError_t merge_pairs_t(const void* W0, const int32_t* pR, const int32_t* pP, 
   const size_t smem = 4 * (size_t)n * sizeof(E);  // two rows as they come, and interleaved
   const int threads = (n / 8 + MAXW * 32 - 1) / (MAXW * 32) * 32;
   int per_sm = (int)((224 * 1024) / (smem + 1024));
-  const int by_threads = 1536 / threads;
+  // as many CTAs as an SM holds at 64 registers a thread, so that all run at once (one more a
+  // SM: 5120 x 5120 bf16 30.1 us against 25.3)
+  const int by_threads = 1024 / threads;
   per_sm = per_sm < 1 ? 1 : per_sm > by_threads ? by_threads : per_sm;
   per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
   int grid = num_sms() * per_sm;
