@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads)
 //
 // Bound: codes and scales at HBM rate (5.6 us at 13824 x 5120); the conversion's masks on the
 // half-rate integer pipe come next (about 3 us there, overlapped in part).  Measured, T = 1, group
-// 128: 6.6 us at 5120 x 5120, 11.3 at 13824 x 5120, 13.6 at 5120 x 13824 (loads alone: 7.0 at
+// 128: 6.6 us at 5120 x 5120, 11.5 at 13824 x 5120, 13.6 at 5120 x 13824 (loads alone: 7.0 at
 // 13824 x 5120).  One load a block without the ring: 8.5, 16.4, 20.4; a persistent grid with
 // the ring in registers: 9.4, 15.4, 22.5 (320 row tiles do not divide evenly).
 constexpr int kRowD = 4;
@@ -361,6 +361,12 @@ struct RowScales<4> {
     return __uint_as_float(h & 1 ? w & 0xffff0000u : w << 16);
   }
 };
+
+// what hi leaves of v (nothing of an infinity: the sum stays one)
+__device__ __forceinline__ __nv_bfloat16 lo_part(float v, __nv_bfloat16 hi) {
+  const float h = __bfloat162float(hi);
+  return __float2bfloat16_rn(fabsf(h) < INFINITY ? v - h : 0.f);
+}
 
 // The row of column g of an MMA of up to 8 tokens: token g, or of up to 4 tokens (hi + lo) token
 // g % 4 of hi (g < 4) or lo; behind the last token, that one again.
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     const int64_t o = (int64_t)tok * m + row0 + r;
     const __nv_bfloat16 hi = __float2bfloat16_rn(4.f * v);
     y[o] = hi;
-    if (LAYER && T <= 4) y_lo[o] = __float2bfloat16_rn(4.f * v - __bfloat162float(hi));
+    if (LAYER && T <= 4) y_lo[o] = lo_part(4.f * v, hi);
   }
 }
 
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
 // (g, t) loads two words (chunk g / 2, half g % 2) of rows 4 t .. 4 t + 3; halves of two rows'
 // words side by side give bf16 pairs along the rows, which the MMA sums over.  The scale changes
 // along the summed index, so it multiplies the bf16 integers (exact for scales of 5 significant
-// bits).  Measured, T = 1, group 128: 8.1 us at 5120 x 5120, 15.1 at 13824 x 5120, 16.4 at 5120 x
+// bits).  Measured, T = 1, group 128: 7.8 us at 5120 x 5120, 14.9 at 13824 x 5120, 15.7 at 5120 x
 // 13824; with loads inside branches (waited for where the paths meet) 10.7, 20.9, 21.5; adding the
 // warps' sums in three halving rounds instead of one costs 1 us.
 constexpr int kColWarps = 8;
@@ -956,7 +962,7 @@ __global__ void __launch_bounds__(32 * kBdWarps)
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
     out[(int64_t)ot * width + c] = hi;
     if (GATHER && T <= 4)
-      lo[(int64_t)ot * width + c] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      lo[(int64_t)ot * width + c] = lo_part(v, hi);
   }
 }
 

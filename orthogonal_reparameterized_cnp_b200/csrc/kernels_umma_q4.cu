@@ -17,6 +17,9 @@
 //   warps 4 ..   G groups that convert every G-th chunk each; then the epilogue
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
+// Bound by the latency of a chunk's way (below), not by a pipe: at 5120 x 5120, group 128, 16
+// tokens take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128 38.5, 256
+// 43.4; 53 tokens of 4999 x 4096 transposed take 35, of 5000 x 4096 15.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.
 #include <cuda.h>
@@ -38,8 +41,8 @@ constexpr int kABytes = 128 * 64 * 2;
 
 // The way of a chunk (slot, conversion, fences and barriers, MMA, commit) takes 1 to 2 us, most
 // of it waiting, so many chunks have to be on their way at once: as many groups and stages as
-// shared memory holds.  Two groups of four warps with three stages, two CTAs an SM: 16.5 us at T = 16,
-// 5120 x 5120, of which 11.5 remain without any conversion.
+// shared memory holds.  Two groups of four warps with three stages, two CTAs an SM: 16.5 us at 16
+// tokens, 5120 x 5120, of which 11.5 remain without any conversion.
 //   G <= chunks in the stages, and SLOTS a multiple of G / 2 (a slot is visited by the same two
 //   groups every time), so that no wait is two phases of its barrier ahead.
 template <int NT, bool TR>

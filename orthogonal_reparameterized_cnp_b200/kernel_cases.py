@@ -11,6 +11,12 @@ Cases (all on cuda:0, seeded random inputs, a few GB of device memory at most):
     layer32            the small fp32 linear: n = m = 256, b = 32, k = 4, T = 512, 5 steps
     cnp nblk b k       CnpBuffers: forward + backward 4 times, the last timed
     q8merge m n        merge_perm_q8 of an m x n bf16 weight, 4 times
+    q4merge m n group  merge_perm_q4 and dequantize_q4 of an m x n bf16 weight, 4 times
+    q4 T m n group     matmul_q4 with an m x n 4-bit weight, forward and transposed in turn, 4 times
+    q4layer T n m      one PoetxLinear (b = 256, k = 4) on a 4-bit weight (group 128) with dropout
+                       0.1: forward + backward 3 times, then 3 forwards without dropout
+    dropout T n        dropout, then dropout fused with an index map (source, output mask) of a
+                       bf16 [T, n], 4 times
 
 Every case ends by checking the library's device status.  Kernel order per step, for
 ncu's --launch-skip: see the docstring of each function.
@@ -125,7 +131,73 @@ def q8merge(m, n):
     print("q8merge ok")
 
 
-CASES = {"gemm": gemm, "layer": layer, "layer32": layer32, "cnp": cnp, "q8merge": q8merge}
+def _q4_weight(m, n, group):
+    W = (torch.randn(m, n, device=_dev()) / n ** 0.5).to(torch.bfloat16)
+    qs, ss = P.q4_shapes(m, n, group)
+    q = torch.empty(qs, dtype=torch.uint8, device=_dev())
+    s = torch.empty(ss, dtype=torch.bfloat16, device=_dev())
+    return W, q, s
+
+
+def q4merge(m, n, group):
+    """Per round: k_merge_q4_pairs (k_merge_q4 where a row does not fit), k_dequant_q4."""
+    W, q, s = _q4_weight(m, n, group)
+    pP, pR = (torch.from_numpy(P.make_perm(i, c)[0]).to(_dev()) for i, c in ((1, n), (2, m)))
+    for _ in range(4):
+        P.merge_perm_q4(W, q, s, pR, pP, group)
+        P.dequantize_q4(q, s, W, group)
+    _check()
+    print("q4merge ok")
+
+
+def q4(T, m, n, group):
+    """Per round one launch forward, one transposed: k_q4_rows and k_q4_cols up to 8 tokens,
+    k_umma_q4 (or k_q4_tile_rows) or k_umma_gemm_pair above."""
+    W, q, s = _q4_weight(m, n, group)
+    P.quantize_q4(W, q, s, group)
+    x = torch.randn(T, n, device=_dev()).to(torch.bfloat16)
+    y = torch.empty(T, m, device=_dev(), dtype=torch.bfloat16)
+    for _ in range(4):
+        P.matmul_q4(x, q, s, y, group)
+        P.matmul_q4(y, q, s, x, group, transpose=True)
+    _check()
+    print("q4 ok")
+
+
+def q4layer(T, n, m):
+    """Up to 8 tokens the last three forwards are k_bd_rows, k_q4_rows, k_bd_rows each."""
+    dev = _dev()
+    W0 = (torch.randn(m, n, device=dev) / n ** 0.5).to(torch.bfloat16)
+    th = [torch.randn(c // 256, 256 * 255 // 2, device=dev) * 0.01 for c in (n, m)]
+    L = P.PoetxLinear(W0, th[0], th[1], P.make_perm(1, n)[0], P.make_perm(2, m)[0], 256, 4, T,
+                      int4_group=128, dropout=P.Dropout(0.1, 7))
+    x, dy = (torch.randn(T, c, device=dev).to(torch.bfloat16) for c in (n, m))
+    y, dx = torch.empty_like(dy), torch.empty_like(x)
+    for _ in range(3):
+        L.step(x, dy, y, dx)
+    L.training = False
+    for _ in range(3):
+        L.forward(x, y)
+    _check()
+    print("q4layer ok")
+
+
+def dropout(T, n):
+    """Per round: k_dropout_vec (or k_dropout), then two k_gather_* launches."""
+    x = torch.randn(T, n, device=_dev()).to(torch.bfloat16)
+    out = torch.empty_like(x)
+    idx = torch.from_numpy(P.make_perm(1, n)[0]).to(_dev())
+    d = P.dropout_desc(0.1, 7)
+    for _ in range(4):
+        P.dropout(d, x, out)
+        P.permute_cols_dropout(d, x, out, idx)
+        P.permute_cols_dropout(d, x, out, idx, mask_output=True)
+    _check()
+    print("dropout ok")
+
+
+CASES = {"gemm": gemm, "layer": layer, "layer32": layer32, "cnp": cnp, "q8merge": q8merge,
+         "q4merge": q4merge, "q4": q4, "q4layer": q4layer, "dropout": dropout}
 
 
 def main(argv=None):

@@ -524,3 +524,33 @@ def test_product_whose_last_tokens_take_the_other_kernel(P, T, m, n, group, tran
     bound = 2.0 ** -8 * want.abs() + 1.01 * (K / 16 + 64) * 2.0 ** -23 * mag
     assert bool(((y[:T].double() - want).abs() <= bound).all())
     assert bool((y[T] == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [2, 6])
+def test_infinities_pass_through_the_few_token_layer(P, T):
+    """Positive weights and rotations: an infinite x gives that infinity in every output of its
+    token, as the formula does, and no other token sees it."""
+    import torch
+    n, m, b, group = 256, 384, 128, 32
+    _, L, pP, _ = _layer(P, T, n, m, b, group, save=False)
+    P.quantize_q4(torch.rand(m, n, device="cuda") + 0.5, L.W0q, L.scales, group)
+    GP = torch.rand(n // b, b, b, device="cuda").add(0.5).bfloat16()
+    GR = torch.rand(m // b, b, b, device="cuda").add(0.5).bfloat16()
+    x = torch.randn(T, n, device="cuda").bfloat16()
+    y = torch.empty(T, m, dtype=torch.bfloat16, device="cuda")
+    P.linear_fwd_ex(L.desc, L.weight, None, x, GP, GR, y, None, None, L.ws)
+    clean = y.clone()
+    x[1, 37] = float("-inf")
+    P.linear_fwd_ex(L.desc, L.weight, None, x, GP, GR, y, None, None, L.ws)
+    keep = [t for t in range(T) if t != 1]
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isfinite(clean).all())
+    assert bool((y[1] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("argv", [["q4merge", "300", "512", "64"], ["q4", "2", "512", "256", "32"],
+                                  ["q4", "70", "512", "256", "32"], ["q4layer", "3", "256", "512"],
+                                  ["q4layer", "40", "256", "512"], ["dropout", "64", "512"]])
+def test_kernel_cases_run(P, argv, capsys):
+    from orthogonal_reparameterized_cnp_b200 import kernel_cases
+    assert kernel_cases.main(argv) == 0
+    assert f"{argv[0]} ok" in capsys.readouterr().out
