@@ -397,7 +397,8 @@ typedef struct poetx_dropout_desc {
   double p;             /* probability of dropping, in [0, 65535/65536] (multiples of 2^-16) */
   uint64_t seed;
   uint32_t site;        /* which of a program's dropouts this is */
-  uint32_t row0;        /* number of the first row (row0 + rows <= 2^32) */
+  uint32_t row0;        /* number of the first row (row0 + rows <= 2^32; fewer than 2^30 rows
+                           and columns a call) */
   const uint64_t* step; /* device counter of steps, read by the kernels when they run (its low
                            32 bits; 8-byte aligned), so that a replayed CUDA graph draws new
                            masks when the caller advances it; NULL: step 0 */

@@ -1066,7 +1066,7 @@ cudaError_t w0_gemm(const void* in, const W0Ref& w, void* out, int T, int n, int
     // The CTA-pair kernel where its 256 x 256 tiles fill half of the pairs (tokens x outputs x
     // sum: 512 x 5120 x 5120 takes 40 us on it and 44 with the weight as the M operand, 256 x
     // 13824 x 5120 41 and 43, 256 x 5120 x 13824 92 and 45).
-    const int tm = (T + 255) / 256, tn = g.N / 256, pairs = num_sms() / 2;
+    const int tm = (int)((T + 255ll) / 256), tn = g.N / 256, pairs = num_sms() / 2;
     if (gemm_pairs_enabled() && umma_pair_q4_eligible(g, w.q4) && 4ll * tm * tn > num_sms()) {
       // A last round of few tiles takes as long as a full one; where it is only the last 256
       // tokens' (and those are at most 0.3 of a round) the other kernel takes them: 1024 x 5120 x
@@ -1126,9 +1126,9 @@ cudaError_t gather_x(const poetx_linear_desc* d, const DropArgs* drop, const voi
 }
 
 // Tokens up to which the layer on a 4-bit weight takes the few-token kernels: three launches, with
-// V and W of up to kHiLoTokens tokens between them as hi + lo of two bf16 numbers each.  More keep the five launches
-// (a form of the three for up to 64 tokens gathered x once for every 16 rows of a block: 5120 x
-// 5120, b = 256: 16 tokens 44 us against 34, 64 tokens 71 against 37).
+// V and W of up to kHiLoTokens tokens between them as hi + lo of two bf16 numbers each.  More keep
+// the five launches (a form of the three for up to 64 tokens gathered x once for every 16 rows of
+// a block: 5120 x 5120, b = 256: 16 tokens 44 us against 34, 64 tokens 71 against 37).
 constexpr int kFewTokens = 8, kHiLoTokens = 4;
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
@@ -1487,6 +1487,7 @@ int drop_args(const poetx_dropout_desc* drop, int64_t rows, DropArgs* a, bool* o
   if (!drop) return POETX_OK;
   if (!(drop->p >= 0.0 && drop->p <= 65535.0 / 65536.0))
     return fail(POETX_ERR_INVALID_ARG, "dropout p must be in [0, 65535/65536]");
+  if (rows >= 1 << 30) return fail(POETX_ERR_SHAPE, "dropout takes fewer than 2^30 rows");
   if ((int64_t)drop->row0 + rows > (1ll << 32))
     return fail(POETX_ERR_INVALID_ARG, "dropout row0 + rows must not pass 2^32");
   if (reinterpret_cast<uintptr_t>(drop->step) & 7)
@@ -1627,6 +1628,7 @@ int poetx_dropout(const poetx_dropout_desc* drop, const void* in, void* out, int
   if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_ERR_DTYPE, "bad dtype");
   if (rows < 0 || cols < 0) return fail(POETX_ERR_INVALID_ARG, "negative size");
   if (!drop) return fail(POETX_ERR_INVALID_ARG, "dropout descriptor is NULL");
+  if (cols >= 1 << 30) return fail(POETX_ERR_SHAPE, "dropout takes fewer than 2^30 columns");
   DropArgs a;
   bool on;
   int st = drop_args(drop, rows, &a, &on);
@@ -1647,6 +1649,7 @@ int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, v
   if (mask_output != 0 && mask_output != 1)
     return fail(POETX_ERR_INVALID_ARG, "mask_output must be 0 or 1");
   if (!drop) return fail(POETX_ERR_INVALID_ARG, "dropout descriptor is NULL");
+  if (cols >= 1 << 30) return fail(POETX_ERR_SHAPE, "dropout takes fewer than 2^30 columns");
   DropArgs a;
   bool on;
   int st = drop_args(drop, rows, &a, &on);

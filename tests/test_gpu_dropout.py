@@ -196,7 +196,8 @@ def _run(L, x, dy):
 
 @pytest.mark.parametrize("kind,T,n,m,b", [("f32", 70, 128, 96, 32), ("bf16", 300, 512, 256, 128),
                                           ("q8", 300, 512, 512, 256), ("q4", 300, 256, 512, 128),
-                                          ("q4", 20, 512, 256, 128), ("bf16", 1, 256, 256, 128)])
+                                          ("q4", 20, 512, 256, 128), ("bf16", 1, 256, 256, 128),
+                                          ("q4", 3, 256, 512, 128)])
 def test_layer_with_dropout_is_the_layer_of_dropped_inputs(P, kind, T, n, m, b):
     """y, dG of the layer with dropout are those of the layer without it on dropout(x), and dx is
     the mask applied to its dx, bit for bit; saved and recomputed activations agree."""

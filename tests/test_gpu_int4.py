@@ -554,3 +554,62 @@ def test_kernel_cases_run(P, argv, capsys):
     from orthogonal_reparameterized_cnp_b200 import kernel_cases
     assert kernel_cases.main(argv) == 0
     assert f"{argv[0]} ok" in capsys.readouterr().out
+
+
+FIRST_CALLS_IN_A_CAPTURE = """
+import torch
+from orthogonal_reparameterized_cnp_b200 import poetx as P
+dev = torch.device("cuda")
+bf = dict(dtype=torch.bfloat16, device=dev)
+m, n, b, group = 512, 768, 128, 64
+qs, ss = P.q4_shapes(m, n, group)
+q, s = torch.empty(qs, dtype=torch.uint8, device=dev), torch.empty(ss, **bf)
+W, out = torch.randn(m, n, **bf), torch.empty(m, n, **bf)
+maps = [torch.from_numpy(a).to(dev) for a in (*P.make_perm(1, n), *P.make_perm(2, m))]
+GP, GR = torch.randn(n // b, b, b, **bf), torch.randn(m // b, b, b, **bf)
+calls, bufs = [], []
+for T in (2, 12, 40, 9600):
+    x, y = torch.randn(T, n, **bf), torch.empty(T, m, **bf)
+    back, z = torch.empty(T, n, **bf), torch.empty(T, m, **bf)
+    d, w = P.linear_desc(T, n, m, b, P.POETX_BF16, *maps), P.linear_weight_q4(q, s, group)
+    ws = torch.empty(P.linear_ex_workspace(d, w, False, False) + 16, dtype=torch.uint8, device=dev)
+    drop = P.dropout_desc(0.25, 5)
+    masked, gathered = torch.empty_like(x), torch.empty_like(x)
+    bufs += [y, back, z, masked, gathered]
+    calls += [lambda x=x, y=y: P.matmul_q4(x, q, s, y, group),
+              lambda y=y, o=back: P.matmul_q4(y, q, s, o, group, transpose=True),
+              lambda x=x, z=z, d=d, w=w, ws=ws: P.linear_fwd_ex(d, w, None, x, GP, GR, z, None,
+                                                                None, ws),
+              lambda x=x, o=masked, d=drop: P.dropout(d, x, o),
+              lambda x=x, o=gathered, d=drop: P.permute_cols_dropout(d, x, o, maps[0])]
+def run():
+    P.quantize_q4(W, q, s, group)
+    P.dequantize_q4(q, s, out, group)
+    for c in calls:
+        c()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in bufs]
+for t in bufs:
+    t.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, c) for a, c in zip(bufs, got)), "replay differs"
+assert P.device_status() == P.POETX_OK
+print("captured first")
+"""
+
+
+def test_first_calls_inside_a_capture(P):
+    """A program whose first call of every kernel is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_IN_A_CAPTURE], cwd=root, timeout=300,
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]

@@ -162,6 +162,7 @@ def test_dropout_refusals():
     assert call(i=None) == P.POETX_ERR_INVALID_ARG
     assert call(o=ODD) == P.POETX_ERR_ALIGN
     assert call(rows=0) == P.POETX_OK and call(cols=0) == P.POETX_OK
+    assert call(rows=1 << 30) == P.POETX_ERR_SHAPE and call(cols=1 << 30) == P.POETX_ERR_SHAPE
 
     def perm(d=_drop(), i=F, o=F2, idx=F, mode=0):
         return L.poetx_permute_cols_dropout(ctypes.byref(d), i, o, idx, 4, 8, mode, P.POETX_F32,
