@@ -22,9 +22,11 @@ __device__ __forceinline__ float q4_f32<uint16_t>(uint16_t v) {
   return __uint_as_float((uint32_t)v << 16);
 }
 
-// Codes and scales of W0[perm_R][:, perm_P] (NULL maps: identity).  Two rows at a time: they come
-// in with cp.async while the pair before them is quantised, and are then interleaved in shared
-// memory, so that one access gathers a column of both (bf16: 4 bytes, fp32: 8).  Thread t owns the
+// Codes and scales of W0[perm_R][:, perm_P] (NULL maps: identity).  Two rows at a time.  bf16: they
+// come in with cp.async while the pair before them is quantised, and are then interleaved in shared
+// memory, so that one access gathers a column of both.  fp32: they come in between two pairs and
+// stay as they are; the smaller buffer lets a third CTA run on an SM, whose work hides the loads
+// (13824 x 5120: 96 us interleaved, 81 so).  Thread t owns the
 // code words t, t + threads, .. (8 columns each) of every row, with their index map in registers
 // (16 bits a column); the group maximum is taken over the 4, 8 or 16 threads of a group by
 // shuffles, for bf16 both rows in one register.
@@ -79,11 +81,6 @@ __device__ __forceinline__ void put_pair(uint32_t* dst, const uint4& a, const ui
   d[1] = make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(a.z, b.z, 0x7632),
                     __byte_perm(a.w, b.w, 0x5410), __byte_perm(a.w, b.w, 0x7632));
 }
-__device__ __forceinline__ void put_pair(uint2* dst, const uint4& a, const uint4& b) {  // fp32
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  d[0] = make_uint4(a.x, b.x, a.y, b.y);
-  d[1] = make_uint4(a.z, b.z, a.w, b.w);
-}
 
 // the code word of 8 columns with scale s (bits sb)
 template <bool BF16>
@@ -130,8 +127,9 @@ __global__ void __launch_bounds__(512)
   using P = Pair<E>;
   using T = typename P::T;
   constexpr int V = 16 / sizeof(E);
-  T* pair = reinterpret_cast<T*>(row_raw);                        // [n]
-  const unsigned char* stage = row_raw + (size_t)n * sizeof(T);   // [2][n] elements
+  constexpr bool MIX = sizeof(E) == 2;  // interleave
+  T* pair = reinterpret_cast<T*>(row_raw);                                    // [n] (MIX)
+  const unsigned char* stage = row_raw + (MIX ? (size_t)n * sizeof(T) : 0);  // [2][n] elements
   const uint32_t stage_s = (uint32_t)__cvta_generic_to_shared(stage);
   const int threads = blockDim.x, tid = threadIdx.x;
   const int words = n / 8, vecs = n / V;
@@ -170,15 +168,18 @@ __global__ void __launch_bounds__(512)
   };
   int pr = blockIdx.x;
   fetch(pr);
-  const unsigned char* cols = row_raw;
   for (; pr < npair; pr += gridDim.x) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // each thread interleaves the vectors it fetched itself (the gathers of the pair before
-    // ended at the barrier below)
-    for (int v = tid; v < vecs; v += threads)
-      put_pair(pair + v * V, lds_u4(stage_s + 16u * v), lds_u4(stage_s + 16u * (vecs + v)));
-    __syncthreads();
-    fetch(pr + gridDim.x);
+    if constexpr (MIX) {
+      // each thread interleaves the vectors it fetched itself (the gathers of the pair before
+      // ended at the barrier below)
+      for (int v = tid; v < vecs; v += threads)
+        put_pair(pair + v * V, lds_u4(stage_s + 16u * v), lds_u4(stage_s + 16u * (vecs + v)));
+      __syncthreads();
+      fetch(pr + gridDim.x);
+    } else {
+      __syncthreads();
+    }
 #pragma unroll
     for (int j = 0; j < MAXW; ++j) {
       const int c = tid + j * threads;
@@ -188,7 +189,12 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t off = (e & 1) ? idx[j][e / 2] >> 16 : idx[j][e / 2] & 0xffffu;
-        const T v = *reinterpret_cast<const T*>(cols + off * (sizeof(T) / 4));
+        T v;
+        if constexpr (MIX)
+          v = *reinterpret_cast<const T*>(row_raw + off);
+        else
+          v = make_uint2(*reinterpret_cast<const uint32_t*>(row_raw + off),
+                         *reinterpret_cast<const uint32_t*>(row_raw + (size_t)n * 4 + off));
         most.see(v);
         P::split(v, a[e], b[e]);
       }
@@ -211,6 +217,7 @@ __global__ void __launch_bounds__(512)
       }
     }
     __syncthreads();
+    if constexpr (!MIX) fetch(pr + gridDim.x);
   }
 }
 
@@ -980,7 +987,8 @@ cudaError_t merge_pairs_t(const void* W0, const int32_t* pR, const int32_t* pP, 
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  const size_t smem = 4 * (size_t)n * sizeof(E);  // two rows as they come, and interleaved
+  // two rows as they come, for bf16 interleaved as well
+  const size_t smem = (sizeof(E) == 2 ? 4 : 2) * (size_t)n * sizeof(E);
   const int threads = (n / 8 + MAXW * 32 - 1) / (MAXW * 32) * 32;
   int per_sm = (int)((224 * 1024) / (smem + 1024));
   // as many CTAs as an SM holds at 64 registers a thread, so that all run at once (one more a
@@ -1000,9 +1008,9 @@ cudaError_t merge_pairs_t(const void* W0, const int32_t* pR, const int32_t* pP, 
 template <typename E, int GS>
 cudaError_t merge_t(const void* W0, const int32_t* pR, const int32_t* pP, uint8_t* codes,
                     void* scales, int m, int n, cudaStream_t s) {
-  // pairs of rows: at most 4 code words a thread (n <= 16384), two rows twice in shared memory
+  // pairs of rows: at most 4 code words a thread (n <= 16384)
   const int words = n / 8;
-  if (words <= 4 * 512 && 4 * (size_t)n * sizeof(E) <= 224 * 1024)
+  if (words <= 4 * 512)
     return words <= 512    ? merge_pairs_t<E, GS, 1>(W0, pR, pP, codes, scales, m, n, s)
            : words <= 1024 ? merge_pairs_t<E, GS, 2>(W0, pR, pP, codes, scales, m, n, s)
                            : merge_pairs_t<E, GS, 4>(W0, pR, pP, codes, scales, m, n, s);

@@ -51,7 +51,8 @@ def _weights(m, n, dt, seed):
 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("m,n", [(1, 128), (7, 384), (300, 2176), (65, 13824), (2, 25600)])
+@pytest.mark.parametrize("m,n", [(1, 128), (7, 384), (300, 2176), (65, 13824), (5, 16384),
+                                 (3, 16512), (2, 25600)])
 def test_merge_and_read_back_bit_exact(P, m, n, dt, group):
     import torch
     act = torch.bfloat16 if dt == "bf16" else torch.float32
