@@ -12,14 +12,15 @@
 // Roles:
 //   warp 0       bulk loads of codes and scales into slots (contiguous runs, see q4_dev.cuh)
 //   warp 1       TMEM allocation, MMA issue
-//   warps 2, 3   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
-//                vectors, words put together and stored by both warps
-//   warps 4 ..   G groups that convert every G-th chunk each; then the epilogue
+//   warps 2 ..   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
+//                vectors, words put together and stored by four warps
+//   then         G groups that convert every G-th chunk each; then the epilogue
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
 // Bound by the latency of a chunk's way (below), not by a pipe: at 5120 x 5120, group 128, 16
 // tokens take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128 38.5, 256
-// 43.4; 53 tokens of 4999 x 4096 transposed take 35, of 5000 x 4096 15.
+// 43.4; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of 5000 x
+// 4096 15.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.
 #include <cuda.h>
@@ -51,7 +52,9 @@ struct QCfg {
   static constexpr int STAGES = NT <= 32 ? 4 : NT <= 128 ? 3 : 2;  // of two chunks
   static constexpr int G = NT <= 32 ? 8 : NT == 64 ? 6 : NT == 128 ? 4 : 2;
   static constexpr int GT = NT <= 64 ? 64 : NT == 128 ? 128 : 256;  // threads of a group
-  static constexpr int threads = 128 + G * GT;
+  static constexpr int TW = NT <= 64 ? 4 : 2;     // warps of token loaders
+  static constexpr int first = 64 + 32 * TW;      // thread of the first group
+  static constexpr int threads = first + G * GT;
   // tiles of 128 rows x 128 columns: two chunks in either direction
   static constexpr int SLOTS = NT <= 32 ? 4 : NT == 64 ? 6 : 2;
   static constexpr int CODES = 8192;
@@ -123,8 +126,8 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < RS; ++s) {
-      // the converter groups of its chunks; the TMA thread (and its bytes), or the 64 token loaders
-      mbar_init(full_bar(s), 2 + (p.vec ? 1 : 64));
+      // the converter groups of its chunks; the TMA thread (and its bytes), or the token loaders
+      mbar_init(full_bar(s), 2 + (p.vec ? 1 : 32 * C::TW));
       mbar_init(empty_bar(s), 1);
     }
     for (int j = 0; j < C::SLOTS; ++j) {
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
       // every MMA issued here completes before TMEM and the stages are used again
       umma_commit(done_bar);
     }
-  } else if (warp < 4) {
+  } else if (warp < 2 + C::TW) {
     // ------------------------------------------------------------ tokens
     const int tid = threadIdx.x - 64;
     if (p.vec) {
@@ -216,8 +219,9 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
     } else {
       // 8 values from any 2-byte boundary: the five aligned words around them, shifted together;
       // a run of up to 8 such pieces a thread is loaded while the run before it is stored
-      constexpr int PER = NT * 8 / 64, RUN = PER < 8 ? PER : 8, RUNS = PER / RUN;  // a chunk
-      // The thread's pieces are column chunk c of tokens t0, t0 + 8, ..: 4 K words apart, so they
+      constexpr int TS = 4 * C::TW, PER = NT / TS;  // tokens apart, pieces of a thread and chunk
+      constexpr int RUN = PER < 8 ? PER : 8, RUNS = PER / RUN;
+      // The thread's pieces are column chunk c of tokens t0, t0 + TS, ..: whole words apart, so they
       // start on the same side of a word.
       const int t0 = tid >> 3, c = tid & 7;
       const int64_t total = (int64_t)p.T * p.K, whole = total >> 1;  // values; whole words
@@ -227,11 +231,11 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
       auto load = [&](int n, uint32_t (&w)[RUN][5]) {
         const int k = (c_first + n / RUNS) * 64 + 8 * c;
         const int i0 = (n % RUNS) * RUN;
-        int64_t word = ((row + k) >> 1) + (int64_t)i0 * 4 * p.K;
+        int64_t word = ((row + k) >> 1) + (int64_t)i0 * (TS / 2) * p.K;
         const bool col_on = n < cnt * RUNS && k < p.K;
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
-          const bool on = col_on && tok0 + t0 + 8 * (i0 + i) < p.T;
+          const bool on = col_on && tok0 + t0 + TS * (i0 + i) < p.T;
           const int have = on ? (int)min((int64_t)5, whole - word) : 0;
 #pragma unroll
           for (int j = 0; j < 5; ++j) {
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
 #pragma unroll
             for (int j = 0; j < 5; ++j) ld_u16_if(w[i][j], p.x + total - 1, word + j == whole);
           }
-          word += 4 * (int64_t)p.K;
+          word += TS / 2 * (int64_t)p.K;
         }
       };
       bool ok = true;
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
         const int k0 = (c_first + it) * 64;
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
-          const int tok = t0 + 8 * ((n % RUNS) * RUN + i), k = k0 + 8 * c;
+          const int tok = t0 + TS * ((n % RUNS) * RUN + i), k = k0 + 8 * c;
           uint32_t v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -283,7 +287,8 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   } else {
     // ------------------------------------------------------------ codes -> bf16 operand
     // group g converts chunks it = g, g + G, .. (q4_convert)
-    const int grp = (threadIdx.x - 128) / GT, gt = (threadIdx.x - 128) % GT;
+    const int grp = ((int)threadIdx.x - C::first) / GT;
+    const int gt = ((int)threadIdx.x - C::first) % GT;
     const int bar_id = 1 + grp;
     const uint32_t sg = (uint32_t)p.sg;
     bool ok = true;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   // (without a timeout every MMA of this CTA completes; with one the sums mean nothing, and the
   // wait below covers the MMAs that were issued)
   int done = 0;
-  if (warp >= 4 && warp < 12) {
+  if (warp >= 8 && warp < 16) {
     if (lane == 0) done = mbar_wait(done_bar, 0, p.err, p.wait_ns) ? 1 : 0;
     done = __shfl_sync(0xffffffffu, done, 0);
   }
@@ -334,9 +339,9 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   __syncthreads();
   float* buf = reinterpret_cast<float*>(gbase);  // [NT][132]
   constexpr int LD = 132;
-  if (done) {  // warps 4 .. 11
+  if (done) {  // warps 8 .. 15
     tc_fence_after();
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int q = warp & 3, half = (warp - 8) >> 2;
 #pragma unroll
     for (int c = 0; c < NT / 2; c += 8) {
       const int col = half * (NT / 2) + c;

@@ -53,7 +53,9 @@ POETX_WEIGHT_Q4 = 2
 
 class LinearWeight(ctypes.Structure):
     _fields_ = [("kind", _c_i32), ("group", _c_i32), ("w", _vp), ("scales", _vp)]
-    keep = ()  # the tensors of the weight (linear_weight_dense, _q8, _q4)
+    keep = ()  # the tensors of the weight (linear_weight_dense, _q8, _q4), on one device
+    device = -1
+    fits = None  # the (m, n, dtype) that they were checked against last
 
 
 _descp = ctypes.POINTER(LinearDesc)
@@ -559,25 +561,30 @@ class Dropout:
 
 
 # ------------------------------------------------------------------------ layer, any weight
-def linear_weight_dense(W0p) -> LinearWeight:
-    w = LinearWeight(POETX_WEIGHT_DENSE, 0, _ptr(W0p), None)
-    w.keep = (W0p,)
+def _hold(w: LinearWeight, *tensors) -> LinearWeight:
+    w.keep, w.device = tensors, tensors[0].get_device()
+    if any(t.get_device() != w.device for t in tensors):
+        raise ValueError("the tensors of a weight must be on one device")
     return w
+
+
+def linear_weight_dense(W0p) -> LinearWeight:
+    return _hold(LinearWeight(POETX_WEIGHT_DENSE, 0, _ptr(W0p), None), W0p)
 
 
 def linear_weight_q8(W0q, scales) -> LinearWeight:
-    w = LinearWeight(POETX_WEIGHT_Q8, 0, _ptr(W0q), _ptr(scales))
-    w.keep = (W0q, scales)
-    return w
+    return _hold(LinearWeight(POETX_WEIGHT_Q8, 0, _ptr(W0q), _ptr(scales)), W0q, scales)
 
 
 def linear_weight_q4(W0q, scales, group: int) -> LinearWeight:
-    w = LinearWeight(POETX_WEIGHT_Q4, group, _ptr(W0q), _ptr(scales))
-    w.keep = (W0q, scales)
-    return w
+    return _hold(LinearWeight(POETX_WEIGHT_Q4, group, _ptr(W0q), _ptr(scales)), W0q, scales)
 
 
 def _check_weight(desc: LinearDesc, w: LinearWeight):
+    """(Once for a weight and layer: the weight holds its tensors.)"""
+    fits = (desc.m, desc.n, desc.dtype)
+    if w.fits == fits:
+        return
     if not w.keep:
         raise ValueError("a weight comes from linear_weight_dense, linear_weight_q8 or "
                          "linear_weight_q4")
@@ -593,6 +600,12 @@ def _check_weight(desc: LinearDesc, w: LinearWeight):
         _require(tuple(w.keep[0].shape) == (desc.m, desc.n) and
                  _dtype_code(w.keep[0]) == desc.dtype, "the merged weight is [m, n], of the "
                  "layer's type")
+    w.fits = fits
+
+
+def _check_device(w: LinearWeight, x):
+    if w.device != x.get_device():
+        raise ValueError(f"the weight is on CUDA device {w.device}, x on {x.device}")
 
 
 def _drop_ref(drop):
@@ -625,8 +638,8 @@ def linear_fwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, G_P, G_R, y, 
     """Layer forward on any form of the merged weight, with dropout of x (drop or None)."""
     n, m = desc.n, desc.m
     _check_layer(desc, weight, ((x, n), (y, m), (save_u, n), (save_w, m)), G_P, G_R)
-    ptrs = _ptrs(x, G_P, G_R, y, save_u, save_w, ws, *weight.keep,
-                 None if drop is None else drop.keep)
+    ptrs = _ptrs(x, G_P, G_R, y, save_u, save_w, ws, None if drop is None else drop.keep)
+    _check_device(weight, x)
     _check(_load().poetx_linear_fwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
                                        *ptrs[:7], 0 if ws is None else ws.nbytes,
                                        _stream(stream)), "poetx_linear_fwd_ex")
@@ -641,8 +654,9 @@ def linear_bwd_ex(desc: LinearDesc, weight: LinearWeight, drop, x, dy, G_P, G_R,
     for t, G in ((dG_P, G_P), (dG_R, G_R)):
         if t.numel() != G.numel() or t.dtype is not torch.float32:
             raise ValueError("dG_P and dG_R are float32, [n/b, b, b] and [m/b, b, b]")
-    ptrs = _ptrs(x, dy, G_P, G_R, save_u, save_w, dx, dG_P, dG_R, ws, *weight.keep,
+    ptrs = _ptrs(x, dy, G_P, G_R, save_u, save_w, dx, dG_P, dG_R, ws,
                  None if drop is None else drop.keep)
+    _check_device(weight, dy)
     _check(_load().poetx_linear_bwd_ex(ctypes.byref(desc), ctypes.byref(weight), _drop_ref(drop),
                                        *ptrs[:9], int(accumulate), ptrs[9],
                                        0 if ws is None else ws.nbytes, _stream(stream)),
