@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------------------
-// y[t, i] = sum_j W[i, j] x[t, j], up to 8 tokens.  One CTA: 16 rows of W; the K blocks are
+// y[t, i] = sum_j W[i, j] x[t, j], up to 8 tokens (NT = 1) or 16 (NT = 2: each code is unpacked
+// once for two MMAs).  One CTA: 16 rows of W; the K blocks are
 // dealt to its warps.  Lane (g, t) loads chunk t of rows g and g + 8 (1 KB a warp and block,
 // contiguous), which is its A fragment of 8 MMAs once the nibbles are bf16 integers; the
 // integers are multiplied exactly, and the group's sum is scaled in fp32.  Lanes of tokens past
@@ -338,7 +339,9 @@ __global__ void __launch_bounds__(kThreads)
 // Bound: codes and scales at HBM rate (5.6 us at 13824 x 5120); the conversion's masks on the
 // half-rate integer pipe come next (about 3 us there, overlapped in part).  Measured, T = 1, group
 // 128: 6.6 us at 5120 x 5120, 11.5 at 13824 x 5120, 13.6 at 5120 x 13824 (loads alone: 7.0 at
-// 13824 x 5120).  One load a block without the ring: 8.5, 16.4, 20.4; a persistent grid with
+// 13824 x 5120).  16 tokens: 11.3, 22.1, 25.6, and 6.4 at 4096 x 4096 (with the weight as the M
+// operand of tcgen05: 13.8, 28, 27.2, 11.8; 128-row tiles whose tokens pass through shared memory:
+// 21 at 13824 x 5120).  One load a block without the ring: 8.5, 16.4, 20.4; a persistent grid with
 // the ring in registers: 9.4, 15.4, 22.5 (320 row tiles do not divide evenly).
 constexpr int kRowD = 4;
 
@@ -389,8 +392,8 @@ __device__ __forceinline__ const __nv_bfloat16* few_row(const __nv_bfloat16* hi,
 // intermediates of so few tokens are not rounded to bf16 at no cost.  (A form with MMAs of their
 // own for lo, up to 8 tokens, read x twice as often as the codes: 5120 x 13824, 8 tokens, layer
 // 36 us against 29.)
-template <int GS, int WARPS, bool LAYER>
-__global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
+template <int GS, int WARPS, int NT, bool LAYER>
+__global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
     k_q4_rows(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
               const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y,
               const __nv_bfloat16* __restrict__ x_lo, __nv_bfloat16* __restrict__ y_lo, int T,
@@ -398,7 +401,8 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
   constexpr int SG = 128 / GS, D = kRowD;  // SG: scales per row and block
   extern __shared__ __align__(16) unsigned char row_ring[];
   uint4 (*ring)[WARPS][64] = reinterpret_cast<uint4 (*)[WARPS][64]>(row_ring);  // [D]
-  __shared__ float red[WARPS][8][17];
+  static_assert(NT == 1 || !LAYER, "hi + lo: one tile of tokens");
+  __shared__ float red[WARPS][8 * NT][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int row0 = blockIdx.x * 16;
   const int ra = min(row0 + g, m - 1), rb = min(row0 + g + 8, m - 1);
@@ -408,8 +412,12 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
   uint32_t os = ((uint32_t)warp * (uint32_t)m + (uint32_t)ra) * SG;
   const uint32_t dc = (uint32_t)(rb - ra) * 4u, ds = (uint32_t)(rb - ra) * SG;
   const uint32_t step = (uint32_t)WARPS * (uint32_t)m;
-  const uint4* xp = reinterpret_cast<const uint4*>(
-      (LAYER ? few_row(x, x_lo, g, T, n) : x + (int64_t)min(g, T - 1) * n) + warp * 128 + t * 8);
+  const uint4* xp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    xp[i] = reinterpret_cast<const uint4*>(
+        (LAYER ? few_row(x, x_lo, g, T, n) : x + (int64_t)min(8 * i + g, T - 1) * n) +
+        warp * 128 + t * 8);
   RowScales<SG> sa[2], sb[2];
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(&ring[0][warp][lane]);
   int left = cnt;  // blocks whose loads are to be issued
@@ -439,35 +447,46 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     pdl_wait();
     pdl_trigger();
   }
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
   uint32_t slot = slot0;
   auto compute = [&](int b) {
-    uint4 xv[4];
+    uint4 xv[NT][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) xv[w] = ld_u4(xp + w * 4);
-    xp += WARPS * 16;
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) xv[i][w] = ld_u4(xp[i] + w * 4);
+      xp[i] += WARPS * 16;
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     const uint4 ca = lds_u4(slot), cb = lds_u4(slot + 512u);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
-    float part[4], odd[4];  // two chains of MMAs
+    float part[NT][4], odd[NT][4];  // two chains of MMAs
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint32_t qa[4], qb[4];
       q4_unpack(wa[w], qa);
       q4_unpack(wb[w], qb);
-      if (w % (GS / 32) == 0) {
-        mma16816_zero(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
-        mma16816_zero(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
-      } else {
-        mma16816(part, qa[0], qb[0], qa[1], qb[1], xv[w].x, xv[w].y);
-        mma16816(odd, qa[2], qb[2], qa[3], qb[3], xv[w].z, xv[w].w);
-      }
-      if ((w + 1) % (GS / 32) == 0) {
-        const float a = sa[b].at(w / (GS / 32)), c = sb[b].at(w / (GS / 32));
-        acc[0] = fmaf(a, part[0] + odd[0], acc[0]);
-        acc[1] = fmaf(a, part[1] + odd[1], acc[1]);
-        acc[2] = fmaf(c, part[2] + odd[2], acc[2]);
-        acc[3] = fmaf(c, part[3] + odd[3], acc[3]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 v = xv[i][w];
+        if (w % (GS / 32) == 0) {
+          mma16816_zero(part[i], qa[0], qb[0], qa[1], qb[1], v.x, v.y);
+          mma16816_zero(odd[i], qa[2], qb[2], qa[3], qb[3], v.z, v.w);
+        } else {
+          mma16816(part[i], qa[0], qb[0], qa[1], qb[1], v.x, v.y);
+          mma16816(odd[i], qa[2], qb[2], qa[3], qb[3], v.z, v.w);
+        }
+        if ((w + 1) % (GS / 32) == 0) {
+          const float a = sa[b].at(w / (GS / 32)), c = sb[b].at(w / (GS / 32));
+          acc[i][0] = fmaf(a, part[i][0] + odd[i][0], acc[i][0]);
+          acc[i][1] = fmaf(a, part[i][1] + odd[i][1], acc[i][1]);
+          acc[i][2] = fmaf(c, part[i][2] + odd[i][2], acc[i][2]);
+          acc[i][3] = fmaf(c, part[i][3] + odd[i][3], acc[i][3]);
+        }
       }
     }
     load(slot);  // (the slot's codes are in registers)
@@ -481,13 +500,17 @@ __global__ void __launch_bounds__(32 * WARPS, 24 / WARPS)
     compute(1);
   }
   if (j < cnt) compute(0);
-  red[warp][2 * t][g] = acc[0];
-  red[warp][2 * t + 1][g] = acc[1];
-  red[warp][2 * t][g + 8] = acc[2];
-  red[warp][2 * t + 1][g + 8] = acc[3];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    red[warp][8 * i + 2 * t][g] = acc[i][0];
+    red[warp][8 * i + 2 * t + 1][g] = acc[i][1];
+    red[warp][8 * i + 2 * t][g + 8] = acc[i][2];
+    red[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+  }
   __syncthreads();
-  const int tok = threadIdx.x >> 4, r = threadIdx.x & 15;
-  if (tok < min(T, 8) && row0 + r < m) {
+  const int r = threadIdx.x & 15;
+  if (row0 + r >= m) return;
+  for (int tok = threadIdx.x >> 4; tok < min(T, 8 * NT); tok += 2 * WARPS) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += red[w][tok][r];  // fixed order
@@ -675,195 +698,6 @@ __global__ void __launch_bounds__(32 * kColWarps, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// y[t, i] = sum_j W[i, j] x[t, j] for 9 to 16 tokens.  Each CTA: 128 rows of W and its share of the
-// blocks; the shares of a tile are a cluster, whose partial sums are added in rank order through
-// distributed shared memory.  Warps: 4 along the rows (32 each) x 2 along the blocks.  The
-// activations of a step pass through shared memory (cp.async, two stages); the codes go straight
-// to registers, one step ahead.  The scale multiplies the bf16 integers (exact for scales of 5
-// significant bits).  Bound by the latency of its short loops: 20 us at 13824 x 5120, 14 at 5120 x
-// 5120 (the tcgen05 form: 28 and 14).
-constexpr int kTileThreads = 256;
-
-// adds the two half-sums and the cluster's shares, and hands every (token, row) of the tile to
-// `store`.  buf: [TOK][COLS + 4] floats.
-template <int TOK, int COLS, typename Put, typename Store>
-__device__ __forceinline__ void tile_reduce(float* buf, bool upper, Put put, Store store) {
-  constexpr int LD = COLS + 4;
-  __syncthreads();  // the stages that share this memory are done
-  if (upper) put(buf, LD, false);
-  __syncthreads();
-  if (!upper) put(buf, LD, true);
-  const int splits = gridDim.z;
-  if (splits == 1) {
-    __syncthreads();
-    for (int o = threadIdx.x; o < TOK * COLS; o += kTileThreads) {
-      const int tok = o / COLS, c = o - tok * COLS;
-      store(tok, c, buf[tok * LD + c]);
-    }
-    return;
-  }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-  const uint32_t local = (uint32_t)__cvta_generic_to_shared(buf);
-  for (int o = (int)blockIdx.z * kTileThreads + threadIdx.x; o < TOK * COLS;
-       o += splits * kTileThreads) {
-    const int tok = o / COLS, c = o - tok * COLS;
-    float v = 0.f;
-    for (int q = 0; q < splits; ++q) {
-      uint32_t addr;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(addr) : "r"(local + 4u * (uint32_t)(tok * LD + c)), "r"(q));
-      float f;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr) : "memory");
-      v += f;
-    }
-    store(tok, c, v);
-  }
-  // no CTA leaves while another still reads its shared memory
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(on ? 16 : 0)
-               : "memory");
-}
-
-// a step of 128 values of the tokens into shared memory rows of LDB bytes; values past `len` (and
-// tokens past T) are zero
-template <int TOK, int LDB>
-__device__ __forceinline__ void stage_tokens(unsigned char* dst, const __nv_bfloat16* x, int T,
-                                             int k0, int len) {
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  for (int e = threadIdx.x; e < TOK * 16; e += kTileThreads) {
-    const int tok = e >> 4, c = (e & 15) * 8;
-    const bool on = tok < T && k0 + c < len;
-    cp_async16_zfill(d + tok * LDB + c * 2, on ? x + (int64_t)tok * len + k0 + c : x, on);
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-constexpr int tile_row_smem(int nt) {
-  const int stages = 2 * 2 * nt * 8 * 320, sums = nt * 8 * (128 + 4) * 4;
-  return stages > sums ? stages : sums;
-}
-// warp (rw, kw) takes rows 32 rw .. 32 rw + 31 of the tile and every second block
-template <int NT, int GS>
-__global__ void __launch_bounds__(kTileThreads, 2)
-    k_q4_tile_rows(const uint8_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
-                   const __nv_bfloat16* __restrict__ x, __nv_bfloat16* __restrict__ y, int T,
-                   int m, int n, int blocks_per_cta) {
-  extern __shared__ __align__(16) unsigned char tile_raw[];
-  constexpr int TOK = 8 * NT, LDB = 320, STAGE = TOK * LDB;
-  constexpr int SG = 128 / GS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rw = warp & 3, kw = warp >> 2;
-  const int row0 = blockIdx.x * 128 + rw * 32;
-  const int nb = n / 128;
-  const int kb_first = blockIdx.z * blocks_per_cta;
-  const int kb_last = min(nb, kb_first + blocks_per_cta);
-  const int iters = (kb_last - kb_first + 1) / 2;
-  int row[4];  // rows g, g + 8, g + 16, g + 24 of the warp's 32
-#pragma unroll
-  for (int i = 0; i < 4; ++i) row[i] = min(row0 + 8 * i + g, m - 1);
-  const uint16_t* sc16 = reinterpret_cast<const uint16_t*>(scales);
-  float acc[2][NT][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int a = 0; a < NT; ++a)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][a][c] = 0.f;
-  uint4 cd[4];
-  uint16_t sc[4][SG];
-  auto load_codes = [&](int kb) {
-    const bool on = kb < kb_last;
-    const int64_t base = (int64_t)(on ? kb : kb_first) * m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cd[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-      if (on) cd[i] = __ldg(reinterpret_cast<const uint4*>(codes + (base + row[i]) * 64) + t);
-#pragma unroll
-      for (int h = 0; h < SG; ++h)
-        sc[i][h] = on ? __ldg(sc16 + (base + row[i]) * SG + h) : (uint16_t)0;
-    }
-  };
-  auto stage = [&](int it) {  // both blocks of iteration `it`
-    unsigned char* d = tile_raw + (it & 1) * 2 * STAGE;
-    const int k0 = (kb_first + 2 * it) * 128;
-    stage_tokens<TOK, LDB>(d, x, T, k0, n);
-    stage_tokens<TOK, LDB>(d + STAGE, x, T, k0 + 128, n);
-  };
-  if (iters > 0) {
-    stage(0);
-    load_codes(kb_first + kw);
-  }
-  for (int it = 0; it < iters; ++it) {
-    if (it + 1 < iters) stage(it + 1);
-    if (it + 1 < iters)
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    uint4 cur[4];
-    uint32_t s2[4][SG];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cur[i] = cd[i];
-#pragma unroll
-      for (int h = 0; h < SG; ++h) s2[i][h] = (uint32_t)sc[i][h] * 0x10001u;
-    }
-    if (it + 1 < iters) load_codes(kb_first + 2 * (it + 1) + kw);
-    const unsigned char* xs = tile_raw + (it & 1) * 2 * STAGE + kw * STAGE;
-    // (a block past the share is left out whole: 0 times an infinity there would be a NaN)
-    const int words = kb_first + 2 * it + kw < kb_last ? 4 : 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w >= words) break;
-      uint32_t p[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t wd = w == 0 ? cur[i].x : w == 1 ? cur[i].y : w == 2 ? cur[i].z : cur[i].w;
-        q4_unpack(wd, p[i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[i][e] = bf2_mul(p[i][e], s2[i][w / (GS / 32)]);
-      }
-#pragma unroll
-      for (int a = 0; a < NT; ++a) {
-        const uint4 xv =
-            *reinterpret_cast<const uint4*>(xs + (a * 8 + g) * LDB + w * 64 + t * 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma16816(acc[i][a], p[2 * i][0], p[2 * i + 1][0], p[2 * i][1], p[2 * i + 1][1], xv.x,
-                   xv.y);
-          mma16816(acc[i][a], p[2 * i][2], p[2 * i + 1][2], p[2 * i][3], p[2 * i + 1][3], xv.z,
-                   xv.w);
-        }
-      }
-    }
-    __syncthreads();  // the stage may be refilled
-  }
-  auto put = [&](float* buf, int ld, bool add) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int a = 0; a < NT; ++a)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float* q = buf + (a * 8 + 2 * t + (c & 1)) * ld + rw * 32 + 16 * i + 8 * (c >> 1) + g;
-          *q = add ? acc[i][a][c] + *q : acc[i][a][c];
-        }
-  };
-  tile_reduce<TOK, 128>(reinterpret_cast<float*>(tile_raw), kw == 1, put,
-                        [&](int tok, int c, float v) {
-                          const int r = blockIdx.x * 128 + c;
-                          if (tok < T && r < m)
-                            y[(int64_t)tok * m + r] = __float2bfloat16_rn(4.f * v);
-                        });
-}
-
-// ---------------------------------------------------------------------------------------
 // Block-diagonal product of up to 8 tokens with its index map; V and W of up to 4 tokens are
 // hi + lo (see k_q4_rows):
 //   gather:  V_j = U_j G_P,j^T, U = X[:, p_P] (also written when `save` is given), V = out + lo;
@@ -1047,29 +881,37 @@ cudaError_t dequant_t(const uint8_t* codes, const void* scales, void* out, int m
   return cudaGetLastError();
 }
 
-template <int GS, int WARPS, bool LAYER>
-cudaError_t rows8_t(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo, int T,
-                    cudaStream_t s) {
+template <int GS, int WARPS, int NT, bool LAYER>
+cudaError_t rows_t(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo, int T,
+                   cudaStream_t s) {
   using B = __nv_bfloat16;
   begin_launch("gemm_w0", s);
   const cudaError_t e = launch_pdl(
-      k_q4_rows<GS, WARPS, LAYER>, dim3((w.m + 15) / 16), dim3(32 * WARPS), kRowD * WARPS * 1024, s,
-      w.codes, static_cast<const uint16_t*>(w.scales), static_cast<const B*>(x),
-      static_cast<B*>(y), static_cast<const B*>(x_lo), static_cast<B*>(y_lo), T, w.m, w.n);
+      k_q4_rows<GS, WARPS, NT, LAYER>, dim3((w.m + 15) / 16), dim3(32 * WARPS),
+      kRowD * WARPS * 1024, s, w.codes, static_cast<const uint16_t*>(w.scales),
+      static_cast<const B*>(x), static_cast<B*>(y), static_cast<const B*>(x_lo),
+      static_cast<B*>(y_lo), T, w.m, w.n);
   end_launch("gemm_w0", s);
   return e;
 }
-template <int GS, bool LAYER>
-cudaError_t rows8_layer(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo,
-                     int T, cudaStream_t s) {
-  // eight warps share a row tile where four would leave fewer than 16 warps on an SM (5120 x 5120:
-  // 6.6 us against 9.4; 13824 x 5120: 12.6 against 11.6)
-  if ((w.m + 15) / 16 < 4 * num_sms()) return rows8_t<GS, 8, LAYER>(w, x, y, x_lo, y_lo, T, s);
-  return rows8_t<GS, 4, LAYER>(w, x, y, x_lo, y_lo, T, s);
+template <int GS, int NT, bool LAYER>
+cudaError_t rows_layer(const Q4Weight& w, const void* x, void* y, const void* x_lo, void* y_lo,
+                       int T, cudaStream_t s) {
+  // Eight warps share a row tile where four would leave fewer than 16 warps on an SM (5120 x 5120:
+  // 6.6 us against 9.4; 13824 x 5120: 12.6 against 11.6); with 16 tokens, at 128 registers a
+  // thread, where two such CTAs an SM hold all tiles (5120 x 5120: 12.4 against 11.3 in two rounds;
+  // 4096 x 4096: 6.4).
+  if ((w.m + 15) / 16 <= (NT == 1 ? 4 * num_sms() - 1 : 2 * num_sms()))
+    return rows_t<GS, 8, NT, LAYER>(w, x, y, x_lo, y_lo, T, s);
+  return rows_t<GS, 4, NT, LAYER>(w, x, y, x_lo, y_lo, T, s);
 }
 template <int GS>
 cudaError_t rows8(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  return rows8_layer<GS, false>(w, x, y, nullptr, nullptr, T, s);
+  return rows_layer<GS, 1, false>(w, x, y, nullptr, nullptr, T, s);
+}
+template <int GS>
+cudaError_t rows16(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
+  return rows_layer<GS, 2, false>(w, x, y, nullptr, nullptr, T, s);
 }
 
 template <int GS>
@@ -1099,49 +941,8 @@ cudaError_t cols8(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream
   cfg.numAttrs = 2;
   begin_launch("gemm_w0", s);
   const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, w.m % 16 == 0 ? k_q4_cols<GS, true> : k_q4_cols<GS, false>, w.codes, static_cast<const uint16_t*>(w.scales),
-      static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx), T, w.m, w.n, per);
-  end_launch("gemm_w0", s);
-  return e;
-}
-
-template <int GS>
-cudaError_t rows16(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  auto kern = k_q4_tile_rows<2, GS>;
-  constexpr int smem = tile_row_smem(2);
-  static bool attr_done[64] = {false};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) dev = 0;
-  if (!attr_done[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_done[dev] = true;
-  }
-  // shares of the blocks: one wave of two CTAs an SM, at least two blocks a share
-  const int tiles = (w.m + 127) / 128, steps = w.n / 128;
-  int64_t splits = 2ll * num_sms() / tiles;
-  if (splits > steps / 2) splits = steps / 2;
-  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
-  const int per = (int)((steps + splits - 1) / splits);
-  splits = (steps + per - 1) / per;  // every share has a block
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, 1, (unsigned)splits);
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = (unsigned)splits;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  begin_launch("gemm_w0", s);
-  const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, kern, w.codes, static_cast<const __nv_bfloat16*>(w.scales),
-      static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(y), T, w.m, w.n, per);
+      &cfg, w.m % 16 == 0 ? k_q4_cols<GS, true> : k_q4_cols<GS, false>, w.codes,
+      static_cast<const uint16_t*>(w.scales), static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx), T, w.m, w.n, per);
   end_launch("gemm_w0", s);
   return e;
 }
@@ -1204,9 +1005,7 @@ cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, 
                               cudaStream_t s) {
   if (T <= 0 || w.m <= 0 || w.n <= 0) return cudaSuccess;
   if (T <= 8) return transpose ? Q4_BY_GROUP(cols8) : Q4_BY_GROUP(rows8);
-  // 9 to 16 tokens on many rows: the warp-level form (13824 x 5120: 20 us against 28, where the
-  // tcgen05 form's tiles leave a quarter of the SMs idle; 5120 x 5120: 14 both)
-  if (!transpose && T <= 16 && w.m >= 64 * 128) return Q4_BY_GROUP(rows16);
+  if (!transpose && T <= 16) return Q4_BY_GROUP(rows16);
   return launch_umma_q4(w, x, y, T, transpose, s);
 }
 #undef Q4_BY_GROUP
@@ -1218,9 +1017,9 @@ cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w
   if (T <= 0 || T > 8) return cudaErrorInvalidValue;
   cudaError_t e = bd<true>(G_P, x, V, V_lo, U, perm_P, T, w.n, b, s);
   if (e != cudaSuccess) return e;
-  e = w.group == 32   ? rows8_layer<32, true>(w, V, W, V_lo, W_lo, T, s)
-      : w.group == 64 ? rows8_layer<64, true>(w, V, W, V_lo, W_lo, T, s)
-                      : rows8_layer<128, true>(w, V, W, V_lo, W_lo, T, s);
+  e = w.group == 32   ? rows_layer<32, 1, true>(w, V, W, V_lo, W_lo, T, s)
+      : w.group == 64 ? rows_layer<64, 1, true>(w, V, W, V_lo, W_lo, T, s)
+                      : rows_layer<128, 1, true>(w, V, W, V_lo, W_lo, T, s);
   if (e != cudaSuccess || !y) return e;
   return bd<false>(G_R, W, y, W_lo, nullptr, perm_R, T, w.m, b, s);
 }

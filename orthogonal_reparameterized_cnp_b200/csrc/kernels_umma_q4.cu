@@ -18,7 +18,7 @@
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
 // Bound by the latency of a chunk's way (below), not by a pipe: at 5120 x 5120, group 128, 16
-// tokens take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128 38.5, 256
+// tokens (transposed) take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128 38.5, 256
 // 43.4; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of 5000 x
 // 4096 15.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
@@ -455,7 +455,9 @@ cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStrea
 
 template <bool TR>
 cudaError_t launch_tr(const Q4Weight& w, const void* x, void* y, int T, cudaStream_t s) {
-  if (T <= 16) return launch_q<16, TR>(w, x, y, T, s);
+  if constexpr (TR) {  // (forward, up to 16 tokens never come here)
+    if (T <= 16) return launch_q<16, TR>(w, x, y, T, s);
+  }
   if (T <= 32) return launch_q<32, TR>(w, x, y, T, s);
   // (rows that the 64 loader threads put together: small token tiles)
   if (T <= 64 || (TR ? w.m : w.n) % 8 != 0) return launch_q<64, TR>(w, x, y, T, s);

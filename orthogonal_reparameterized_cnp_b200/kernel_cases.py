@@ -151,8 +151,8 @@ def q4merge(m, n, group):
 
 
 def q4(T, m, n, group):
-    """Per round one launch forward, one transposed: k_q4_rows and k_q4_cols up to 8 tokens,
-    k_umma_q4 (or k_q4_tile_rows) or k_umma_gemm_pair above."""
+    """Per round one launch forward, one transposed: k_q4_rows up to 16 tokens and k_q4_cols up
+    to 8, then k_umma_q4, then k_umma_gemm_pair."""
     W, q, s = _q4_weight(m, n, group)
     P.quantize_q4(W, q, s, group)
     x = torch.randn(T, n, device=_dev()).to(torch.bfloat16)
