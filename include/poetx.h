@@ -428,7 +428,7 @@ int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, v
  *   POETX_WEIGHT_DENSE  w = W0' [m, n] (dtype); scales, group unused
  *   POETX_WEIGHT_Q8     w = int8 codes, scales fp32 [m] (poetx_merge_perm_q8)
  *   POETX_WEIGHT_Q4     w = 4-bit codes, scales bf16, group (poetx_merge_perm_q4); bf16 layer.
- *                       Up to 8 tokens without dropout run as three launches (gather + block
+ *                       A few tokens without dropout run as three launches (gather + block
  *                       product, weight product, block product + scatter); up to 4 tokens V
  *                       and W go between them as sums of two bf16 numbers (save_w receives W
  *                       in bf16).

@@ -401,7 +401,6 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
   constexpr int SG = 128 / GS, D = kRowD;  // SG: scales per row and block
   extern __shared__ __align__(16) unsigned char row_ring[];
   uint4 (*ring)[WARPS][64] = reinterpret_cast<uint4 (*)[WARPS][64]>(row_ring);  // [D]
-  static_assert(NT == 1 || !LAYER, "hi + lo: one tile of tokens");
   __shared__ float red[WARPS][8 * NT][17];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int row0 = blockIdx.x * 16;
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     xp[i] = reinterpret_cast<const uint4*>(
-        (LAYER ? few_row(x, x_lo, g, T, n) : x + (int64_t)min(8 * i + g, T - 1) * n) +
+        (LAYER && NT == 1 ? few_row(x, x_lo, g, T, n) : x + (int64_t)min(8 * i + g, T - 1) * n) +
         warp * 128 + t * 8);
   RowScales<SG> sa[2], sb[2];
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(&ring[0][warp][lane]);
@@ -514,14 +513,14 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) v += red[w][tok][r];  // fixed order
-    if (LAYER && T <= 4) {
+    if (LAYER && NT == 1 && T <= 4) {
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) v += red[w][tok + 4][r];
     }
     const int64_t o = (int64_t)tok * m + row0 + r;
     const __nv_bfloat16 hi = __float2bfloat16_rn(4.f * v);
     y[o] = hi;
-    if (LAYER && T <= 4) y_lo[o] = lo_part(4.f * v, hi);
+    if (LAYER && NT == 1 && T <= 4) y_lo[o] = lo_part(4.f * v, hi);
   }
 }
 
@@ -698,8 +697,8 @@ __global__ void __launch_bounds__(32 * kColWarps, 2)
 }
 
 // ---------------------------------------------------------------------------------------
-// Block-diagonal product of up to 8 tokens with its index map; V and W of up to 4 tokens are
-// hi + lo (see k_q4_rows):
+// Block-diagonal product of a few tokens (8 a CTA) with its index map; V and W of up to 4 tokens
+// are hi + lo (see k_q4_rows):
 //   gather:  V_j = U_j G_P,j^T, U = X[:, p_P] (also written when `save` is given), V = out + lo;
 //   scatter: Z_j = W_j G_R,j^T, W = in + lo, Y[:, p_R[i]] = Z[:, i].
 // One CTA: 16 rows of one block; its four warps split k and add their sums in a fixed order.  A
@@ -724,6 +723,12 @@ __global__ void __launch_bounds__(32 * kBdWarps)
     pdl_wait();
     pdl_trigger();  // after the wait: what the next launch reads early was there before this one
   }
+  // tokens 8 blockIdx.y ..: `few` of them
+  const int few = min(8, T - 8 * (int)blockIdx.y);
+  const bool two = T <= 4;  // hi + lo
+  in += (int64_t)blockIdx.y * 8 * width;
+  out += (int64_t)blockIdx.y * 8 * width;
+  if (save) save += (int64_t)blockIdx.y * 8 * width;
   uint4 ga[RT][KI], gb[RT][KI], xv[KI];
   const __nv_bfloat16* gp = G + ((int64_t)j * b + i0 + g) * b + k0;
   uint32_t c_out = 0;
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(32 * kBdWarps)
         ga[r][i] = ld_u4(gp + 16 * r * b + 32 * i);
         gb[r][i] = ld_u4(gp + (16 * r + 8) * b + 32 * i);
       }
-    const __nv_bfloat16* x = in + (int64_t)min(g, T - 1) * width;
+    const __nv_bfloat16* x = in + (int64_t)min(g, few - 1) * width;
     uint32_t e[KI][8];
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
@@ -754,7 +759,7 @@ __global__ void __launch_bounds__(32 * kBdWarps)
     for (int i = 0; i < KI; ++i) {
       xv[i] = make_uint4(e[i][0] | e[i][1] << 16, e[i][2] | e[i][3] << 16,
                          e[i][4] | e[i][5] << 16, e[i][6] | e[i][7] << 16);
-      if (save && i0 == 0 && g < T)
+      if (save && i0 == 0 && g < few)
         *reinterpret_cast<uint4*>(save + (int64_t)g * width + j * b + k0 + 32 * i) = xv[i];
     }
   } else {
@@ -768,7 +773,8 @@ __global__ void __launch_bounds__(32 * kBdWarps)
       }
     pdl_trigger();
     pdl_wait();
-    const __nv_bfloat16* w = few_row(in, lo, g, T, width) + j * b + k0;
+    const __nv_bfloat16* w =
+        (two ? few_row(in, lo, g, T, width) : in + (int64_t)min(g, few - 1) * width) + j * b + k0;
 #pragma unroll
     for (int i = 0; i < KI; ++i) xv[i] = ld_u4(w + 32 * i);
   }
@@ -788,13 +794,13 @@ __global__ void __launch_bounds__(32 * kBdWarps)
   }
   __syncthreads();
   const int ot = threadIdx.x >> 4, row = threadIdx.x & 15;  // an output of each row tile
-  if (ot >= T) return;
+  if (ot >= few) return;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kBdWarps; ++w) v += red[r][w][ot][row];
-    if (!GATHER && T <= 4) {
+    if (!GATHER && two) {
 #pragma unroll
       for (int w = 0; w < kBdWarps; ++w) v += red[r][w][ot + 4][row];
     }
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(32 * kBdWarps)
         GATHER ? (uint32_t)(j * b + i0 + 16 * r + row) : min(c_out, (uint32_t)width - 1);
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
     out[(int64_t)ot * width + c] = hi;
-    if (GATHER && T <= 4)
+    if (GATHER && two)
       lo[(int64_t)ot * width + c] = lo_part(v, hi);
   }
 }
@@ -953,7 +959,8 @@ cudaError_t bd_t(const void* G, const void* in, void* out, void* lo, void* save,
   using B = __nv_bfloat16;
   begin_launch("gemm_blockdiag", s);
   const cudaError_t e =
-      launch_pdl(k_bd_rows<KI, RT, GATHER>, dim3(width / (16 * RT)), dim3(32 * kBdWarps), 0, s,
+      launch_pdl(k_bd_rows<KI, RT, GATHER>, dim3(width / (16 * RT), (T + 7) / 8),
+                 dim3(32 * kBdWarps), 0, s,
                  static_cast<const B*>(G), static_cast<const B*>(in), static_cast<B*>(out),
                  static_cast<B*>(lo), static_cast<B*>(save), idx, T, width);
   end_launch("gemm_blockdiag", s);
@@ -1010,16 +1017,23 @@ cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, 
 }
 #undef Q4_BY_GROUP
 
-cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
+cudaError_t launch_q4_few(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
                              void* y, void* U, void* V, void* V_lo, void* W, void* W_lo,
                              const int32_t* perm_P, const int32_t* perm_R, int T, int b,
                              cudaStream_t s) {
-  if (T <= 0 || T > 8) return cudaErrorInvalidValue;
+  if (T <= 0) return cudaErrorInvalidValue;
   cudaError_t e = bd<true>(G_P, x, V, V_lo, U, perm_P, T, w.n, b, s);
   if (e != cudaSuccess) return e;
-  e = w.group == 32   ? rows_layer<32, 1, true>(w, V, W, V_lo, W_lo, T, s)
-      : w.group == 64 ? rows_layer<64, 1, true>(w, V, W, V_lo, W_lo, T, s)
-                      : rows_layer<128, 1, true>(w, V, W, V_lo, W_lo, T, s);
+  if (T <= 8)
+    e = w.group == 32   ? rows_layer<32, 1, true>(w, V, W, V_lo, W_lo, T, s)
+        : w.group == 64 ? rows_layer<64, 1, true>(w, V, W, V_lo, W_lo, T, s)
+                        : rows_layer<128, 1, true>(w, V, W, V_lo, W_lo, T, s);
+  else if (T > 16)
+    e = launch_q4_product(w, V, W, T, false, s);
+  else
+    e = w.group == 32   ? rows_layer<32, 2, true>(w, V, W, nullptr, nullptr, T, s)
+        : w.group == 64 ? rows_layer<64, 2, true>(w, V, W, nullptr, nullptr, T, s)
+                        : rows_layer<128, 2, true>(w, V, W, nullptr, nullptr, T, s);
   if (e != cudaSuccess || !y) return e;
   return bd<false>(G_R, W, y, W_lo, nullptr, perm_R, T, w.m, b, s);
 }

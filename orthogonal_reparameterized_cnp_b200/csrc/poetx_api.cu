@@ -1125,11 +1125,16 @@ cudaError_t gather_x(const poetx_linear_desc* d, const DropArgs* drop, const voi
   return launch_gather(x, U, nullptr, d->perm_P, d->T, d->n, d->n, d->n, es, s);
 }
 
-// Tokens up to which the layer on a 4-bit weight takes the few-token kernels: three launches, with
-// V and W of up to kHiLoTokens tokens between them as hi + lo of two bf16 numbers each.  More keep
-// the five launches (a form of the three for up to 64 tokens gathered x once for every 16 rows of
-// a block: 5120 x 5120, b = 256: 16 tokens 44 us against 34, 64 tokens 71 against 37).
-constexpr int kFewTokens = 8, kHiLoTokens = 4;
+// The layer on a 4-bit weight in three launches (launch_q4_few) instead of five, with V and W of up
+// to kHiLoTokens tokens between them as hi + lo of two bf16 numbers each: up to 16 tokens (b = 256,
+// 5120 x 5120 20.6 us against 30; 8 tokens 12.9), and up to 64 where the block products, which
+// read x by single values once for every 32 rows of a block, stay small (tokens (n + m) b up to
+// 2^26: 64 tokens of 1024 x 1024 14 us against 23, 32 of 3584 x 3584 24 against 30, 24 of 5120 x
+// 5120 31 against 35; past it 32 of 5120 x 5120 37 against 35, 48 42 against 36).
+constexpr int kHiLoTokens = 4;
+bool few_tokens(const poetx_linear_desc* d) {
+  return d->T <= 16 || (d->T <= 64 && (int64_t)d->T * ((int64_t)d->n + d->m) * d->b <= 1 << 26);
+}
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
 // Writes U (if U != x-gather target), V, W; Z and y only when y != nullptr.
@@ -1140,9 +1145,9 @@ int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, con
   const int T = d->T, n = d->n, m = d->m, b = d->b;
   const bool bf = d->dtype == POETX_BF16;
   const int es = bf ? 2 : 4;
-  if (w0.q4.codes && !drop && T <= kFewTokens) {
-    POETX_CUDA(launch_q4_layer8(G_P, G_R, w0.q4, x, y, U, V, w0.v_lo, W, w0.w_lo, d->perm_P,
-                                d->perm_R, T, b, s),
+  if (w0.q4.codes && !drop && few_tokens(d)) {
+    POETX_CUDA(launch_q4_few(G_P, G_R, w0.q4, x, y, U, V, w0.v_lo, W, w0.w_lo, d->perm_P,
+                                 d->perm_R, T, b, s),
                "few-token layer");
     return POETX_OK;
   }

@@ -111,10 +111,10 @@ cudaError_t launch_q4_product(const Q4Weight& w, const void* x, void* y, int T, 
 // the same on tcgen05 with the weight as the M operand (kernels_umma_q4.cu)
 cudaError_t launch_umma_q4(const Q4Weight& w, const void* x, void* y, int T, bool transpose,
                            cudaStream_t s);
-// The layer's forward on up to 8 tokens (b % 128 == 0, no dropout) in three launches: gather +
+// The layer's forward on a few tokens (b % 128 == 0, no dropout) in three launches: gather +
 // block product, weight product, block product + scatter (left out when y is NULL).  V and W of up to
 // 4 tokens go between them as hi + lo, two bf16 numbers each; U is written if given.
-cudaError_t launch_q4_layer8(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
+cudaError_t launch_q4_few(const void* G_P, const void* G_R, const Q4Weight& w, const void* x,
                              void* y, void* U, void* V, void* V_lo, void* W, void* W_lo,
                              const int32_t* perm_P, const int32_t* perm_R, int T, int b,
                              cudaStream_t s);

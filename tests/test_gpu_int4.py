@@ -381,7 +381,9 @@ def test_decoding_in_a_graph_while_a_step_runs(P):
 
 @pytest.mark.parametrize("T,n,m,b,group", [(1, 512, 768, 128, 64), (3, 1024, 512, 256, 32),
                                            (4, 2560, 256, 256, 128), (2, 512, 1024, 512, 128),
-                                           (7, 512, 2048, 512, 128), (8, 2560, 256, 256, 128)])
+                                           (7, 512, 2048, 512, 128), (8, 2560, 256, 256, 128),
+                                           (11, 512, 768, 128, 32), (16, 768, 512, 256, 64),
+                                           (19, 512, 1024, 256, 128), (32, 256, 768, 128, 64)])
 def test_roundings_of_the_few_token_layer(P, T, n, m, b, group):
     """y is off by half a step (2^-8) and by what V and W are off by: half a step each, or up to 4
     tokens, where they are sums of two bf16 numbers, 2^-16 (half a step of half a step); the fp32
