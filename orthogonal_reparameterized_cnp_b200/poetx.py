@@ -412,7 +412,7 @@ def _ptrs(*tensors):
     launch on that device's stream.  (Checked here once, in plain ifs: a decoding call's time on
     the host counts.)"""
     import torch
-    dev = torch.cuda.current_device()
+    dev = torch.cuda.current_device()  # (raises without a CUDA device)
     out = []
     for t in tensors:
         if t is None:
@@ -445,13 +445,12 @@ def _check_q4(q, scales, m, n, group):
 
 def _check_map(idx, n, what):
     import torch
-    _require(idx is None or (idx.dtype == torch.int32 and tuple(idx.shape) == (n,)),
-             f"{what} must be int32 with {n} entries")
+    if idx is not None and (idx.dtype is not torch.int32 or idx.shape != (n,)):
+        raise ValueError(f"{what} must be int32 with {n} entries")
 
 
 def quantize_q4(W, q, scales, group: int, stream=None):
     """4-bit codes and group scales of W (format and rounding: see the header)."""
-    _require_cuda()
     m, n = W.shape
     _check_q4(q, scales, m, n, group)
     _check(_load().poetx_quantize_q4(*_ptrs(W, q, scales), m, n, group, _dtype_code(W),
@@ -461,7 +460,6 @@ def quantize_q4(W, q, scales, group: int, stream=None):
 def merge_perm_q4(W0, q, scales, perm_R, perm_P, group: int, stream=None):
     """4-bit codes and group scales of W0' = W0[perm_R][:, perm_P], without forming W0' (both
     maps None: identity)."""
-    _require_cuda()
     m, n = W0.shape
     _check_q4(q, scales, m, n, group)
     _check_map(perm_R, m, "perm_R")
@@ -473,7 +471,6 @@ def merge_perm_q4(W0, q, scales, perm_R, perm_P, group: int, stream=None):
 
 def dequantize_q4(q, scales, out, group: int, stream=None):
     """out [m, n] (bf16 or fp32) = the weight that 4-bit codes and scales stand for."""
-    _require_cuda()
     m, n = out.shape
     _check_q4(q, scales, m, n, group)
     _check(_load().poetx_dequantize_q4(*_ptrs(q, scales, out), m, n, group, _dtype_code(out),
@@ -511,7 +508,6 @@ def dropout_desc(p: float, seed: int, site: int = 0, row0: int = 0, step=None) -
 
 def dropout(drop: DropoutDesc, x, out, stream=None):
     """out = dropout(x) (out may be x); the backward is the same call on the gradient."""
-    _require_cuda()
     rows, cols = x.shape
     _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
     a, o, _ = _ptrs(x, out, drop.keep)
@@ -522,7 +518,6 @@ def dropout(drop: DropoutDesc, x, out, stream=None):
 def permute_cols_dropout(drop: DropoutDesc, x, out, idx, mask_output: bool = False, stream=None):
     """out[:, i] = dropout(x)[:, idx[i]], or (mask_output) x[:, idx[i]] masked by the output
     column: with the inverse map, the gradient of the first form."""
-    _require_cuda()
     rows, cols = x.shape
     _require(out.shape == x.shape and out.dtype == x.dtype, "out must be like x")
     _check_map(idx, cols, "idx")
