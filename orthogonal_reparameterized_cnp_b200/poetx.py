@@ -558,8 +558,9 @@ class Dropout:
 # ------------------------------------------------------------------------ layer, any weight
 def _hold(w: LinearWeight, *tensors) -> LinearWeight:
     w.keep, w.device = tensors, tensors[0].get_device()
-    if any(t.get_device() != w.device for t in tensors):
-        raise ValueError("the tensors of a weight must be on one device")
+    for t in tensors:
+        if t.get_device() != w.device:
+            raise ValueError("the tensors of a weight must be on one device")
     return w
 
 
