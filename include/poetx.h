@@ -349,7 +349,8 @@ int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* d
  * Other bf16 scales (written by the caller) are accepted: s q is then rounded to bf16, except
  * in forward products of up to 16 tokens, which may scale fp32 sums instead.
  *
- * Layout (n % 128 == 0, any m, m n < 2^36): blocks of 128 columns, each with every row's part side by side:
+ * Layout (n % 128 == 0, any m, m n < 2^36): blocks of 128 columns, each with every row's part
+ * side by side:
  *   q       uint8 [n/128, m, 64]: a row's 64 bytes of a block are four 16-byte chunks t of four
  *           little-endian 32-bit words w; word (t, w) holds columns 32 w + 8 t + e (e < 8) of
  *           the block, column e as q + 8 in bits [4 p, 4 p + 4), p = e / 2 + 4 (e % 2).

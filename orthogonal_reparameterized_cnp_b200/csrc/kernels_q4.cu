@@ -948,7 +948,8 @@ cudaError_t cols8(const Q4Weight& w, const void* dy, void* dx, int T, cudaStream
   begin_launch("gemm_w0", s);
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, w.m % 16 == 0 ? k_q4_cols<GS, true> : k_q4_cols<GS, false>, w.codes,
-      static_cast<const uint16_t*>(w.scales), static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dx), T, w.m, w.n, per);
+      static_cast<const uint16_t*>(w.scales), static_cast<const __nv_bfloat16*>(dy),
+      static_cast<__nv_bfloat16*>(dx), T, w.m, w.n, per);
   end_launch("gemm_w0", s);
   return e;
 }

@@ -18,9 +18,9 @@
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
 // Bound by the latency of a chunk's way (below), not by a pipe: at 5120 x 5120, group 128, 16
-// tokens (transposed) take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128 38.5, 256
-// 43.4; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of 5000 x
-// 4096 15.
+// tokens (transposed) take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128
+// 38.5, 256 43.4; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of
+// 5000 x 4096 15.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.
 #include <cuda.h>
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
       // a run of up to 8 such pieces a thread is loaded while the run before it is stored
       constexpr int TS = 4 * C::TW, PER = NT / TS;  // tokens apart, pieces of a thread and chunk
       constexpr int RUN = PER < 8 ? PER : 8, RUNS = PER / RUN;
-      // The thread's pieces are column chunk c of tokens t0, t0 + TS, ..: whole words apart, so they
-      // start on the same side of a word.
+      // The thread's pieces are column chunk c of tokens t0, t0 + TS, ..: whole words apart, so
+      // they start on the same side of a word.
       const int t0 = tid >> 3, c = tid & 7;
       const int64_t total = (int64_t)p.T * p.K, whole = total >> 1;  // values; whole words
       const int64_t row = (int64_t)(tok0 + t0) * p.K;
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
       const int rows = TR ? min(64, p.m - k) : min(128, p.m - row0);
       if (!ok) {
       } else if (p.bulk_scales && (!TR || rows == 64)) {
-        q4_convert<TR ? 64 : 128, GT, true>(src, ssrc, dst, gt, (uint32_t)it & 1u, sg, rows, nullptr);
+        q4_convert<TR ? 64 : 128, GT, true>(src, ssrc, dst, gt, (uint32_t)it & 1u, sg, rows,
+                                            nullptr);
       } else {
         // (a chunk past the sum: rows <= 0, zeros; its scales' place is the last row's)
         const int64_t row = TR ? (int64_t)blockIdx.x * p.m + min(k, p.m - 1)

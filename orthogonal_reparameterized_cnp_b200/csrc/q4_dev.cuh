@@ -213,8 +213,8 @@ __device__ __forceinline__ uint32_t q4_scale_bits(uint32_t amax_bits) {
 }
 
 // q = the integer nearest to w / s (ties to even), in [-7, 7]; inv = 1 / s within two units in
-// the last place.  w * inv is within 2^-19 of w / s, so its rounding can only be off where w / s lies next to a half; the
-// residual w - q s is exact in fp32 (both are multiples of the finer unit and it is below s),
+// the last place.  w * inv is within 2^-19 of w / s, so its rounding can only be off where w / s
+// lies next to a half; the residual w - q s is exact in fp32 (both are multiples of the finer unit and it is below s),
 // and it decides those cases.
 __device__ __forceinline__ int q4_code(float w, float s, float inv, float half_s) {
   float q = rintf(w * inv);
