@@ -577,13 +577,20 @@ def linear_weight_q4(W0q, scales, group: int) -> LinearWeight:
 
 
 def _check_weight(desc: LinearDesc, w: LinearWeight):
-    """(Once for a weight and layer: the weight holds its tensors.)"""
-    fits = (desc.m, desc.n, desc.dtype)
-    if w.fits == fits:
-        return
+    """(Once for a weight and layer: the weight holds its tensors.)  A tensor whose storage was
+    exchanged since (``tensor.data = ...``) is pointed to and checked anew."""
     if not w.keep:
         raise ValueError("a weight comes from linear_weight_dense, linear_weight_q8 or "
                          "linear_weight_q4")
+    for field, t in zip(("w", "scales"), w.keep):
+        if t.data_ptr() != (getattr(w, field) or 0):
+            if t.get_device() != w.device:
+                raise ValueError("the tensors of a weight must be on one device")
+            setattr(w, field, _ptr(t))
+            w.fits = None
+    fits = (desc.m, desc.n, desc.dtype)
+    if w.fits == fits:
+        return
     if w.kind == POETX_WEIGHT_Q4:
         _check_q4(*w.keep, desc.m, desc.n, w.group)
     elif w.kind == POETX_WEIGHT_Q8:
@@ -742,7 +749,9 @@ class PoetxLinear:
     The permutations are merged into W0' once, at construction (and again by merge()).
 
     The merged weight is kept in W0's type, in int8 (int8_weight) or in 4 bits with a scale per
-    int4_group (32, 64 or 128) columns.  dropout (a Dropout) acts on the layer's input while
+    int4_group (32, 64 or 128) columns: ``W0p``, or ``W0q`` and ``scales``, which are the tensors of
+    ``weight``, the one that every call reads.  Another tensor may be assigned to each (of the same
+    shape, type and device, contiguous).  dropout (a Dropout) acts on the layer's input while
     ``training`` is true; step() moves its counter.
     """
 
@@ -770,7 +779,6 @@ class PoetxLinear:
         self.perm_P, self.inv_P = torch.as_tensor(pP, **i32), torch.as_tensor(iP, **i32)
         self.perm_R, self.inv_R = torch.as_tensor(pR, **i32), torch.as_tensor(iR, **i32)
         self.W0 = W0
-        self.W0p = None if int8_weight or int4_group else torch.empty_like(W0)
         if cnp is None:
             cnp = CnpBuffers(nblk, b, k, dev, W0.dtype if self.bf16 else None)
             first_block = 0
@@ -798,16 +806,20 @@ class PoetxLinear:
         if int8_weight:
             if not self.bf16:
                 raise ValueError("the int8 base weight needs the bf16 layer")
-            self.W0q = torch.empty((self.m, self.n), dtype=torch.int8, device=dev)
-            self.scales = torch.empty((self.m,), dtype=torch.float32, device=dev)
+            self.weight = linear_weight_q8(
+                torch.empty((self.m, self.n), dtype=torch.int8, device=dev),
+                torch.empty((self.m,), dtype=torch.float32, device=dev))
         # 4-bit merged weight: codes + group scales (bf16)
         self.int4_group = int4_group
         if int4_group:
             if not self.bf16:
                 raise ValueError("the 4-bit base weight needs the bf16 layer")
             qs, ss = q4_shapes(self.m, self.n, int4_group)
-            self.W0q = torch.empty(qs, dtype=torch.uint8, device=dev)
-            self.scales = torch.empty(ss, dtype=torch.bfloat16, device=dev)
+            self.weight = linear_weight_q4(torch.empty(qs, dtype=torch.uint8, device=dev),
+                                           torch.empty(ss, dtype=torch.bfloat16, device=dev),
+                                           int4_group)
+        if not int8_weight and not int4_group:
+            self.weight = linear_weight_dense(torch.empty_like(W0))
         self.dropout = dropout
         self.training = True
         need = _layer_scratch_bytes(self.desc, self.save, int8_weight, int4_group)
@@ -816,15 +828,52 @@ class PoetxLinear:
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("shared layer scratch too small")
         self.ws = ws
-        if int8_weight:  # the merged weight exists only as int8 codes (merge_perm_q8)
-            self.W0p = None
-        if int4_group:
-            self.weight = linear_weight_q4(self.W0q, self.scales, int4_group)
-        elif int8_weight:
-            self.weight = linear_weight_q8(self.W0q, self.scales)
-        else:
-            self.weight = linear_weight_dense(self.W0p)
         self.merge()
+
+    # The merged weight has one holder, `weight`; these are its tensors by name.
+    def _weight_tensor(self, i: int, coded: bool):
+        return self.weight.keep[i] if (self.weight.kind != POETX_WEIGHT_DENSE) == coded else None
+
+    def _replace_weight(self, i: int, coded: bool, t):
+        kind = self.weight.kind
+        if t is None or (kind != POETX_WEIGHT_DENSE) != coded:
+            raise ValueError("the merged weight is W0p (a layer in W0's type), or W0q and scales "
+                             "(int8, 4 bits)")
+        if t.get_device() != self.weight.device:
+            raise ValueError(f"the merged weight is on CUDA device {self.weight.device}")
+        keep = list(self.weight.keep)
+        keep[i] = t
+        w = (linear_weight_q4(*keep, self.int4_group) if kind == POETX_WEIGHT_Q4 else
+             linear_weight_q8(*keep) if kind == POETX_WEIGHT_Q8 else linear_weight_dense(*keep))
+        _check_weight(self.desc, w)
+        self.weight = w
+
+    @property
+    def W0p(self):
+        """The merged weight in W0's type; None in the int8 and 4-bit forms."""
+        return self._weight_tensor(0, False)
+
+    @W0p.setter
+    def W0p(self, t):
+        self._replace_weight(0, False, t)
+
+    @property
+    def W0q(self):
+        """The codes of the int8 or 4-bit merged weight."""
+        return self._weight_tensor(0, True)
+
+    @W0q.setter
+    def W0q(self, t):
+        self._replace_weight(0, True, t)
+
+    @property
+    def scales(self):
+        """The scales of the int8 or 4-bit merged weight."""
+        return self._weight_tensor(1, True)
+
+    @scales.setter
+    def scales(self, t):
+        self._replace_weight(1, True, t)
 
     def _drop(self):
         """Descriptor of the active dropout, or None."""
