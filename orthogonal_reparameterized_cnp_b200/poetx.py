@@ -753,6 +753,10 @@ class PoetxLinear:
     ``weight``, the one that every call reads.  Another tensor may be assigned to each (of the same
     shape, type and device, contiguous).  dropout (a Dropout) acts on the layer's input while
     ``training`` is true; step() moves its counter.
+
+    T is the largest number of tokens (rows) of a call: forward(), backward() and step() also take
+    fewer, a last ragged batch or the few tokens of decoding, with the same weight.  A backward takes
+    as many as the forward before it.
     """
 
     def __init__(self, W0, theta_P, theta_R, perm_P, perm_R, b: int, k: int, T: int,
@@ -828,6 +832,8 @@ class PoetxLinear:
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("shared layer scratch too small")
         self.ws = ws
+        self._need = {}  # scratch bytes by number of tokens (below T)
+        self._more = {}  # the scratch of those that need more than T tokens do
         self.merge()
 
     # The merged weight has one holder, `weight`; these are its tensors by name.
@@ -896,31 +902,53 @@ class PoetxLinear:
     def cnp_forward(self, stream=None):
         self.cnp.forward(stream)
 
+    def _tokens(self, lead, width, outer):
+        """Descriptor, save buffers and scratch for the tokens of `lead` ([tokens, width]), T or
+        fewer; outer: the call's tensors, as _check_layer takes them (the calls without dropout on
+        a dense or int8 weight check none themselves)."""
+        T = lead.numel() // width
+        if T >= self.T:  # (more: the dense and int8 calls take the first T, the others refuse them)
+            return self.desc, self.U, self.Wsave, self.ws
+        desc = LinearDesc.from_buffer_copy(self.desc)
+        desc.T = T
+        _check_layer(desc, self.weight, outer, *self.G_ops())
+        need = self._need.get(T)
+        if need is None:
+            need = self._need[T] = _layer_scratch_bytes(desc, self.save, self.int8,
+                                                        self.int4_group)
+        ws = self.ws
+        if need > ws.nbytes:  # (up to 4 tokens of a layer of 5; other splits of the dG sums)
+            ws = self._more.get(T)
+            if ws is None:
+                ws = self._more[T] = self.ws.new_empty(need)
+        if not self.save:
+            return desc, None, None, ws
+        return desc, self.U[:T], self.Wsave[:T], ws
+
     def forward(self, x, y, stream=None):
         GP, GR = self.G_ops()
         drop = self._drop()
+        desc, U, W, ws = self._tokens(x, self.n, ((x, self.n), (y, self.m)))
         if self.int4_group or drop is not None:
-            linear_fwd_ex(self.desc, self.weight, drop, x, GP, GR, y, self.U, self.Wsave, self.ws,
-                          stream)
+            linear_fwd_ex(desc, self.weight, drop, x, GP, GR, y, U, W, ws, stream)
         elif self.int8:
-            linear_fwd_q8(self.desc, x, GP, GR, self.W0q, self.scales, y, self.U, self.Wsave,
-                          self.ws, stream)
+            linear_fwd_q8(desc, x, GP, GR, self.W0q, self.scales, y, U, W, ws, stream)
         else:
-            linear_fwd(self.desc, x, GP, GR, self.W0p, y, self.U, self.Wsave, self.ws, stream)
+            linear_fwd(desc, x, GP, GR, self.W0p, y, U, W, ws, stream)
 
     def backward(self, x, dy, dx, accumulate=0, stream=None):
         GP, GR = self.G_ops()
         drop = self._drop()
+        dGP, dGR = self.dG[: self.nP], self.dG[self.nP:]
+        desc, U, W, ws = self._tokens(dy, self.m, ((x, self.n), (dy, self.m), (dx, self.n)))
         if self.int4_group or drop is not None:
-            linear_bwd_ex(self.desc, self.weight, drop, x, dy, GP, GR, self.U, self.Wsave, dx,
-                          self.dG[: self.nP], self.dG[self.nP:], accumulate, self.ws, stream)
+            linear_bwd_ex(desc, self.weight, drop, x, dy, GP, GR, U, W, dx, dGP, dGR, accumulate,
+                          ws, stream)
         elif self.int8:
-            linear_bwd_q8(self.desc, x, dy, GP, GR, self.W0q, self.scales, self.U, self.Wsave,
-                          dx, self.dG[: self.nP], self.dG[self.nP:], accumulate, self.ws,
-                          stream)
+            linear_bwd_q8(desc, x, dy, GP, GR, self.W0q, self.scales, U, W, dx, dGP, dGR,
+                          accumulate, ws, stream)
         else:
-            linear_bwd(self.desc, x, dy, GP, GR, self.W0p, self.U, self.Wsave, dx,
-                       self.dG[: self.nP], self.dG[self.nP:], accumulate, self.ws, stream)
+            linear_bwd(desc, x, dy, GP, GR, self.W0p, U, W, dx, dGP, dGR, accumulate, ws, stream)
 
     def cnp_backward(self, stream=None):
         """dtheta from dG; reads Q, S and F' of the last cnp_forward (theta unchanged)."""
