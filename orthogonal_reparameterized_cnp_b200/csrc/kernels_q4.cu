@@ -38,6 +38,10 @@ __device__ __forceinline__ float q4_f32<uint16_t>(uint16_t v) {
 // the residual w - q s sends the elements next to a half through the exact decision of q4_code.
 // Codes are put together as fp32 sums (16 u1 + u0 ...), which keeps the work on the multiply-add
 // pipe.
+//
+// More than 8192 columns: four words a thread (MAXW = 4), held to 64 registers so that two CTAs run
+// on an SM (128 and one CTA otherwise; 8 spilled bytes in the bf16 forms, 84 in the fp32 ones).
+// 5120 x 13824, groups of 64: bf16 77 -> 65 us, fp32 111 -> 91.
 template <typename E>
 struct Pair;  // a column of two rows
 template <>
@@ -119,7 +123,7 @@ __device__ __forceinline__ uint32_t q4_word(const float (&w)[8], uint32_t sb) {
 }
 
 template <typename E, int GS, int MAXW>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, MAXW == 4 ? 2 : 0)  // (0: not given)
     k_merge_q4_pairs(const E* __restrict__ W0, const int32_t* __restrict__ perm_R,
                      const int32_t* __restrict__ perm_P, uint8_t* __restrict__ codes,
                      __nv_bfloat16* __restrict__ scales, int m, int n) {
@@ -830,12 +834,12 @@ cudaError_t merge_pairs_t(const void* W0, const int32_t* pR, const int32_t* pP, 
   // two rows as they come, for bf16 interleaved as well
   const size_t smem = (sizeof(E) == 2 ? 4 : 2) * (size_t)n * sizeof(E);
   const int threads = (n / 8 + MAXW * 32 - 1) / (MAXW * 32) * 32;
-  int per_sm = (int)((224 * 1024) / (smem + 1024));
-  // as many CTAs as an SM holds at 64 registers a thread, so that all run at once (one more a
-  // SM: 5120 x 5120 bf16 30.1 us against 25.3)
-  const int by_threads = 1024 / threads;
-  per_sm = per_sm < 1 ? 1 : per_sm > by_threads ? by_threads : per_sm;
-  per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+  // as many CTAs as an SM holds, so that all run at once (one more a SM: 5120 x 5120 bf16 30.1 us
+  // against 25.3)
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  if (e != cudaSuccess) return e;
+  per_sm = per_sm < 1 ? 1 : per_sm;
   int grid = num_sms() * per_sm;
   if (grid > (m + 1) / 2) grid = (m + 1) / 2;
   begin_launch("quant", s);
