@@ -13,7 +13,8 @@
 //   warp 0       bulk loads of codes and scales into slots (contiguous runs, see q4_dev.cuh)
 //   warp 1       TMEM allocation, MMA issue
 //   warps 2 ..   the tokens' operand: one thread's TMA loads, or, where rows are not whole 16-byte
-//                vectors, words put together and stored by four warps
+//                vectors (transposed, up to 64 tokens a tile), words put together and stored by
+//                four warps
 //   then         G groups that convert every G-th chunk each; then the epilogue
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
@@ -52,7 +53,12 @@ struct QCfg {
   static constexpr int STAGES = NT <= 32 ? 4 : NT <= 128 ? 3 : 2;  // of two chunks
   static constexpr int G = NT <= 32 ? 8 : NT == 64 ? 6 : NT == 128 ? 4 : 2;
   static constexpr int GT = NT <= 64 ? 64 : NT == 128 ? 128 : 256;  // threads of a group
-  static constexpr int TW = NT <= 64 ? 4 : 2;     // warps of token loaders
+  // token rows that are not whole vectors: only transposed (forward rows are n % 128 == 0 long),
+  // and only in tiles of up to 64 tokens, whose threads have the registers for the words
+  static constexpr bool words = TR && NT <= 64;
+  // warps of token loaders (TMA needs one thread; with a second warp 128 tokens of 13824 x 5120
+  // take 39.4 us, with one 39.1, but 256 tokens of 5120 x 5120 24.8 with one and 24.2 with two)
+  static constexpr int TW = words ? 4 : NT == 128 ? 1 : 2;
   static constexpr int first = 64 + 32 * TW;      // thread of the first group
   static constexpr int threads = first + G * GT;
   // tiles of 128 rows x 128 columns: two chunks in either direction
@@ -64,6 +70,7 @@ struct QCfg {
   static constexpr uint32_t tmem_cols = NT < 32 ? 32 : NT;
   static_assert(G <= 2 * STAGES && SLOTS % (G / 2) == 0, "phases");
   static_assert(smem <= 227 * 1024 && threads <= 1024, "resources");
+  static_assert(threads >= 512, "the epilogue's warps 8 .. 15");
   static_assert(sums <= 2 * STAGES * (kABytes + B), "sums fit the stages");
   static_assert(8 * (2 * STAGES + 2 * SLOTS + 2) <= 512, "barriers");
 };
@@ -127,7 +134,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < RS; ++s) {
       // the converter groups of its chunks; the TMA thread (and its bytes), or the token loaders
-      mbar_init(full_bar(s), 2 + (p.vec ? 1 : 32 * C::TW));
+      mbar_init(full_bar(s), 2 + (!C::words || p.vec ? 1 : 32 * C::TW));
       mbar_init(empty_bar(s), 1);
     }
     for (int j = 0; j < C::SLOTS; ++j) {
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
   } else if (warp < 2 + C::TW) {
     // ------------------------------------------------------------ tokens
     const int tid = threadIdx.x - 64;
-    if (p.vec) {
+    if (!C::words || p.vec) {
       if (tid == 0) {
         int it = 0;
         bool ok = true;
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(QCfg<NT, TR>::threads, 1)
           for (int j = (it > RS ? it - RS : 0); j < it; ++j)
             mbar_drain_wait(full_bar(j % RS), (j / RS) & 1);
       }
-    } else {
+    } else if constexpr (C::words) {
       // 8 values from any 2-byte boundary: the five aligned words around them, shifted together;
       // a run of up to 8 such pieces a thread is loaded while the run before it is stored
       constexpr int TS = 4 * C::TW, PER = NT / TS;  // tokens apart, pieces of a thread and chunk
@@ -418,6 +425,7 @@ cudaError_t launch_q(const Q4Weight& w, const void* x, void* y, int T, cudaStrea
   p.chunks = (p.K + 63) / 64;
   p.bulk_scales = ((int64_t)w.m * p.sg) % 8 == 0;
   p.vec = p.K % 8 == 0;
+  if (!p.vec && !C::words) return cudaErrorInvalidValue;
   p.err = device_error_flag();
   if (!p.err) return cudaErrorInvalidDevice;  // the bounded waits need the flag
   p.wait_ns = wait_limit_ns();
@@ -460,8 +468,8 @@ cudaError_t launch_tr(const Q4Weight& w, const void* x, void* y, int T, cudaStre
     if (T <= 16) return launch_q<16, TR>(w, x, y, T, s);
   }
   if (T <= 32) return launch_q<32, TR>(w, x, y, T, s);
-  // (rows that the 64 loader threads put together: small token tiles)
-  if (T <= 64 || (TR ? w.m : w.n) % 8 != 0) return launch_q<64, TR>(w, x, y, T, s);
+  // (rows that the loader threads put together: small token tiles)
+  if (T <= 64 || (TR && w.m % 8 != 0)) return launch_q<64, TR>(w, x, y, T, s);
   if (T <= 128) return launch_q<128, TR>(w, x, y, T, s);
   return launch_q<256, TR>(w, x, y, T, s);
 }

@@ -38,3 +38,10 @@ def test_wide_merge_runs_two_blocks_on_a_multiprocessor():
     assert len(got) == 18 and len(wide) == 6  # (types x groups x words a thread)
     for args, registers, spilled in wide:
         assert 2 * 512 * registers <= 65536 and spilled <= 4 * 32, (args, registers, spilled)
+
+
+def test_products_of_tens_of_tokens_keep_their_values_in_registers():
+    """No spills in any token tile, in either direction."""
+    got = _report("kernels_umma_q4.cu", "k_umma_q4")
+    assert len(got) == 9  # (tiles of 32 .. 256 tokens, of 16 transposed only)
+    assert [g for g in got if g[2]] == []
