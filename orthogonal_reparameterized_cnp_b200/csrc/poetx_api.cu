@@ -1135,9 +1135,12 @@ constexpr int kHiLoTokens = 4;
 bool few_tokens(const poetx_linear_desc* d) {
   return d->T <= 16 || (d->T <= 64 && (int64_t)d->T * ((int64_t)d->n + d->m) * d->b <= 1 << 26);
 }
+bool few_path(const poetx_linear_desc* d, const W0Ref& w0, const DropArgs* drop) {
+  return w0.q4.codes && !drop && few_tokens(d);
+}
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
-// Writes U (if U != x-gather target), V, W; Z and y only when y != nullptr.
+// Writes U (which few_path alone may do without: nullptr), V, W; Z and y only when y != nullptr.
 int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, const void* G_R,
                  const W0Ref& w0, const DropArgs* drop, void* y, void* U, void* V, void* W,
                  void* Z, cudaStream_t s) {
@@ -1145,7 +1148,7 @@ int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, con
   const int T = d->T, n = d->n, m = d->m, b = d->b;
   const bool bf = d->dtype == POETX_BF16;
   const int es = bf ? 2 : 4;
-  if (w0.q4.codes && !drop && few_tokens(d)) {
+  if (few_path(d, w0, drop)) {
     POETX_CUDA(launch_q4_few(G_P, G_R, w0.q4, x, y, U, V, w0.v_lo, W, w0.w_lo, d->perm_P,
                                  d->perm_R, T, b, s),
                "few-token layer");
@@ -1207,7 +1210,7 @@ int linear_fwd_impl(const poetx_linear_desc* d, const void* x, const void* G_P, 
   if (L.total && !ws) return fail(POETX_ERR_INVALID_ARG, "scratch is NULL");
   if ((st = check_opt(ws)) != POETX_OK) return st;
   Carve cv(ws);
-  void* U = save_u ? save_u : cv.take(L.U);
+  void* U = save_u || few_path(d, w0, drop) ? save_u : cv.take(L.U);
   void* V = cv.take(L.V);
   void* W = save_w ? save_w : cv.take(L.W);
   void* Z = cv.take(L.Z);

@@ -191,3 +191,22 @@ def test_refusals_of_token_counts(P, kind):
             L.backward(a, d, o)
     with pytest.raises(ValueError):  # rows that are not side by side
         L.forward(x[::2], y[:3])
+
+
+@pytest.mark.parametrize("T,n,m", [(1, 256, 384), (4, 512, 256), (9, 256, 256), (40, 384, 256)])
+def test_few_tokens_that_save_nothing_write_v_and_w_alone(P, T, n, m):
+    """The three launches of a few tokens keep V and W in scratch (up to 4 tokens as two bf16
+    numbers each), not the gathered input nor Z; the outputs are those of a call that saves."""
+    import torch
+    L, x, dy = _layer(P, "q4", T, n, m)
+    y, z = torch.empty_like(dy), torch.empty_like(dy)
+    L.forward(x, y)
+    GP, GR = L.G_ops()
+    room = P.linear_ex_workspace(L.desc, L.weight, False, False)
+    ws = torch.full((room,), 0xA5, dtype=torch.uint8, device="cuda")
+    P.linear_fwd_ex(L.desc, L.weight, None, x, GP, GR, z, None, None, ws)
+    assert torch.equal(y, z)
+    written = int((ws.view(torch.int16) != -23131).sum())  # (0xA5A5 as a bf16 is an unlikely value)
+    halves = 2 if T <= 4 else 1
+    assert 0.9 * halves * T * (n + m) <= written <= halves * T * (n + m)
+    assert torch.equal(L.U, x[:, L.perm_P.long()])
