@@ -55,7 +55,7 @@ class LinearWeight(ctypes.Structure):
     _fields_ = [("kind", _c_i32), ("group", _c_i32), ("w", _vp), ("scales", _vp)]
     keep = ()  # the tensors of the weight (linear_weight_dense, _q8, _q4), on one device
     device = -1
-    fits = None  # the (m, n, dtype) that they were checked against last
+    fits = None  # the (m, n, dtype) and addresses with which they were checked last
 
 
 _descp = ctypes.POINTER(LinearDesc)
@@ -578,19 +578,19 @@ def linear_weight_q4(W0q, scales, group: int) -> LinearWeight:
 
 def _check_weight(desc: LinearDesc, w: LinearWeight):
     """(Once for a weight and layer: the weight holds its tensors.)  A tensor whose storage was
-    exchanged since (``tensor.data = ...``) is pointed to and checked anew."""
+    exchanged since (``tensor.data = ...``) is checked and pointed to anew."""
     if not w.keep:
         raise ValueError("a weight comes from linear_weight_dense, linear_weight_q8 or "
                          "linear_weight_q4")
-    for field, t in zip(("w", "scales"), w.keep):
-        if t.data_ptr() != (getattr(w, field) or 0):
+    at, end = w.keep[0].data_ptr(), w.keep[-1].data_ptr()
+    fits = (desc.m, desc.n, desc.dtype, at, end)
+    if w.fits == fits:
+        return
+    if w.w != at or (w.scales or at) != end:
+        for t, field in zip(w.keep, ("w", "scales")):
             if t.get_device() != w.device:
                 raise ValueError("the tensors of a weight must be on one device")
             setattr(w, field, _ptr(t))
-            w.fits = None
-    fits = (desc.m, desc.n, desc.dtype)
-    if w.fits == fits:
-        return
     if w.kind == POETX_WEIGHT_Q4:
         _check_q4(*w.keep, desc.m, desc.n, w.group)
     elif w.kind == POETX_WEIGHT_Q8:
