@@ -321,3 +321,38 @@ def test_step_counter_moved_by_the_launch_just_before(P):
     for a, b in zip(outs[:30], outs[30:]):
         assert torch.equal(a, b)
     assert not torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("T,n,m,b", [(1, 256, 512, 128), (3, 256, 512, 128), (20, 512, 256, 128),
+                                     (64, 512, 512, 256)])
+def test_gradients_of_a_few_tokens_with_dropout(P, T, n, m, b):
+    """Few tokens on a 4-bit weight: other kernels run the forward without dropout than with it, but
+    dx and dG_P depend on dy, G, the weight, U and the mask alone, so they are those of the layer
+    without dropout on dropout(x) bit for bit, dx through the mask.  dG_R = dZ^T W, whose W comes
+    from the two forwards: each stores it rounded to bf16, one (above 4 tokens both) from a V
+    rounded to bf16."""
+    import torch
+    drop = P.Dropout(0.2, 5, site=4, row0=1000)
+    L, x, dy = _layer(P, "q4", T, n, m, b, drop)
+    _, dx, dG = _run(L, x, dy)
+    W = L.Wsave.float()
+    xd = torch.empty_like(x)
+    P.dropout(drop.desc(), x, xd)
+    L.training = False
+    _, dx0, dG0 = _run(L, xd, dy)
+    masked = torch.empty_like(dx0)
+    P.dropout(drop.desc(), dx0, masked)
+    assert _same(dx, masked) and bool((masked == 0).any())
+    assert torch.equal(dG[: L.nP], dG0[: L.nP]) and bool((dG[: L.nP] != 0).any())
+    # dG_R from each stored W: exact products, fp32 sums on the tensor cores (one truncation every 16
+    # products and as many as 64 in the joins)
+    dZ = dy[:, L.perm_R.long()].double().view(T, -1, b)
+    for got, Ws in ((dG, W), (dG0, L.Wsave.float())):
+        Wb = Ws.double().view(T, -1, b)
+        want, mag = (torch.einsum("tji,tjk->jik", u, v) for u, v in ((dZ, Wb),
+                                                                     (dZ.abs(), Wb.abs())))
+        assert bool(((got[L.nP:].double() - want).abs() <= (T / 16 + 64) * 2.0 ** -23 * mag).all())
+    # the two W: up to four bf16 roundings (V and W, twice), 0.0017 of the value each in the root
+    # mean square; 2^-7 is more than twice their sum in squares
+    assert float((W - L.Wsave.float()).norm()) <= 2.0 ** -7 * float(W.norm())
+    assert P.device_status() == P.POETX_OK
