@@ -256,6 +256,10 @@ size_t poetx_linear_bwd_workspace(const poetx_linear_desc* d, int has_save_u, in
  *   save_u device [T, n] or NULL: receives U = X[:, p_P] for the backward.
  *   save_w device [T, m] or NULL: receives W = V W0'^T for the backward (POET-Xfast);
  *          NULL together with NULL in the backward gives the recompute mode (POET-Xmem).
+ *   Precision: d->dtype, chosen by the caller, is that of every [T, .] tensor between the products
+ *   too, V, W and Z here, dZ, dW, dV and dU in the backward.  POETX_F32 keeps all of them in fp32.
+ *   POETX_BF16 sums in fp32 and rounds each product once when it is stored; y is off by three such
+ *   roundings (V, W, its own), dx by as many (dW, dV, its own), 0.0029 in norm where one is 0.0017.
  *   T = 0 is a no-op.  Errors: INVALID_ARG, SHAPE, DTYPE, ALIGN, WORKSPACE, CUDA.
  */
 int poetx_linear_fwd(const poetx_linear_desc* d, const void* x, const void* G_P, const void* G_R,
@@ -432,7 +436,9 @@ int poetx_permute_cols_dropout(const poetx_dropout_desc* drop, const void* in, v
  *                       A few tokens without dropout run as three launches (gather + block
  *                       product, weight product, block product + scatter); up to 4 tokens V
  *                       and W go between them as sums of two bf16 numbers (save_w receives W
- *                       in bf16).
+ *                       in bf16), so that y bears its own rounding alone.
+ * Precision as in poetx_linear_fwd; dropout adds the rounding of dropout(x), and in dx that of the
+ * masked gradient (y and dx of a bf16 step then 0.0033 in norm).
  * Without dropout the first two give the results of poetx_linear_{fwd,bwd}{,_q8} bit for bit.
  * ws: at least poetx_linear_ex_workspace bytes (enough for either direction).  Other arguments
  * and errors as poetx_linear_fwd / poetx_linear_bwd.

@@ -1140,6 +1140,16 @@ bool few_path(const poetx_linear_desc* d, const W0Ref& w0, const DropArgs* drop)
 }
 
 // Forward body shared by poetx_linear_fwd and the recompute path of the backward.
+//
+// The bf16 layer stores V, W and Z (and dW, dV, dU in the backward) in bf16, whatever the form of
+// its weight: they are the next product's tensor-core operands, their type is the one that the
+// caller chose for x and y, and each costs half a bf16 step (y 0.0029 off in norm where one rounding
+// gives 0.0017).  As hi + lo of two bf16 numbers they would take every product twice: on 4096 tokens
+// of a 4-bit 13824 x 5120 weight the two W0' products, 414 and 440 us of a step of 1349, take 830 and
+// 910 with twice the rows.  Up to kHiLoTokens tokens the second halves have idle MMA columns and
+// cost nothing.  Z is y before its columns move, U and dZ are x and dy moved: no rounding of their
+// own.
+//
 // Writes U (which few_path alone may do without: nullptr), V, W; Z and y only when y != nullptr.
 int forward_body(const poetx_linear_desc* d, const void* x, const void* G_P, const void* G_R,
                  const W0Ref& w0, const DropArgs* drop, void* y, void* U, void* V, void* W,

@@ -754,9 +754,12 @@ class PoetxLinear:
     shape, type and device, contiguous).  dropout (a Dropout) acts on the layer's input while
     ``training`` is true; step() moves its counter.
 
+    W0's type is that of every tensor of the layer, those between its products included: a float32
+    layer rounds nothing to fewer bits, a bfloat16 one each product once (sums are fp32).
+
     T is the largest number of tokens (rows) of a call: forward(), backward() and step() also take
-    fewer, a last ragged batch or the few tokens of decoding, with the same weight.  A backward takes
-    as many as the forward before it.
+    fewer, a last ragged batch or the few tokens of decoding, with the same weight.  A backward
+    takes as many as the forward before it.
     """
 
     def __init__(self, W0, theta_P, theta_R, perm_P, perm_R, b: int, k: int, T: int,

@@ -210,3 +210,38 @@ def test_few_tokens_that_save_nothing_write_v_and_w_alone(P, T, n, m):
     halves = 2 if T <= 4 else 1
     assert 0.9 * halves * T * (n + m) <= written <= halves * T * (n + m)
     assert torch.equal(L.U, x[:, L.perm_P.long()])
+
+
+@pytest.mark.parametrize("kind,T,y_roundings,dx_roundings",
+                         [("f32", 70, 0, 0), ("bf16", 300, 3, 3), ("q8", 300, 3, 3),
+                          ("q4", 300, 3, 3), ("q4", 64, 3, 3), ("q4", 16, 3, 3), ("q4", 4, 1, 3),
+                          ("q4", 1, 1, 3)])
+def test_roundings_of_y_and_dx(P, kind, T, y_roundings, dx_roundings):
+    """As many bf16 roundings as the header says.  One is off by up to half of 2^-7 2^e in a value
+    of [2^e, 2^(e+1)), evenly: at most 2^-7 / sqrt(12) of the value in the root mean square.  The
+    rotations keep norms and the random weight does so in the mean, so k of them give sqrt(k) times
+    that; a tenth more for the spread (2^8 values and more), 1e-5 for fp32 sums and second halves."""
+    import torch
+    n, m, b = 512, 768, 128
+    L, x, dy = _layer(P, kind, T, n, m, b)
+    y, dx, _ = _run(L, x, dy)
+    if kind == "q4":
+        W = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+        P.dequantize_q4(L.W0q, L.scales, W, 64)
+    else:
+        W = (L.scales[:, None] * L.W0q.float()).bfloat16() if kind == "q8" else L.W0p
+    W = W.double()
+    GP, GR = (G.double() for G in L.G_ops())
+    pP, pR = L.perm_P.long(), L.perm_R.long()
+
+    def blocks(a, G):
+        return torch.einsum("tji,jki->tjk", a.view(T, -1, b), G).reshape(T, -1)
+
+    want_y = torch.empty(T, m, dtype=torch.float64, device="cuda")
+    want_y[:, pR] = blocks(blocks(x.double()[:, pP], GP) @ W.t(), GR)
+    want_dx = torch.empty(T, n, dtype=torch.float64, device="cuda")
+    want_dx[:, pP] = blocks(blocks(dy.double()[:, pR], GR.transpose(1, 2)) @ W,
+                            GP.transpose(1, 2))
+    for got, want, k in ((y, want_y, y_roundings), (dx, want_dx, dx_roundings)):
+        off = float((got.double() - want).norm() / want.norm())
+        assert off <= 1.1 * (k / 12) ** 0.5 * 2.0 ** -7 + 1e-5, (off, k)
