@@ -835,8 +835,7 @@ class PoetxLinear:
         elif ws.numel() * ws.element_size() < need:
             raise ValueError("shared layer scratch too small")
         self.ws = ws
-        self._need = {}  # scratch bytes by number of tokens (below T)
-        self._more = {}  # the scratch of those that need more than T tokens do
+        self._fewer = {}  # descriptor and scratch by number of tokens (below T)
         self.merge()
 
     # The merged weight has one holder, `weight`; these are its tensors by name.
@@ -905,36 +904,39 @@ class PoetxLinear:
     def cnp_forward(self, stream=None):
         self.cnp.forward(stream)
 
-    def _tokens(self, lead, width, outer):
+    def _tokens(self, lead, width):
         """Descriptor, save buffers and scratch for the tokens of `lead` ([tokens, width]), T or
-        fewer; outer: the call's tensors, as _check_layer takes them (the calls without dropout on
-        a dense or int8 weight check none themselves)."""
+        fewer."""
         T = lead.numel() // width
         if T >= self.T:  # (more: the dense and int8 calls take the first T, the others refuse them)
             return self.desc, self.U, self.Wsave, self.ws
-        desc = LinearDesc.from_buffer_copy(self.desc)
-        desc.T = T
-        _check_layer(desc, self.weight, outer, *self.G_ops())
-        need = self._need.get(T)
-        if need is None:
-            need = self._need[T] = _layer_scratch_bytes(desc, self.save, self.int8,
-                                                        self.int4_group)
-        ws = self.ws
-        if need > ws.nbytes:  # (up to 4 tokens of a layer of 5; other splits of the dG sums)
-            ws = self._more.get(T)
-            if ws is None:
-                ws = self._more[T] = self.ws.new_empty(need)
+        few = self._fewer.get(T)
+        if few is None:
+            desc = LinearDesc.from_buffer_copy(self.desc)
+            desc.T = T
+            need = _layer_scratch_bytes(desc, self.save, self.int8, self.int4_group)
+            # (up to 4 tokens of a layer of 5, or another split of the dG sums, may need more)
+            ws = self.ws if need <= self.ws.nbytes else self.ws.new_empty(need)
+            few = self._fewer[T] = desc, ws
+        desc, ws = few
         if not self.save:
             return desc, None, None, ws
         return desc, self.U[:T], self.Wsave[:T], ws
 
+    def _check_fewer(self, desc, outer):
+        """(The calls without dropout on a dense or int8 weight check no shapes themselves.)"""
+        if desc.T < self.T:
+            _check_layer(desc, self.weight, outer, *self.G_ops())
+
     def forward(self, x, y, stream=None):
         GP, GR = self.G_ops()
         drop = self._drop()
-        desc, U, W, ws = self._tokens(x, self.n, ((x, self.n), (y, self.m)))
+        desc, U, W, ws = self._tokens(x, self.n)
         if self.int4_group or drop is not None:
             linear_fwd_ex(desc, self.weight, drop, x, GP, GR, y, U, W, ws, stream)
-        elif self.int8:
+            return
+        self._check_fewer(desc, ((x, self.n), (y, self.m)))
+        if self.int8:
             linear_fwd_q8(desc, x, GP, GR, self.W0q, self.scales, y, U, W, ws, stream)
         else:
             linear_fwd(desc, x, GP, GR, self.W0p, y, U, W, ws, stream)
@@ -943,11 +945,13 @@ class PoetxLinear:
         GP, GR = self.G_ops()
         drop = self._drop()
         dGP, dGR = self.dG[: self.nP], self.dG[self.nP:]
-        desc, U, W, ws = self._tokens(dy, self.m, ((x, self.n), (dy, self.m), (dx, self.n)))
+        desc, U, W, ws = self._tokens(dy, self.m)
         if self.int4_group or drop is not None:
             linear_bwd_ex(desc, self.weight, drop, x, dy, GP, GR, U, W, dx, dGP, dGR, accumulate,
                           ws, stream)
-        elif self.int8:
+            return
+        self._check_fewer(desc, ((x, self.n), (dy, self.m), (dx, self.n)))
+        if self.int8:
             linear_bwd_q8(desc, x, dy, GP, GR, self.W0q, self.scales, U, W, dx, dGP, dGR,
                           accumulate, ws, stream)
         else:
