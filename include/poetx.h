@@ -345,7 +345,7 @@ int poetx_linear_bwd_q8(const poetx_linear_desc* d, const void* x, const void* d
  * low-bit base weight, dequantised on the fly where it is needed).  The pages give no scheme;
  * here one bf16 scale per group of `group` (32, 64 or 128) consecutive columns of a row of W0':
  *   a = max |w| of the group;  s = a / 7 (fp32, IEEE division) rounded to 5 significant bits,
- *   nearest even;  q = the integer nearest to w / s (ties to even; decided exactly), clamped to
+ *   nearest even (below 2^-126, where fp32 has fewer: to a multiple of 2^-130);  q = the integer nearest to w / s (ties to even; decided exactly), clamped to
  *   [-7, 7].  An all-zero group: scale 0, codes 0.  A group holding an infinity or a NaN: scale
  *   NaN, codes 0, so it reads back as NaN.
  * With 5 bits in the scale, s q is exactly a bf16 number: nothing in the library rounds the

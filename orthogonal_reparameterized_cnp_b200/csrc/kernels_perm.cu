@@ -356,9 +356,10 @@ cudaError_t il8_launch(const void* in, void* out, const int32_t* row_idx, const 
 // accesses leave room for the generator's instructions.  Each thread's two generator calls (one a
 // row) run side by side.  Measured (source / output mask): 40 / 39 us at 8192 x
 // 5120 bf16 (floor 25.6 at the HBM copy rate; the map alone 34.6, dropout and map one after the
-// other 67), 54 / 53 us at 4096 x 13824.  With the masks in the row-batched pipeline: 54 / 47 and
-// 76 / 67.  Bound: the generator and selection (about 11 instructions a value) on top of the
-// gather's shared-memory accesses.
+// other 67), 54 / 53 us at 4096 x 13824; fp32 4096 x 5120 33.4 / 33.1 (floor 25.6).  With the masks
+// in the row-batched pipeline: 54 / 47 and 76 / 67.  Bound: no unit is full (issue 54%, integer pipe
+// 51%, warps 38%); a CTA fetches, masks and gathers a pair in turn, with two barriers a pair, and
+// the generator and selection (about 11 instructions a value) are part of that way.
 constexpr int kPairThreads = 512;
 constexpr size_t kPairSmem = 224 * 1024;
 

@@ -44,7 +44,9 @@
 // no loading warp).  Converting costs about 1.9 instructions a code (q4_unpack and half a
 // multiplication in packed bf16, exact for the quantiser's scales) against 2.8 for int8.
 // Measured at 13824 x 5120, forward / transposed, 4096 tokens: 414 / 440 us (1.40 / 1.32
-// PFLOP/s), 8192 tokens 830 / 910.  Stages of one chunk, with the codes through slots of shared
+// PFLOP/s), 8192 tokens 830 / 910, in a replayed graph of some ms; at the clocks of a longer run
+// 8192 forward tokens take 930 to 960, and the two products of 4096 tokens in a step 850 to 910
+// together.  Stages of one chunk, with the codes through slots of shared
 // memory: 473 / 525 and 955 / 1030 (one chunk in registers: 562 / 524; groups of two warps: 435 /
 // 481; eight epilogue warps and other rasters: the same).
 //
@@ -327,7 +329,6 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
                : "memory");
 }
 
-// untiled bulk copy of contiguous bytes into this CTA's shared memory
 template <bool B_MN>
 __device__ __forceinline__ uint32_t make_idesc_pair() {
   return (1u << 4)                              // D format: f32

@@ -19,8 +19,8 @@
 // A stage holds two chunks, so that the MMA thread's wait and commit (about 0.2 us of the 0.34 us a
 // chunk took with a commit each, conversion aside) come once for both.
 // Bound by the latency of a chunk's way (below), not by a pipe: at 5120 x 5120, group 128, 16
-// tokens (transposed) take 13.7 us, 64 15.2, 128 20.2, 256 24.8; at 13824 x 5120 64 take 28.9, 128
-// 38.5, 256 43.4; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of
+// tokens (transposed) take 13.8 us, 64 15.4, 128 20.1, 256 24.2; at 13824 x 5120 64 take 29.1, 128
+// 39.1, 256 42.9; 53 tokens of 4999 x 4096 transposed take 28 (35 with two warps of loaders), of
 // 5000 x 4096 15.
 // Every wait is bounded (Params::wait_ns); a role whose wait runs out records the timeout, leaves
 // its loop, waits for its own copies and meets the others.

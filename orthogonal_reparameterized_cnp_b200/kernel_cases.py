@@ -11,7 +11,8 @@ Cases (all on cuda:0, seeded random inputs, a few GB of device memory at most):
     layer32            the small fp32 linear: n = m = 256, b = 32, k = 4, T = 512, 5 steps
     cnp nblk b k       CnpBuffers: forward + backward 4 times, the last timed
     q8merge m n        merge_perm_q8 of an m x n bf16 weight, 4 times
-    q4merge m n group  merge_perm_q4 and dequantize_q4 of an m x n bf16 weight, 4 times
+    q4merge m n group [f32]  merge_perm_q4 and dequantize_q4 of an m x n weight (bf16, or fp32 when
+                       f32 is 1), 4 times
     q4 T m n group     matmul_q4 with an m x n 4-bit weight, forward and transposed in turn, 4 times
     q4layer T n m      one PoetxLinear (b = 256, k = 4) on a 4-bit weight (group 128) with dropout
                        0.1: forward + backward 3 times, then 3 forwards without dropout
@@ -139,9 +140,10 @@ def _q4_weight(m, n, group):
     return W, q, s
 
 
-def q4merge(m, n, group):
+def q4merge(m, n, group, f32=0):
     """Per round: k_merge_q4_pairs (k_merge_q4 where a row does not fit), k_dequant_q4."""
     W, q, s = _q4_weight(m, n, group)
+    W = W.float() if f32 else W
     pP, pR = (torch.from_numpy(P.make_perm(i, c)[0]).to(_dev()) for i, c in ((1, n), (2, m)))
     for _ in range(4):
         P.merge_perm_q4(W, q, s, pR, pP, group)
@@ -165,7 +167,9 @@ def q4(T, m, n, group):
 
 
 def q4layer(T, n, m):
-    """Up to 8 tokens the last three forwards are k_bd_rows, k_q4_rows, k_bd_rows each."""
+    """Up to 16 tokens, and up to 64 where T (n + m) 256 is at most 2^26, the last three forwards are
+    three launches each: k_bd_rows, the product (k_q4_rows up to 16 tokens, then k_umma_q4),
+    k_bd_rows."""
     dev = _dev()
     W0 = (torch.randn(m, n, device=dev) / n ** 0.5).to(torch.bfloat16)
     th = [torch.randn(c // 256, 256 * 255 // 2, device=dev) * 0.01 for c in (n, m)]

@@ -22,3 +22,9 @@ def test_kernel_case_runs(argv, capsys):
 def test_kernel_cases_usage():
     from orthogonal_reparameterized_cnp_b200 import kernel_cases
     assert kernel_cases.main([]) == 2
+
+
+def test_fp32_case_of_the_4_bit_merge(capsys):
+    from orthogonal_reparameterized_cnp_b200 import kernel_cases
+    assert kernel_cases.main(["q4merge", "300", "512", "64", "1"]) == 0
+    assert "q4merge ok" in capsys.readouterr().out
