@@ -746,7 +746,8 @@ class PoetxLinear:
     ``cnp`` (a CnpBuffers of this layer alone unless one is shared, see PoetxLinearGroup);
     ``theta``, ``G``, ``dG``, ``dtheta`` are this layer's rows of it.  The inverse index
     maps come from the library, which rejects a perm_P or perm_R that is not a bijection.
-    The permutations are merged into W0' once, at construction (and again by merge()).
+    The permutations are merged into W0' once, at construction (and again by merge(), which W0
+    is kept for: a layer that is done merging gives it up with ``layer.W0 = None``).
 
     The merged weight is kept in W0's type, in int8 (int8_weight) or in 4 bits with a scale per
     int4_group (32, 64 or 128) columns: ``W0p``, or ``W0q`` and ``scales``, which are the tensors of
@@ -844,6 +845,8 @@ class PoetxLinear:
 
     def _replace_weight(self, i: int, coded: bool, t):
         kind = self.weight.kind
+        if t is None and self._weight_tensor(i, coded) is None:
+            return
         if t is None or (kind != POETX_WEIGHT_DENSE) != coded:
             raise ValueError("the merged weight is W0p (a layer in W0's type), or W0q and scales "
                              "(int8, 4 bits)")
@@ -893,6 +896,8 @@ class PoetxLinear:
 
     def merge(self, stream=None):
         """W0' = Pi_R W0 Pi_P^T (or its int8 or 4-bit codes): once per set of permutations."""
+        if self.W0 is None:
+            raise ValueError("the layer has given up W0")
         if self.int4_group:
             merge_perm_q4(self.W0, self.W0q, self.scales, self.perm_R, self.perm_P,
                           self.int4_group, stream)

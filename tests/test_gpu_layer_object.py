@@ -245,3 +245,22 @@ def test_roundings_of_y_and_dx(P, kind, T, y_roundings, dx_roundings):
     for got, want, k in ((y, want_y, y_roundings), (dx, want_dx, dx_roundings)):
         off = float((got.double() - want).norm() / want.norm())
         assert off <= 1.1 * (k / 12) ** 0.5 * 2.0 ** -7 + 1e-5, (off, k)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_layer_that_gave_up_w0(P, kind):
+    """It trains as before, without holding the unquantised weight, and cannot merge again."""
+    import gc
+    import weakref
+    L, x, dy = _layer(P, kind, 20, 256, 384)
+    want = _run(L, x, dy)
+    held = weakref.ref(L.W0)
+    L.W0 = None
+    gc.collect()
+    assert held() is None
+    assert _equal(_run(L, x, dy), want)
+    with pytest.raises(ValueError):
+        L.merge()
+    assert _equal(_run(L, x, dy), want)
+    for name in (("W0p",) if kind in ("q8", "q4") else ("W0q", "scales")):
+        setattr(L, name, None)  # what the form does not have
